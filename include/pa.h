@@ -47,6 +47,11 @@ extern "C" {
 #define PA_BF16 1
 /* E4M3 KV-cache codes (pools only; see pa_cache_write_fp8 / pa_decode_fp8) */
 #define PA_FP8_E4M3 2
+/* 4-bit KV cache: E2M1 codes with an E4M3 scale per 16 head_dim values (pools
+ * only; layout at pa_cache_write_fp4) */
+#define PA_FP4_E2M1 3
+/* bytes of one token's K or V row of one head in a 4-bit pool */
+#define PA_FP4_ROW_BYTES(head_dim) ((head_dim) / 2 + (head_dim) / 16)
 
 /* status codes returned by the entry points */
 #define PA_OK 0
@@ -144,7 +149,8 @@ int pa_cache_write_mapped(const void* k, const void* v, const int32_t* block_tab
  * of V from src to dst.  Pairs are independent: dst blocks must be distinct and
  * no dst may also be a src.  A pair out of range, or one that breaks this rule,
  * sets PA_DEVERR_COPY_PAIR and is not copied.  dtype PA_FP8_E4M3 copies pools
- * of 1-byte codes.
+ * of 1-byte codes, PA_FP4_E2M1 the blocks of 4-bit pools (block_size >= 4),
+ * codes and scales together.
  */
 int pa_copy_blocks(const int32_t* src_dst_pairs, int32_t num_pairs, void* k_cache, void* v_cache,
                    int64_t num_blocks, int32_t block_size, int32_t num_kv_heads,
@@ -166,7 +172,8 @@ int pa_copy_blocks(const int32_t* src_dst_pairs, int32_t num_pairs, void* k_cach
  *                 node over NVLink-C2C), any host memory; memory that
  *                 cudaHostGetDevicePointer cannot translate returns
  *                 PA_ERR_INVALID_ARG
- *   dtype         PA_F16, PA_BF16 or PA_FP8_E4M3 (1-byte codes)
+ *   dtype         PA_F16, PA_BF16, PA_FP8_E4M3 (1-byte codes) or PA_FP4_E2M1
+ *                 (4-bit pools, block_size >= 4)
  * One kernel launch copies every pair (K and V), bit-exact, reading or
  * writing the host pool through its mapped device address.  A pair out of
  * range, or a dst that appears twice, sets PA_DEVERR_COPY_PAIR and is not
@@ -224,7 +231,8 @@ int pa_cache_write_fp8_mapped(const void* k, const void* v, int32_t src_dtype,
  * largest call serves calls of any shape and num_ctas.  num_ctas = 0 selects
  * the default grid (a multiple of the SM count); larger than
  * PA_DECODE_MAX_CTAS returns PA_ERR_INVALID_ARG; flags as for pa_decode.
- * dtype PA_FP8_E4M3 sizes the workspace of pa_decode_fp8.
+ * dtype PA_FP8_E4M3 sizes the workspace of pa_decode_fp8, PA_FP4_E2M1 that of
+ * pa_decode_fp4.
  */
 #define PA_DECODE_MAX_CTAS 16384
 int pa_decode_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
@@ -386,6 +394,145 @@ int pa_decode_noalloc(const void* q, const void* k_cache, const void* v_cache,
                       int32_t head_dim, int32_t block_size, int64_t num_blocks, int32_t dtype,
                       float scale, void* out, int32_t flags, int32_t num_ctas,
                       int32_t* err_word, pa_stream stream);
+
+/*
+ * pa_append_rope -- a step's queries, keys and values enter the attention: an
+ * optional RMS norm of every query and key head, the position rotation, the
+ * rotated queries written out, and keys and values stored at their slots, in
+ * one launch.  [P1] "How is vLLM's KV cache paged?", bullet "Writing" (when a
+ * token's K and V are computed a small kernel stores them at its slot); the
+ * norm and the rotation are what a model computes on them just before.
+ *   q, k, v       [num_tokens][heads][head_dim] of src_dtype (PA_F16 or
+ *                 PA_BF16), consecutive tokens q_stride / k_stride / v_stride
+ *                 elements apart (multiples of 8, at least one token's rows):
+ *                 views of a fused projection's output, for instance
+ *   cos_sin       float [max_pos][rotary_dim]: the row of a position holds
+ *                 rotary_dim / 2 cosines, then as many sines
+ *   rotary_dim    a multiple of 16, at most head_dim; elements from it on pass
+ *                 unrotated; 0: no rotation (cos_sin may be NULL)
+ *   interleaved   0: element i < rotary_dim / 2 is rotated with element
+ *                 i + rotary_dim / 2; otherwise elements 2 i and 2 i + 1
+ *   q_norm, k_norm  [head_dim] weights of src_dtype, or NULL: no norm there
+ *   eps           finite, >= 0 (read when a norm is given)
+ *   token_seq, token_pos  int32 [num_tokens], as for pa_slot_mapping; the
+ *                 position also selects the row of cos_sin.  token_seq -1
+ *                 marks a padding token
+ *   q_out         [num_tokens][num_q_heads][head_dim] contiguous; may be q
+ *                 itself when q is contiguous, and overlaps no other argument.
+ *                 num_q_heads 0: q, q_out unused
+ *   cache_dtype   src_dtype (pools of pa_cache_write), PA_FP8_E4M3 (pools of
+ *                 pa_cache_write_fp8) or PA_FP4_E2M1 (pools of
+ *                 pa_cache_write_fp4); k_scale, v_scale of the last two
+ *   slot_mapping  int64 [num_tokens], receives the slots when not NULL
+ * With x a head's 16-bit row, r = 1 / sqrt(mean(x^2) + eps), y = x r w (y = x
+ * without a norm) and pairs (a, b) of y: a' = a cos - b sin, b' = b cos +
+ * a sin, in fp32 with one rounding to 16 bits at the end; what a quantized
+ * pool stores is quantized from that 16-bit value, so the pools end as after a
+ * 16-bit rotation followed by the pool's own write.
+ * A padding token gets slot -1 and writes nothing, neither pools nor q_out.  A
+ * sequence or position outside its table, or a position not below max_pos,
+ * does the same and sets PA_DEVERR_POSITION; a bad table entry sets
+ * PA_DEVERR_BLOCK_ID.  Two tokens with the same slot: a row may hold bytes of
+ * both.
+ */
+int pa_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                   int64_t v_stride, int32_t src_dtype, const float* cos_sin, int32_t rotary_dim,
+                   int32_t max_pos, int32_t interleaved, const void* q_norm, const void* k_norm,
+                   float eps, const int32_t* block_tables, int32_t table_stride, int32_t num_seqs,
+                   const int32_t* token_seq, const int32_t* token_pos, int64_t num_tokens,
+                   void* q_out, void* k_cache, void* v_cache, int64_t num_blocks,
+                   int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                   int32_t head_dim, int32_t cache_dtype, float k_scale, float v_scale,
+                   int64_t* slot_mapping, int32_t* err_word, pa_stream stream);
+
+/*
+ * pa_cache_write_fp4 -- pa_cache_write into a 4-bit KV cache: a quarter of the
+ * 16-bit pool's bytes in codes plus a scale byte for every 16 of them (0.5625
+ * bytes an element).  The pages stop at kv_cache_dtype="fp8" ([P1] "How can one
+ * customize the tokenizer, cache strategy, or scheduler strategy?"); the
+ * format is E2M1 (0, .5, 1, 1.5, 2, 3, 4, 6 and their negatives) in groups of
+ * 16 consecutive head_dim values x of one token and head:
+ *   s16  = e4m3(max|x| / (6 * scale)), to nearest even, at most 448
+ *   code = e2m1(x / (s16 * scale)), to nearest even, at most 6; 0 where
+ *          s16 is 0
+ *   value = code * s16 * scale
+ * with binary32 products and IEEE divisions: the codes are bit-exact.  A scale
+ * of max|tensor| / 2688 uses the whole range; groups whose max|x| is at most
+ * scale * 6 * 2^-10 become zero.
+ *   k, v          [num_tokens][num_kv_heads][head_dim], contiguous, src_dtype
+ *                 (PA_F16 or PA_BF16), finite
+ *   k_cache, v_cache  uint8 [num_blocks][num_kv_heads][P] with P = block_size *
+ *                 PA_FP4_ROW_BYTES(head_dim): the plane of a block's head holds
+ *                 its codes [block_size][head_dim / 2] (element 2 i in the low
+ *                 nibble of byte i), then its scales
+ *                 [block_size / 4][head_dim / 16][4], the last index being the
+ *                 token's slot in the block modulo 4
+ *   block_size    a power of two in [4, 256]
+ *   k_scale, v_scale  finite and > 0, 6 * scale finite
+ * Slots as for pa_cache_write, but two tokens with the same slot may leave
+ * bytes of both in it.
+ */
+int pa_cache_write_fp4(const void* k, const void* v, int32_t src_dtype,
+                       const int64_t* slot_mapping, int64_t num_tokens, void* k_cache,
+                       void* v_cache, int64_t num_blocks, int32_t block_size,
+                       int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale,
+                       int32_t* err_word, pa_stream stream);
+
+/*
+ * pa_cache_write_fp4_mapped -- the slots of pa_append_rope and
+ * pa_cache_write_fp4 in one launch, for keys that are rotated already ([P1]
+ * "How is vLLM's KV cache paged?", bullet "Writing").  Tokens, errors and
+ * slot_mapping as for pa_append_rope.
+ */
+int pa_cache_write_fp4_mapped(const void* k, const void* v, int32_t src_dtype,
+                              const int32_t* block_tables, int32_t table_stride, int32_t num_seqs,
+                              const int32_t* token_seq, const int32_t* token_pos,
+                              int64_t num_tokens, void* k_cache, void* v_cache, int64_t num_blocks,
+                              int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                              float k_scale, float v_scale, int64_t* slot_mapping,
+                              int32_t* err_word, pa_stream stream);
+
+/*
+ * pa_cache_read_fp4 -- the rows at given slots of a 4-bit cache as 16-bit
+ * values, the inverse of pa_cache_write_fp4: code * s16 * scale, rounded to
+ * out_dtype.  Rows read into a 16-bit pool's blocks serve pa_prefill, which
+ * reads 16-bit pools ([P1] "How does it support prompts of arbitrary length?").
+ *   slot_mapping  int64 [num_tokens]; slot < 0: the output row is left as it
+ *                 is; slot >= num_blocks * block_size: the same, and
+ *                 PA_DEVERR_SLOT
+ *   k_out, v_out  [num_tokens][num_kv_heads][head_dim] of out_dtype
+ */
+int pa_cache_read_fp4(const int64_t* slot_mapping, int64_t num_tokens, const void* k_cache,
+                      const void* v_cache, int64_t num_blocks, int32_t block_size,
+                      int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale,
+                      void* k_out, void* v_out, int32_t out_dtype, int32_t* err_word,
+                      pa_stream stream);
+
+/*
+ * pa_decode_fp4 -- pa_decode over 4-bit pools written by pa_append_rope or
+ * pa_cache_write_fp4, with sliding-window attention as in pa_decode_window.
+ *   q, out        [num_seqs][num_q_heads][head_dim] in q_dtype (PA_F16 or PA_BF16)
+ *   k_cache, v_cache  4-bit pools, block_size a power of two in [4, 256]
+ *   window        >= 1: attend to the last `window` tokens; 0: to all
+ *   workspace     as for pa_decode, sized by pa_decode_workspace_size with
+ *                 dtype PA_FP4_E2M1
+ *   flags         PA_DECODE_AUTO or PA_DECODE_MMA, optionally OR-ed with
+ *                 PA_DECODE_TABLES_READY
+ * The tensor scales are applied outside the products (k_scale joins `scale`,
+ * v_scale multiplies the output); code * s16 and the queries (a bfloat16 row
+ * after a power-of-two scaling) are binary16, every sum is fp32.  For binary16
+ * outputs the softmax weights are a pair of binary16 values, for bfloat16
+ * outputs one.  Tokens of a block whose table entry is out of range
+ * (PA_DEVERR_BLOCK_ID) are left out of the softmax.  Every other argument,
+ * the errors and the workspace rules are those of pa_decode.
+ */
+int pa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
+                  const int32_t* block_tables, int32_t table_stride, const int32_t* seq_lens,
+                  int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                  int32_t block_size, int64_t num_blocks, int32_t q_dtype, float scale,
+                  float k_scale, float v_scale, int32_t window, void* out, void* workspace,
+                  size_t workspace_bytes, int32_t flags, int32_t num_ctas, int32_t* err_word,
+                  pa_stream stream);
 
 /*
  * pa_gather_kv -- (test support) gather every sequence's K and V rows into

@@ -496,3 +496,126 @@ def sliding_window_max_blocks(W, B):
     """[P1 "How does it support prompts of arbitrary length? ..."]  a window of
     W tokens touches at most ceil(W / B) + 1 blocks."""
     return blocks_for(W, B) + 1
+
+
+# --------------------------------------------------------------------------
+# 4-bit KV cache: E2M1 codes in groups of 16 head_dim values, one E4M3 scale a
+# group and one scale per tensor.  value = e2m1(code) * e4m3(s16) * scale;
+# s16 = e4m3(max|x| / (6 scale)), code = e2m1(x / (s16 scale)), products and
+# divisions in binary32, roundings to nearest even.
+# --------------------------------------------------------------------------
+
+_E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def e2m1_encode(x):
+    """Values -> E2M1 codes 0..15: the nearest magnitude, a tie to the even
+    code, magnitudes beyond 6 to 6."""
+    x = np.asarray(x, np.float64)
+    dist = np.abs(np.abs(x)[..., None] - _E2M1)
+    near = dist == dist.min(-1, keepdims=True)   # one code, or the two of a tie
+    even = near & (np.arange(8) % 2 == 0)
+    mag = np.where(even.any(-1), even.argmax(-1), near.argmax(-1)).astype(np.uint8)
+    return mag | (np.signbit(x).astype(np.uint8) << 3)
+
+
+def e2m1_decode(codes):
+    c = np.asarray(codes, np.uint8)
+    return np.where(c & 8, -1.0, 1.0) * _E2M1[c & 7]
+
+
+def fp4_quantize(x, scale):
+    """x float32 [..., D] -> (codes uint8 [..., D], scale codes uint8 [..., D/16])."""
+    x = np.ascontiguousarray(x, np.float32)
+    g = x.reshape(x.shape[:-1] + (x.shape[-1] // 16, 16))
+    s = np.float32(scale)
+    s16 = e4m3_encode(np.abs(g).max(-1) / (np.float32(6) * s))
+    d = e4m3_decode(s16).astype(np.float32) * s
+    with np.errstate(divide="ignore", invalid="ignore"):
+        y = np.where(d[..., None] > 0, g / d[..., None], np.float32(0))
+    return e2m1_encode(y).reshape(x.shape), s16
+
+
+def fp4_put(pool, block, row, head, codes, s16):
+    """Write one token's row into the plane of (block, head) of a 4-bit pool
+    uint8 [num_blocks, H, B, 9 D / 16]."""
+    B, D = pool.shape[2], codes.size
+    plane = pool[block, head].reshape(-1)
+    plane[row * D // 2:(row + 1) * D // 2] = codes[0::2] | (codes[1::2] << 4)
+    for g in range(D // 16):
+        plane[B * D // 2 + ((row // 4) * (D // 16) + g) * 4 + row % 4] = s16[g]
+
+
+def cache_write_fp4(k_cache, v_cache, k, v, slots, k_scale, v_scale):
+    """In place: rows of 4-bit pools at `slots` <- k, v float32 [n, H, D]; slot < 0 skipped."""
+    B = k_cache.shape[2]
+    for pool, x, scale in ((k_cache, k, k_scale), (v_cache, v, v_scale)):
+        codes, s16 = fp4_quantize(x, scale)
+        for n, s in enumerate(slots):
+            if s >= 0:
+                for h in range(pool.shape[1]):
+                    fp4_put(pool, int(s) // B, int(s) % B, h, codes[n, h], s16[n, h])
+
+
+def fp4_dequant(pool, D):
+    """code * s16 of every row: float64 [num_blocks, B, H, D]."""
+    nb, H, B, _ = pool.shape
+    planes = pool.reshape(nb, H, -1)
+    packed = planes[..., :B * D // 2].reshape(nb, H, B, D // 2)
+    codes = np.stack((packed & 15, packed >> 4), -1).reshape(nb, H, B, D)
+    s16 = planes[..., B * D // 2:].reshape(nb, H, B // 4, D // 16, 4)
+    s16 = s16.transpose(0, 1, 2, 4, 3).reshape(nb, H, B, D // 16)
+    v = e2m1_decode(codes) * np.repeat(e4m3_decode(s16), 16, axis=-1)
+    return v.transpose(0, 2, 1, 3)
+
+
+def paged_decode_fp4(q, k_cache, v_cache, k_scale, v_scale, block_tables, seq_lens, scale,
+                     window=0):
+    """fp64 (out, spread) [N, Hq, D] over 4-bit pools; q fp64 [N, Hq, D].
+    spread = sum_t w_t |V_t - out|, as in paged_decode."""
+    N, Hq, D = q.shape
+    B, H = k_cache.shape[2], k_cache.shape[1]
+    G = Hq // H
+    out, sp = np.zeros((N, Hq, D)), np.zeros((N, Hq, D))
+    for i in range(N):
+        T = int(seq_lens[i])
+        first = max(0, T - window) if window > 0 else 0
+        if T == 0:
+            continue
+        blocks = np.asarray(block_tables[i, first // B:-(-T // B)], np.int64)
+        off = first - first // B * B
+        K = fp4_dequant(k_cache[blocks], D).reshape(-1, H, D)[off:off + T - first]
+        V = fp4_dequant(v_cache[blocks], D).reshape(-1, H, D)[off:off + T - first]
+        K = K * float(np.float32(k_scale))
+        V = V * float(np.float32(v_scale))
+        for hq in range(Hq):
+            s = K[:, hq // G] @ q[i, hq] * scale
+            w = np.exp(s - s.max())
+            w /= w.sum()
+            out[i, hq] = w @ V[:, hq // G]
+            sp[i, hq] = w @ np.abs(V[:, hq // G] - out[i, hq])
+    return out, sp
+
+
+# --------------------------------------------------------------------------
+# Head norms and the position rotation
+# --------------------------------------------------------------------------
+
+def head_norm(x, weight, eps):
+    """x fp64 [..., D]: x / sqrt(mean(x^2) + eps) * weight."""
+    return x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * weight
+
+
+def rotate(x, cos_sin_rows, interleaved):
+    """x [n, heads, D], cos_sin_rows [n, rot] (rot / 2 cosines, then sines)
+    of the same float type; the products and the sum rounded one by one."""
+    rot = cos_sin_rows.shape[1]
+    c = cos_sin_rows[:, None, :rot // 2]
+    s = cos_sin_rows[:, None, rot // 2:]
+    out = x.copy()
+    ia = np.arange(0, rot, 2) if interleaved else np.arange(rot // 2)
+    ib = ia + 1 if interleaved else ia + rot // 2
+    a, b = x[..., ia], x[..., ib]
+    out[..., ia] = a * c - b * s
+    out[..., ib] = b * c + a * s
+    return out

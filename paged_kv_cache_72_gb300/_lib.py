@@ -11,6 +11,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libpa.so")
 PA_F16 = 0
 PA_BF16 = 1
 PA_FP8_E4M3 = 2
+PA_FP4_E2M1 = 3
 PA_OK = 0
 PA_ERR_INVALID_ARG = 1
 PA_ERR_UNSUPPORTED = 2
@@ -72,6 +73,21 @@ SIGNATURES = {
     "pa_decode_noalloc": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
                                          _i32, _i64, _i32, ctypes.c_float, _vp, _i32, _i32, _vp,
                                          _vp]),
+    "pa_append_rope": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i32, _i32, _i32,
+                                      _vp, _vp, ctypes.c_float, _vp, _i32, _i32, _vp, _vp, _i64,
+                                      _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32,
+                                      ctypes.c_float, ctypes.c_float, _vp, _vp, _vp]),
+    "pa_cache_write_fp4": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i64, _vp, _vp, _i64, _i32, _i32,
+                                          _i32, ctypes.c_float, ctypes.c_float, _vp, _vp]),
+    "pa_cache_write_fp4_mapped": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _i64,
+                                                 _vp, _vp, _i64, _i32, _i32, _i32, ctypes.c_float,
+                                                 ctypes.c_float, _vp, _vp, _vp]),
+    "pa_cache_read_fp4": (ctypes.c_int, [_vp, _i64, _vp, _vp, _i64, _i32, _i32, _i32,
+                                         ctypes.c_float, ctypes.c_float, _vp, _vp, _i32, _vp,
+                                         _vp]),
+    "pa_decode_fp4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
+                                     _i64, _i32, ctypes.c_float, ctypes.c_float, ctypes.c_float,
+                                     _i32, _vp, _vp, _sz, _i32, _i32, _vp, _vp]),
     "pa_gather_kv": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i64,
                                     _i32, _i32, _vp, _vp, _vp, _vp]),
     "pa_get_error": (ctypes.c_int, [_vp, _vp, ctypes.POINTER(_i32)]),

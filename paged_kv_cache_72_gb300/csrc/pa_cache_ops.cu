@@ -393,10 +393,20 @@ static int pairs_per_cta(int n, int sm_count) {
 }
 
 static bool shape_ok(int32_t block_size, int32_t num_kv_heads, int32_t head_dim, int32_t dtype,
-                     bool allow_fp8 = false) {
+                     bool quantized = false) {
   return (head_dim == 64 || head_dim == 128) && num_kv_heads > 0 && is_pow2(block_size) &&
          block_size <= 256 &&
-         (dtype == PA_F16 || dtype == PA_BF16 || (allow_fp8 && dtype == PA_FP8_E4M3));
+         (dtype == PA_F16 || dtype == PA_BF16 || (quantized && dtype == PA_FP8_E4M3) ||
+          (quantized && dtype == PA_FP4_E2M1 && block_size >= 4));
+}
+
+// 16-byte vectors of one block of a pool: whole ones (a 4-bit block of at
+// least 4 tokens is a multiple of 144 bytes a head)
+static long long block_vecs(int32_t block_size, int32_t num_kv_heads, int32_t head_dim,
+                            int32_t dtype) {
+  const int row = dtype == PA_FP4_E2M1 ? PA_FP4_ROW_BYTES(head_dim)
+                                       : head_dim * (dtype == PA_FP8_E4M3 ? 1 : 2);
+  return (long long)block_size * num_kv_heads * row / 16;
 }
 
 }  // namespace pa
@@ -488,8 +498,7 @@ int pa_copy_blocks(const int32_t* src_dst_pairs, int32_t num_pairs, void* k_cach
   if (num_pairs > 65535) return PA_ERR_INVALID_ARG;
   if (!src_dst_pairs || !k_cache || !v_cache) return PA_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID_ARG;
-  const int eb = dtype == PA_FP8_E4M3 ? 1 : 2;
-  const long long vecs = (long long)block_size * num_kv_heads * head_dim * eb / 16;
+  const long long vecs = block_vecs(block_size, num_kv_heads, head_dim, dtype);
   if (vecs > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
   DeviceInfo di;
   if (int rc = current_device_info(&di)) return rc;
@@ -525,8 +534,7 @@ int pa_swap_blocks(const int32_t* src_dst_pairs, int32_t num_pairs, int32_t dire
     cudaGetLastError();   // not addressable from the GPU: the caller's error, not a sticky one
     return PA_ERR_INVALID_ARG;
   }
-  const int eb = dtype == PA_FP8_E4M3 ? 1 : 2;
-  const long long vecs = (long long)block_size * num_kv_heads * head_dim * eb / 16;
+  const long long vecs = block_vecs(block_size, num_kv_heads, head_dim, dtype);
   if (vecs > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
   const bool out = direction == PA_SWAP_OUT;
   DeviceInfo di;

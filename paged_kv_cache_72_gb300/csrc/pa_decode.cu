@@ -441,6 +441,9 @@ int pa_decode_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t 
                              size_t* bytes) {
   if (!bytes) return PA_ERR_INVALID_ARG;
   flags &= ~PA_DECODE_TABLES_READY;   // the workspace does not depend on it
+  if (dtype == PA_FP4_E2M1)
+    return decode_fp4_workspace(num_q_heads, num_kv_heads, head_dim, block_size, flags, num_ctas,
+                                bytes);
   // an E4M3 cache: the workspace does not depend on the query dtype
   const int q_dtype = dtype == PA_FP8_E4M3 ? PA_BF16 : dtype;
   DecodePlan p;

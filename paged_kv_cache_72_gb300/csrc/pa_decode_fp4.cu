@@ -1,0 +1,844 @@
+// Paged single-query decode attention over a 4-bit (E2M1) KV cache.
+//
+// What it computes, with K and V the values the pool's codes stand for:
+//   s_t = scale * k_scale * sum_d q_d codeK_td s16K_t(d/16)
+//   o   = v_scale * sum_t softmax(s)_t codeV_t s16V_t(d/16),
+// t over [max(0, T - window), T).  The tensor scales stay outside the products;
+// code * s16 has at most 6 significant bits and lies in [2^-10, 2688], so it is
+// exact in binary16, and every product is an f16 x f16 MMA with fp32 sums.
+//
+// Bound: bytes first (0.5625 bytes an element and nothing read twice), then the
+// conversions: one cvt, one multiply by the scale and (for V) half a byte merge
+// a pair of elements.  So the kernel keeps both small:
+//  * One warp is one pipeline.  A warp owns a (sequence, KV head) context or a
+//    contiguous range of one and reads its planes straight from global memory
+//    into MMA fragments: the layout of a plane lets every lane load its own
+//    fragment bytes as whole vectors, so there is no shared-memory staging, no
+//    producer and no barrier between warps until a block's end.
+//  * The next tile's K is loaded as soon as this tile's K is in the tensor
+//    cores, and the next V after this V: one set of registers each, with the
+//    other half of the tile's work to cover the latency.
+//  * Transposed products: S^T = K Q^T (16 tokens x 8 heads), O^T += V^T P^T
+//    (16 head_dim rows x 8 heads); groups of more than 8 query heads take two
+//    8-head tiles.
+//
+// Index maps (a contraction's order is free, an output row's place is undone
+// at the write):
+//  * a half tile is 16 tokens; MMA row r < 8 is token 4 (r / 2) + r % 2, row
+//    8 + r the token two further.  The K rows of lane (gid, tig) = (lane / 4,
+//    lane % 4) and its four V rows 4 tig .. 4 tig + 3 then each lie in one
+//    group of four tokens: one block-table entry, one scale word.
+//  * S^T, k-step s: k index 2 tig + e stands for d = (D/4) tig + 4 s + e, and
+//    2 tig + 8 + e for d + 2: the lane's K bytes are contiguous.
+//  * O^T, m-tile i: row gid is d = (D/8) gid + 2 i, row gid + 8 the next: the
+//    lane's V bytes are contiguous, and so is the slice of o it ends with.
+//
+// The split.  The tiles of 32 tokens of every (sequence, KV head), in that
+// order, are cut into equal contiguous ranges, one per block, and each block's
+// range into one per warp.  A warp that holds a whole context writes it out.
+// The parts of contexts cut between the warps of a block are merged in shared
+// memory; a context cut between blocks leaves one record (m, l, o) per block
+// in the workspace, and the block that completes the context's count merges
+// them.  No block waits for another.
+#include <cmath>
+#include <mutex>
+
+#include "pa_fp4.cuh"
+#include "pa_host.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 32;                 // tokens per tile
+constexpr uint32_t kFull = 0xffffffffu;
+// Weights are exp2(x - max + kShift): binary16 keeps its full precision down
+// to 2^-14, so the shift moves the loss of small weights from 2^-14 to 2^-24
+// of the largest.  It cancels in o / l.
+constexpr float kShift = 10.f;
+
+struct Args {
+  const uint16_t* q;
+  uint16_t* out;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const int32_t* bt;
+  const int32_t* seq_lens;
+  uint32_t* ws_count;       // [PA_DECODE_MAX_CTAS], zero between calls
+  float* ws_rec;            // [grid][2] records of rec_floats(G, D)
+  int32_t* err;
+  long long num_blocks;
+  int num_seqs, stride, Hq, H, G, log2B, plane;
+  float scale_log2, v_scale;
+  int window, early_tables;
+};
+
+// o[G][D], m[G], l[G], padded to 16 bytes
+__host__ __device__ constexpr size_t rec_floats(int G, int D) {
+  return (size_t)G * D + (size_t)((2 * G + 3) & ~3);
+}
+
+__device__ __forceinline__ int clamp_len(int T, const Args& a) {
+  return (T < 0 || (long long)T > ((long long)a.stride << a.log2B)) ? 0 : T;
+}
+
+__device__ __forceinline__ int first_token(int T, const Args& a) {
+  return (a.window > 0 && T > a.window) ? T - a.window : 0;
+}
+
+// tiles of a context: from the tile that holds its first attended token
+__device__ __forceinline__ int num_tiles(int T, const Args& a) {
+  return (int)(((long long)T + kTile - 1) / kTile) - first_token(T, a) / kTile;
+}
+
+template <int kBytes>
+__device__ __forceinline__ void ld_stream(const uint8_t* p, uint32_t* r) {
+  if constexpr (kBytes == 16)
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "l"(p));
+  else if constexpr (kBytes == 8)
+    asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
+                 : "=r"(r[0]), "=r"(r[1])
+                 : "l"(p));
+  else
+    asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(r[0]) : "l"(p));
+}
+
+// One warp's state over a range of one context's tiles.
+template <int D, bool kBF16, int NH>
+struct Context {
+  static constexpr int KS = D / 16;        // k-steps of S^T
+  static constexpr int MT = D / 16;        // m-tiles of O^T
+  static constexpr int KW = D / 32;        // words of K codes per lane and row
+  static constexpr int VW = D / 64;        // words of V codes per lane and row
+  static constexpr bool kPair = !kBF16;    // weights as a pair of binary16 values
+  uint32_t qb[NH][KS][2];
+  float sl[NH][2];                         // score factor of heads 8 nh + 2 tig + e (log2)
+  float o[NH][MT][4];
+  float m[NH][2], l[NH][2];
+  // the tile being loaded: per half of 16 tokens
+  uint32_t kw[2][2][KW], ksc[2][KW / 2];
+  uint32_t vw[2][4][VW], vsc[2];
+  bool kok[2];
+
+  // The G query rows of this KV head as f16 fragments.  A bfloat16 row is
+  // brought into binary16's range by a power of two (its largest magnitude
+  // into [1, 2)), which the score factor takes back; elements 2^-14 below the
+  // largest lose bits that are below 2^-24 of it.
+  __device__ __forceinline__ void begin(const uint16_t* q, int G, float scale_log2) {
+    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      const int h = 8 * nh + gid;
+      uint32_t w[D / 8];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (h < G) x = __ldg(reinterpret_cast<const uint4*>(q + (size_t)h * D + (D / 4) * tig) + c);
+        w[4 * c] = x.x; w[4 * c + 1] = x.y; w[4 * c + 2] = x.z; w[4 * c + 3] = x.w;
+      }
+      float back = 1.f;
+      if constexpr (kBF16) {
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const float2 f = unpack2<true>(w[i]);
+          mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, 2));
+        // 2^e <= mx < 2^(e+1); zero, subnormal or infinite maxima keep a
+        // factor whose inverse is a normal number
+        int e = (int)(__float_as_uint(mx) >> 23);
+        e = min(max(e, 1), 253);
+        back = __uint_as_float((uint32_t)e << 23);
+        const float to = __uint_as_float((uint32_t)(254 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const float2 f = unpack2<true>(w[i]);
+          w[i] = pack2<false>(f.x * to, f.y * to);
+        }
+      }
+#pragma unroll
+      for (int s = 0; s < KS; ++s) {
+        qb[nh][s][0] = w[2 * s];
+        qb[nh][s][1] = w[2 * s + 1];
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sl[nh][e] = scale_log2 * __shfl_sync(kFull, back, 4 * (2 * tig + e));
+        m[nh][e] = -INFINITY;
+        l[nh][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) o[nh][i][0] = o[nh][i][1] = o[nh][i][2] = o[nh][i][3] = 0.f;
+    }
+  }
+
+  // K of one tile: plane[hf] is the plane of the block of this lane's token
+  // group gid / 2 of half hf, or null (nothing is read); row[hf] the group's
+  // first row in the block
+  __device__ __forceinline__ void load_k(const uint8_t* const (&plane)[2], const int (&row)[2],
+                                         int B) {
+    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      kok[hf] = plane[hf] != nullptr;
+      if (kok[hf]) {
+        const uint8_t* p = plane[hf] + (row[hf] + (gid & 1)) * (D / 2) + tig * (D / 8);
+        ld_stream<D / 8>(p, kw[hf][0]);
+        ld_stream<D / 8>(p + D, kw[hf][1]);
+        // the group's four tokens' scales: D / 64 words, of groups (D/64) tig ..
+        const uint8_t* sp = plane[hf] + B * (D / 2) + row[hf] * (D / 16) + tig * (D / 16);
+        ld_stream<D / 16>(sp, ksc[hf]);
+      }
+    }
+  }
+
+  // V of one tile: the lane's token group is tig
+  __device__ __forceinline__ void load_v(const uint8_t* const (&plane)[2], const int (&row)[2],
+                                         int B) {
+    const int lane = threadIdx.x & 31, gid = lane >> 2;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      if (plane[hf] != nullptr) {
+        const uint8_t* p = plane[hf] + row[hf] * (D / 2) + gid * (D / 16);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) ld_stream<D / 16>(p + t * (D / 2), vw[hf][t]);
+        const uint8_t* sp =
+            plane[hf] + B * (D / 2) + row[hf] * (D / 16) + (D == 128 ? gid : gid >> 1) * 4;
+        ld_stream<4>(sp, &vsc[hf]);
+      } else {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int w = 0; w < VW; ++w) vw[hf][t][w] = 0u;
+        vsc[hf] = 0u;
+      }
+    }
+  }
+
+  // scores of the loaded K
+  __device__ __forceinline__ void scores(float (&s)[2][NH][4]) {
+    const int gid = (threadIdx.x & 31) >> 2;
+    // bytes e and e + 2 of the lane's scale words: its tokens (rows gid, gid + 8)
+    const uint32_t sel = (gid & 1) ? 0x7351u : 0x6240u;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh)
+        s[hf][nh][0] = s[hf][nh][1] = s[hf][nh][2] = s[hf][nh][3] = 0.f;
+      // f16 scale pairs: sa = row gid's groups, sb = row gid + 8's
+      uint32_t sa, sb;
+      e4m3x4_to_f16x2x2(prmt(ksc[hf][0], ksc[hf][KW / 2 - 1], sel), sa, sb);
+#pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        uint32_t a[4], b[4];
+        e2m1x8_to_f16x2(kw[hf][0][w], a);
+        e2m1x8_to_f16x2(kw[hf][1][w], b);
+        const uint32_t dup = w < 2 ? 0x1010u : 0x3232u;   // 16 codes are two words
+        const uint32_t s0 = prmt(sa, sa, dup), s1 = prmt(sb, sb, dup);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i] = hmul2(a[i], s0);
+          b[i] = hmul2(b[i], s1);
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh)
+            mma_16816<false>(s[hf][nh], a[2 * u], b[2 * u], a[2 * u + 1], b[2 * u + 1],
+                             qb[nh][2 * w + u][0], qb[nh][2 * w + u][1]);
+      }
+    }
+  }
+
+  // online softmax of the tile's scores; pb: the weights as B fragments
+  // (pl: what their rounding to binary16 left, for binary16 outputs).  ok: the
+  // K of each half was read; tokens [lo, hi) of the tile are attended.
+  __device__ __forceinline__ void weights(float (&s)[2][NH][4], const bool (&ok)[2], int lo, int hi,
+                                          uint32_t (&pb)[2][NH][2], uint32_t (&pl)[2][NH][2]) {
+    const int gid = (threadIdx.x & 31) >> 2;
+    const int tok = 4 * (gid >> 1) + (gid & 1);
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 16 * hf + tok + (e >> 1) * 2;
+          const bool in = ok[hf] && t >= lo && t < hi;
+          s[hf][nh][e] = in ? s[hf][nh][e] * sl[nh][e & 1] : -INFINITY;
+          mx[e & 1] = fmaxf(mx[e & 1], s[hf][nh][e]);
+        }
+      float alpha[2], base[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], 4));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], 8));
+        mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], 16));
+        const float mn = fmaxf(m[nh][e], mx[e]);
+        // nothing attended so far: any finite base gives weights of zero
+        base[e] = (mn == -INFINITY ? 0.f : mn) - kShift;
+        alpha[e] = m[nh][e] == mn ? 1.f : ex2_approx(m[nh][e] - mn);
+        m[nh][e] = mn;
+      }
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float p0 = ex2_approx(s[hf][nh][2 * r] - base[0]);
+          const float p1 = ex2_approx(s[hf][nh][2 * r + 1] - base[1]);
+          const uint32_t pk = pack2<false>(p0, p1);
+          const float2 f = unpack2<false>(pk);
+          if constexpr (kPair) {
+            sum[0] += p0;
+            sum[1] += p1;
+            pl[hf][nh][r] = movmatrix_trans(pack2<false>(p0 - f.x, p1 - f.y));
+          } else {   // the weights that are used
+            sum[0] += f.x;
+            sum[1] += f.y;
+          }
+          pb[hf][nh][r] = movmatrix_trans(pk);
+        }
+      l[nh][0] = l[nh][0] * alpha[0] + sum[0];
+      l[nh][1] = l[nh][1] * alpha[1] + sum[1];
+      if (__any_sync(kFull, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+          o[nh][i][0] *= alpha[0];
+          o[nh][i][1] *= alpha[1];
+          o[nh][i][2] *= alpha[0];
+          o[nh][i][3] *= alpha[1];
+        }
+      }
+    }
+  }
+
+  // O^T += V^T P^T of the loaded V; tokens [lo, hi) of the tile are attended
+  // (the others' weights are zero, and their scales, which may be NaN codes,
+  // are cleared)
+  __device__ __forceinline__ void values(const uint32_t (&pb)[2][NH][2],
+                                         const uint32_t (&pl)[2][NH][2], int lo, int hi) {
+    const int tig = threadIdx.x & 3;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t sc = vsc[hf];
+      const int t0 = 16 * hf + 4 * tig;
+      if (t0 < lo || t0 + 4 > hi) {
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          if (t0 + b < lo || t0 + b >= hi) sc &= ~(0xffu << (8 * b));
+      }
+      uint32_t s01, s23;
+      e4m3x4_to_f16x2x2(sc, s01, s23);
+#pragma unroll
+      for (int w = 0; w < VW; ++w) {
+        const uint32_t v0 = vw[hf][0][w], v1 = vw[hf][1][w], v2 = vw[hf][2][w], v3 = vw[hf][3][w];
+        constexpr uint32_t kLow = 0x0f0f0f0fu;
+        // bytes of two tokens' codes of one head_dim: even and odd elements
+        uint32_t a0[4], a1[4], a2[4], a3[4];
+        e2m1x8_to_f16x2((v0 & kLow) | ((v1 << 4) & ~kLow), a0);
+        e2m1x8_to_f16x2(((v0 >> 4) & kLow) | (v1 & ~kLow), a1);
+        e2m1x8_to_f16x2((v2 & kLow) | ((v3 << 4) & ~kLow), a2);
+        e2m1x8_to_f16x2(((v2 >> 4) & kLow) | (v3 & ~kLow), a3);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t x0 = hmul2(a0[b], s01), x1 = hmul2(a1[b], s01);
+          const uint32_t x2 = hmul2(a2[b], s23), x3 = hmul2(a3[b], s23);
+#pragma unroll
+          for (int nh = 0; nh < NH; ++nh) {
+            mma_16816<false>(o[nh][4 * w + b], x0, x1, x2, x3, pb[hf][nh][0], pb[hf][nh][1]);
+            if constexpr (kPair)
+              mma_16816<false>(o[nh][4 * w + b], x0, x1, x2, x3, pl[hf][nh][0], pl[hf][nh][1]);
+          }
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ float total_l(int nh, int e) const {
+    float lt = l[nh][e];
+    lt += __shfl_xor_sync(kFull, lt, 4);
+    lt += __shfl_xor_sync(kFull, lt, 8);
+    lt += __shfl_xor_sync(kFull, lt, 16);
+    return lt;
+  }
+
+  // the whole context: its output rows
+  __device__ __forceinline__ void write(uint16_t* out, int G, float v_scale) const {
+    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float lt = total_l(nh, e);
+        const int h = 8 * nh + 2 * tig + e;
+        if (h >= G) continue;
+        const float mul = lt == 0.f ? 0.f : v_scale / lt;
+        uint4* dst = reinterpret_cast<uint4*>(out + (size_t)h * D + (D / 8) * gid);
+#pragma unroll
+        for (int i = 0; i < MT; i += 4) {
+          uint4 pk;
+          pk.x = pack2<kBF16>(o[nh][i][e] * mul, o[nh][i][2 + e] * mul);
+          pk.y = pack2<kBF16>(o[nh][i + 1][e] * mul, o[nh][i + 1][2 + e] * mul);
+          pk.z = pack2<kBF16>(o[nh][i + 2][e] * mul, o[nh][i + 2][2 + e] * mul);
+          pk.w = pack2<kBF16>(o[nh][i + 3][e] * mul, o[nh][i + 3][2 + e] * mul);
+          dst[i / 4] = pk;
+        }
+      }
+  }
+
+  // a part of it: o[G][D], m[G], l[G]
+  __device__ __forceinline__ void store(float* rec, int G) const {
+    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float lt = total_l(nh, e);
+        const int h = 8 * nh + 2 * tig + e;
+        if (h >= G) continue;
+        if (gid == 0) {
+          rec[(size_t)G * D + h] = m[nh][e];
+          rec[(size_t)G * D + G + h] = lt;
+        }
+        float4* dst = reinterpret_cast<float4*>(rec + (size_t)h * D + (D / 8) * gid);
+#pragma unroll
+        for (int i = 0; i < MT; i += 2)
+          dst[i / 2] = make_float4(o[nh][i][e], o[nh][i][2 + e], o[nh][i + 1][e],
+                                   o[nh][i + 1][2 + e]);
+      }
+  }
+};
+
+// Four elements of one row of a context, merged over parts: acc = sum_p
+// 2^(m_p - m) o_p, l likewise, m the largest m_p.
+struct Merged {
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m = -INFINITY, l = 0.f;
+
+  __device__ __forceinline__ void fold(float mk, float lk, const float4& v) {
+    const float mn = fmaxf(m, mk), base = mn == -INFINITY ? 0.f : mn;
+    const float wa = exp2f(m - base), wb = exp2f(mk - base);
+    m = mn;
+    l = l * wa + lk * wb;
+    acc.x = acc.x * wa + v.x * wb;
+    acc.y = acc.y * wa + v.y * wb;
+    acc.z = acc.z * wa + v.z * wb;
+    acc.w = acc.w * wa + v.w * wb;
+  }
+
+  // row r, elements 4 c .. 4 c + 3 of a record
+  __device__ __forceinline__ void fold_record(const float* rec, int G, int D, int r, int c) {
+    fold(rec[(size_t)G * D + r], rec[(size_t)G * D + G + r],
+         *reinterpret_cast<const float4*>(rec + (size_t)r * D + 4 * c));
+  }
+
+  template <bool kBF16>
+  __device__ __forceinline__ void write(uint16_t* dst, float v_scale) const {
+    const float mul = l == 0.f ? 0.f : v_scale / l;
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(pack2<kBF16>(acc.x * mul, acc.y * mul), pack2<kBF16>(acc.z * mul, acc.w * mul));
+  }
+};
+
+// A context's part held by one warp.
+struct Part {
+  long long pair;     // sequence * H + head, or -1
+  long long g0;       // index of the context's first tile
+  int nt;             // its tiles
+  int begins, ends;   // the part starts / ends with the context
+};
+
+struct Shared {
+  long long run_pref[kThreads];   // tiles (of one head) before each thread's run of sequences
+  long long warp_tot[kWarps];
+  Part part[2 * kWarps];
+  int group_first[2 * kWarps + 1];
+  int groups;
+  int merges;                     // contexts this block owes the merge of
+  Part merge[2];
+};
+
+template <int D, bool kBF16, int NH>
+__global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_fp4_kernel(const Args a) {
+  extern __shared__ __align__(16) float slots[];   // [2 * kWarps] records
+  __shared__ Shared sh;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int gid = lane >> 2, tig = lane & 3;
+  const int B = 1 << a.log2B;
+  const size_t rf = rec_floats(a.G, D);
+
+  if (!a.early_tables) grid_dep_wait();
+  // ---- every thread counts the tiles of a run of sequences -----------------
+  const int per = (a.num_seqs + kThreads - 1) / kThreads;
+  const int run0 = min(a.num_seqs, tid * per), run1 = min(a.num_seqs, run0 + per);
+  long long mine = 0;
+  bool odd = false;   // this block has to report or zero one of the run's sequences
+  for (int i = run0; i < run1; ++i) {
+    const int T = clamp_len(__ldg(a.seq_lens + i), a);
+    mine += num_tiles(T, a);
+    odd |= T == 0 && (i % gridDim.x) == blockIdx.x;
+  }
+  long long incl = mine;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long n = __shfl_up_sync(kFull, incl, s);
+    if (lane >= s) incl += n;
+  }
+  if (lane == 31) sh.warp_tot[warp] = incl;
+  if (tid < 2 * kWarps) sh.part[tid].pair = -1;
+  if (tid == 0) sh.merges = 0;
+  __syncthreads();
+  long long off = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) off += sh.warp_tot[w];
+    total += sh.warp_tot[w];
+  }
+  sh.run_pref[tid] = off + incl - mine;
+  __syncthreads();
+  if (a.early_tables) grid_dep_wait();
+  if (tid == 0) grid_dep_launch();
+  if (odd)
+    for (int i = run0; i < run1; ++i) {
+      if ((i % gridDim.x) != blockIdx.x) continue;
+      const int T0 = __ldg(a.seq_lens + i);
+      if (clamp_len(T0, a) != T0) set_error(a.err, PA_DEVERR_SEQ_LEN);
+      if (clamp_len(T0, a) == 0) {
+        uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)i * a.Hq * D);
+        for (int e = 0; e < a.Hq * D / 8; ++e) dst[e] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    }
+
+  // ---- this block's and this warp's range of tiles -------------------------
+  // at least kWarps tiles a block, so that small batches do not split contexts
+  // between blocks for nothing
+  const long long U = total * a.H;
+  const long long nb = min((long long)gridDim.x, (U + kWarps - 1) / kWarps);
+  if ((long long)blockIdx.x >= nb) return;
+  const long long c0 = U * blockIdx.x / nb, c1 = U * (blockIdx.x + 1) / nb;
+  const long long n_cta = c1 - c0;
+  long long g = c0 + n_cta * warp / kWarps;
+  const long long g_end = c0 + n_cta * (warp + 1) / kWarps;
+
+  if (g < g_end) {
+    // the sequence of tile g: the last run that starts at or before it, then
+    // along the run
+    int r = 0;
+#pragma unroll
+    for (int b = kThreads / 2; b > 0; b >>= 1)
+      if (sh.run_pref[r + b] * a.H <= g) r += b;
+    int i = r * per;
+    long long g_seq = sh.run_pref[r] * a.H;   // first tile of sequence i
+    int T = 0, nt = 0;
+    auto load_seq = [&]() {
+      T = i < a.num_seqs ? clamp_len(__ldg(a.seq_lens + i), a) : 0;
+      nt = num_tiles(T, a);
+    };
+    load_seq();
+    auto skip_to = [&]() {   // the sequence that holds tile g
+      while (i < a.num_seqs && g >= g_seq + (long long)nt * a.H) {
+        g_seq += (long long)nt * a.H;
+        ++i;
+        load_seq();
+      }
+    };
+    skip_to();
+
+    Context<D, kBF16, NH> cx;
+    int segments = 0;
+    while (g < g_end && i < a.num_seqs) {
+      if (g < g_seq) {   // only if seq_lens changes during the call: never walk blind
+        set_error(a.err, PA_DEVERR_SEQ_LEN);
+        break;
+      }
+      const int h = (int)((g - g_seq) / nt);
+      const long long g0 = g_seq + (long long)h * nt;
+      const int ta = (int)(g - g0), tb = (int)min((long long)nt, g_end - g0);
+      const int first = first_token(T, a);
+      const int tile_base = first / kTile;
+      const int32_t* row_bt = a.bt + (size_t)i * a.stride;
+      int win = -1, ent = -1;   // entries [32 win, 32 win + 32) of the table row, one a lane
+      // the planes and rows of tile k: K by token group gid / 2 of each half, V by group tig
+      const uint8_t *kp[2], *vp[2];
+      int kr[2], vr[2];
+      auto locate = [&](int k) {
+        const int t0 = (tile_base + k) * kTile;
+        const int w = (t0 >> a.log2B) >> 5;
+        if (w != win) {
+          win = w;
+          const int idx = 32 * w + lane;
+          ent = -1;
+          // entries of blocks that hold an attended token
+          if (idx >= (first >> a.log2B) && idx <= ((T - 1) >> a.log2B)) {
+            ent = __ldg(row_bt + idx);
+            if (ent < 0 || (long long)ent >= a.num_blocks) {
+              set_error(a.err, PA_DEVERR_BLOCK_ID);
+              ent = -1;
+            }
+          }
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int tk = t0 + 16 * hf + 4 * (gid >> 1), tv = t0 + 16 * hf + 4 * tig;
+          const int bk = __shfl_sync(kFull, ent, (tk >> a.log2B) & 31);
+          const int bv = __shfl_sync(kFull, ent, (tv >> a.log2B) & 31);
+          kr[hf] = tk & (B - 1);
+          vr[hf] = tv & (B - 1);
+          kp[hf] = (bk < 0 || tk >= T || tk + 4 <= first)
+                       ? nullptr
+                       : a.kc + fp4_plane(bk, a.H, h, a.plane);
+          vp[hf] = (bv < 0 || tv >= T || tv + 4 <= first)
+                       ? nullptr
+                       : a.vc + fp4_plane(bv, a.H, h, a.plane);
+        }
+      };
+      locate(ta);
+      cx.load_k(kp, kr, B);
+      cx.load_v(vp, vr, B);
+      cx.begin(a.q + ((size_t)i * a.Hq + (size_t)h * a.G) * D, a.G, a.scale_log2);
+      for (int k = ta; k < tb; ++k) {
+        const int t0 = (tile_base + k) * kTile;
+        float s[2][NH][4];
+        uint32_t pb[2][NH][2], pl[2][NH][2];
+        const bool ok[2] = {cx.kok[0], cx.kok[1]};
+        cx.scores(s);
+        const bool more = k + 1 < tb;
+        if (more) {
+          locate(k + 1);
+          cx.load_k(kp, kr, B);
+        }
+        cx.weights(s, ok, first - t0, T - t0, pb, pl);
+        cx.values(pb, pl, first - t0, T - t0);
+        if (more) cx.load_v(vp, vr, B);
+      }
+      if (ta == 0 && tb == nt) {
+        cx.write(a.out + ((size_t)i * a.Hq + (size_t)h * a.G) * D, a.G, a.v_scale);
+      } else {
+        const int k = 2 * warp + (segments > 0 ? 1 : 0);
+        cx.store(slots + (size_t)k * rf, a.G);
+        if (lane == 0) {
+          Part& p = sh.part[k];
+          p.pair = (long long)i * a.H + h;
+          p.g0 = g0;
+          p.nt = nt;
+          p.begins = ta == 0;
+          p.ends = tb == nt;
+        }
+      }
+      ++segments;
+      g = g0 + tb;
+      skip_to();
+    }
+  }
+  __syncthreads();
+
+  // ---- parts of one context held by this block's warps ---------------------
+  // parts are in tile order; those of one context follow each other
+  if (tid == 0) {
+    int n = 0;
+    long long last = -1;
+    for (int k = 0; k < 2 * kWarps; ++k) {
+      if (sh.part[k].pair < 0) continue;
+      if (sh.part[k].pair != last) sh.group_first[n++] = k;
+      last = sh.part[k].pair;
+    }
+    sh.group_first[n] = 2 * kWarps;
+    sh.groups = n;
+  }
+  __syncthreads();
+  const int cols = D / 4, per_group = a.G * cols;
+  for (int e = tid; e < sh.groups * per_group; e += kThreads) {
+    const int gr = e / per_group, r = (e % per_group) / cols, c = e % cols;
+    const int k0 = sh.group_first[gr], k1 = sh.group_first[gr + 1];
+    Merged x;
+    int k_last = k0;
+    for (int k = k0; k < k1; ++k) {
+      if (sh.part[k].pair < 0) continue;
+      k_last = k;
+      x.fold_record(slots + (size_t)k * rf, a.G, D, r, c);
+    }
+    const long long pair = sh.part[k0].pair;
+    if (sh.part[k0].begins && sh.part[k_last].ends) {
+      const long long i = pair / a.H, h = pair % a.H;
+      x.write<kBF16>(a.out + ((size_t)i * a.Hq + (size_t)h * a.G + r) * D + 4 * c, a.v_scale);
+    } else {
+      // record 0: the context began in an earlier block; 1: it begins here
+      float* rec = a.ws_rec + ((size_t)blockIdx.x * 2 + (sh.part[k0].begins ? 1 : 0)) * rf;
+      *reinterpret_cast<float4*>(rec + (size_t)r * D + 4 * c) = x.acc;
+      if (c == 0) {
+        rec[(size_t)a.G * D + r] = x.m;
+        rec[(size_t)a.G * D + a.G + r] = x.l;
+      }
+    }
+  }
+  __syncthreads();
+  // ---- contexts cut between blocks: count this block's record --------------
+  if (tid == 0) {
+    for (int gr = 0; gr < sh.groups; ++gr) {
+      const Part p = sh.part[sh.group_first[gr]];
+      // inside this block's range: already written
+      if (p.g0 >= c0 && p.g0 + p.nt <= c1) continue;
+      const long long f = ((p.g0 + 1) * nb - 1) / U, e = ((p.g0 + p.nt) * nb - 1) / U;
+      uint32_t* cnt = a.ws_count + e;
+      // releases the block's record (ordered before by the barrier), acquires
+      // those counted before it
+      if (atom_add_acq_rel_gpu(cnt, 1u) + 1u == (uint32_t)(e - f + 1)) {
+        *cnt = 0u;   // ready for the next call
+        sh.merge[sh.merges++] = p;
+      }
+    }
+  }
+  __syncthreads();
+  for (int k = 0; k < sh.merges; ++k) {
+    const Part p = sh.merge[k];
+    const long long f = ((p.g0 + 1) * nb - 1) / U, e = ((p.g0 + p.nt) * nb - 1) / U;
+    const long long i = p.pair / a.H, h = p.pair % a.H;
+    for (int t = tid; t < per_group; t += kThreads) {
+      const int r = t / cols, c = t % cols;
+      // record 1 of block f, then record 0 of blocks f + 1 .. e
+      Merged x;
+      x.fold_record(a.ws_rec + ((size_t)f * 2 + 1) * rf, a.G, D, r, c);
+#pragma unroll 4
+      for (long long b = f + 1; b <= e; ++b)
+        x.fold_record(a.ws_rec + (size_t)b * 2 * rf, a.G, D, r, c);
+      x.write<kBF16>(a.out + ((size_t)i * a.Hq + (size_t)h * a.G + r) * D + 4 * c, a.v_scale);
+    }
+  }
+}
+
+typedef void (*Kernel)(const Args);
+
+Kernel pick(int D, bool bf16, bool hi) {
+  if (D == 64)
+    return bf16 ? (hi ? decode_fp4_kernel<64, true, 2> : decode_fp4_kernel<64, true, 1>)
+                : (hi ? decode_fp4_kernel<64, false, 2> : decode_fp4_kernel<64, false, 1>);
+  return bf16 ? (hi ? decode_fp4_kernel<128, true, 2> : decode_fp4_kernel<128, true, 1>)
+              : (hi ? decode_fp4_kernel<128, false, 2> : decode_fp4_kernel<128, false, 1>);
+}
+
+struct Plan {
+  Kernel kern;
+  int grid;
+  size_t smem, count_bytes, rec_bytes;
+};
+
+// Blocks per SM depend on the kernel, the group size and the device: looked up
+// once each, with the kernel's opt-in to its shared memory.
+constexpr int kMaxDevices = 64;
+int g_per_sm[kMaxDevices][2][2][17];   // [device][D == 128][bf16][G], 0 = not yet
+std::mutex g_mu;
+
+int make_plan(int Hq, int H, int D, int B, int q_dtype, int flags, int num_ctas, Plan* p) {
+  if (Hq <= 0 || H <= 0 || num_ctas < 0 || num_ctas > PA_DECODE_MAX_CTAS)
+    return PA_ERR_INVALID_ARG;
+  if (q_dtype != PA_F16 && q_dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+  if (D != 64 && D != 128) return PA_ERR_UNSUPPORTED;
+  if (!is_pow2(B) || B < 4 || B > 256) return PA_ERR_UNSUPPORTED;
+  if (Hq % H != 0) return PA_ERR_INVALID_ARG;
+  const int G = Hq / H;
+  if (G > 16) return PA_ERR_UNSUPPORTED;
+  flags &= ~PA_DECODE_TABLES_READY;
+  if (flags == PA_DECODE_SIMT) return PA_ERR_UNSUPPORTED;
+  if (flags != PA_DECODE_AUTO && flags != PA_DECODE_MMA) return PA_ERR_INVALID_ARG;
+  const bool bf16 = q_dtype == PA_BF16;
+  p->kern = pick(D, bf16, G > 8);
+  p->smem = 2 * kWarps * rec_floats(G, D) * sizeof(float);
+  DeviceInfo di;
+  if (int rc = current_device_info(&di)) return rc;
+  int per_sm;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    int& c = g_per_sm[di.device][D == 128][bf16][G];
+    if (c == 0) {
+      const size_t most = 2 * kWarps * rec_floats(G > 8 ? 16 : 8, D) * sizeof(float);
+      int n = 0;
+      cudaError_t e = cudaFuncSetAttribute(p->kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           (int)most);
+      if (e) return launch_status(e, "cudaFuncSetAttribute (4-bit decode)");
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, p->kern, kThreads, p->smem);
+      if (e) return launch_status(e, "occupancy (4-bit decode)");
+      if (n < 1) return PA_ERR_UNSUPPORTED;
+      c = n;
+    }
+    per_sm = c;
+  }
+  p->grid = num_ctas > 0 ? num_ctas : di.sm_count * per_sm;
+  if (p->grid > PA_DECODE_MAX_CTAS) return PA_ERR_INVALID_ARG;
+  p->count_bytes = (size_t)PA_DECODE_MAX_CTAS * sizeof(uint32_t);
+  p->rec_bytes = (size_t)p->grid * 2 * rec_floats(G, D) * sizeof(float);
+  return PA_OK;
+}
+
+}  // namespace
+
+int decode_fp4_workspace(int Hq, int H, int D, int B, int flags, int num_ctas, size_t* bytes) {
+  Plan b{}, f{};
+  // the larger of the two query dtypes' grids
+  if (int rc = make_plan(Hq, H, D, B, PA_BF16, flags, num_ctas, &b)) return rc;
+  if (int rc = make_plan(Hq, H, D, B, PA_F16, flags, num_ctas, &f)) return rc;
+  *bytes = b.count_bytes + (b.rec_bytes > f.rec_bytes ? b.rec_bytes : f.rec_bytes);
+  return PA_OK;
+}
+
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" int pa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
+                             const int32_t* block_tables, int32_t table_stride,
+                             const int32_t* seq_lens, int32_t num_seqs, int32_t num_q_heads,
+                             int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                             int64_t num_blocks, int32_t q_dtype, float scale, float k_scale,
+                             float v_scale, int32_t window, void* out, void* workspace,
+                             size_t workspace_bytes, int32_t flags, int32_t num_ctas,
+                             int32_t* err_word, pa_stream stream) {
+  if (num_seqs < 0 || table_stride < 0 || num_blocks < 0 || window < 0) return PA_ERR_INVALID_ARG;
+  if (!(k_scale > 0.f) || !(v_scale > 0.f) || !std::isfinite(k_scale) || !std::isfinite(v_scale))
+    return PA_ERR_INVALID_ARG;
+  Plan p{};
+  if (int rc = make_plan(num_q_heads, num_kv_heads, head_dim, block_size, q_dtype, flags, num_ctas,
+                         &p))
+    return rc;
+  if (num_seqs == 0) return PA_OK;
+  if (!q || !k_cache || !v_cache || !block_tables || !seq_lens || !out || !workspace)
+    return PA_ERR_INVALID_ARG;
+  if (num_blocks == 0 || table_stride == 0) return PA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      !aligned16(workspace))
+    return PA_ERR_INVALID_ARG;
+  if (workspace_bytes < p.count_bytes + p.rec_bytes) return PA_ERR_WORKSPACE;
+  Args a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.out = static_cast<uint16_t*>(out);
+  a.kc = static_cast<const uint8_t*>(k_cache);
+  a.vc = static_cast<const uint8_t*>(v_cache);
+  a.bt = block_tables;
+  a.seq_lens = seq_lens;
+  a.ws_count = static_cast<uint32_t*>(workspace);
+  a.ws_rec = reinterpret_cast<float*>(static_cast<char*>(workspace) + p.count_bytes);
+  a.err = err_word;
+  a.num_blocks = num_blocks;
+  a.num_seqs = num_seqs;
+  a.stride = table_stride;
+  a.Hq = num_q_heads;
+  a.H = num_kv_heads;
+  a.G = num_q_heads / num_kv_heads;
+  a.log2B = ilog2(block_size);
+  a.plane = block_size * fp4_row_bytes(head_dim);
+  a.scale_log2 = scale * k_scale * 1.4426950408889634f;
+  a.v_scale = v_scale;
+  a.window = window;
+  a.early_tables = (flags & PA_DECODE_TABLES_READY) ? 1 : 0;
+  clear_stale_error();
+  return launch_status(launch_pdl(p.kern, dim3((unsigned)p.grid), dim3(kThreads), p.smem,
+                                  static_cast<cudaStream_t>(stream), a),
+                       "4-bit decode launch");
+}

@@ -68,6 +68,9 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+// Bytes of workspace pa_decode_fp4 needs for a shape (pa_decode_fp4.cu).
+int decode_fp4_workspace(int Hq, int Hkv, int D, int B, int flags, int num_ctas, size_t* bytes);
+
 // Clears an error left by an earlier, already reported runtime call so that
 // the check after the next launch sees only that launch.
 inline void clear_stale_error() {

@@ -9,7 +9,8 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import PA_BF16, PA_DECODE_AUTO, PA_F16, PA_FP8_E4M3, PA_SWAP_IN, PA_SWAP_OUT
+from ._lib import (PA_BF16, PA_DECODE_AUTO, PA_F16, PA_FP4_E2M1, PA_FP8_E4M3, PA_SWAP_IN,
+                   PA_SWAP_OUT)
 
 
 class PAError(RuntimeError):
@@ -61,6 +62,64 @@ def _fp8_pools(k_cache, v_cache):
     if k_cache.dtype != torch.uint8:
         raise TypeError("E4M3 pools must be uint8 tensors of codes")
     return shape
+
+
+def pa_fp4_pool_shape(num_blocks, block_size, num_kv_heads, head_dim):
+    """Shape of a 4-bit pool, a uint8 tensor: [num_blocks, H_kv, B, 9 D / 16].  A
+    block's head holds its codes [B, D / 2], then its scales
+    [B / 4, D / 16, 4], in the B * 9 D / 16 bytes of that plane."""
+    return (num_blocks, num_kv_heads, block_size, head_dim // 2 + head_dim // 16)
+
+
+# bytes of a 4-bit row -> head_dim
+_FP4_HEAD_DIM = {36: 64, 72: 128}
+
+
+def _fp4_pools(k_cache, v_cache):
+    """(num_blocks, B, H_kv, D) of a pair of 4-bit pools."""
+    nb, H, B, row = _pool_shape(k_cache, v_cache)
+    if k_cache.dtype != torch.uint8:
+        raise TypeError("4-bit pools must be uint8 tensors of codes and scales")
+    if row not in _FP4_HEAD_DIM:
+        raise ValueError("4-bit pools must be [num_blocks, H_kv, B, 9 D / 16], D 64 or 128")
+    return nb, B, H, _FP4_HEAD_DIM[row]
+
+
+def _block_pools(k_cache, v_cache):
+    """(num_blocks, B, H_kv, D, dtype code) of pools of any element type."""
+    a, b, c, d = _pool_shape(k_cache, v_cache)
+    if k_cache.dtype != torch.uint8:
+        return a, b, c, d, _dtype_code(k_cache)
+    if d in _FP4_HEAD_DIM:
+        return a, c, b, _FP4_HEAD_DIM[d], PA_FP4_E2M1
+    return a, b, c, d, PA_FP8_E4M3
+
+
+def _here(*tensors):
+    """Every tensor given is on the current device, whose stream the call uses."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError("every tensor must be on the current device, cuda:%d" % dev)
+
+
+def _i32(t, name):
+    _cuda(t, name)
+    if t.dtype != torch.int32:
+        raise TypeError("%s must be int32" % name)
+
+
+def _err_word(err):
+    if err is not None and (not err.is_cuda or err.dtype != torch.int32 or err.numel() < 1):
+        raise ValueError("err must be an int32 CUDA tensor")
+    return err
+
+
+def _slots_out(slot_mapping, n_tok):
+    if slot_mapping is not None:
+        _cuda(slot_mapping, "slot_mapping")
+        if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != n_tok:
+            raise ValueError("slot_mapping must be int64 [num_tokens]")
 
 
 def pa_version():
@@ -140,14 +199,13 @@ def pa_cache_write_mapped(k, v, block_tables, token_seq, token_pos, k_cache, v_c
 def pa_copy_blocks(pairs, k_cache, v_cache, err=None):
     """Copy pool block src -> dst (K and V) for each row (src, dst) of pairs.
 
-    Pools of float16 / bfloat16 elements, or uint8 E4M3 codes."""
+    Pools of float16 / bfloat16 elements, uint8 E4M3 codes, or 4-bit pools."""
     L = _lib.load()
-    nb, B, H, D = _pool_shape(k_cache, v_cache)
+    nb, B, H, D, code = _block_pools(k_cache, v_cache)
     _cuda(pairs, "pairs")
     if pairs.dtype != torch.int32:
         raise TypeError("pairs must be int32 [n, 2]")
     n = pairs.numel() // 2
-    code = PA_FP8_E4M3 if k_cache.dtype == torch.uint8 else _dtype_code(k_cache)
     _check(L.pa_copy_blocks(_ptr(pairs), n, _ptr(k_cache), _ptr(v_cache), nb, B, H, D,
                             code, _ptr(err), _stream()), "pa_copy_blocks")
 
@@ -169,12 +227,10 @@ def pa_swap_blocks(pairs, src_k, src_v, dst_k, dst_v, err=None):
     for t in (host_k, host_v):
         if not t.is_contiguous():
             raise ValueError("the host pools must be contiguous")
-    _pool_shape(dev_k, dev_v)
+    nbd, B, H, D, code = _block_pools(dev_k, dev_v)
     if host_k.shape[1:] != dev_k.shape[1:] or host_k.dtype != dev_k.dtype or \
             host_v.shape != host_k.shape or host_v.dtype != host_k.dtype:
         raise ValueError("host and device pools must share the block shape and dtype")
-    nbd, B, H, D = dev_k.shape
-    code = PA_FP8_E4M3 if dev_k.dtype == torch.uint8 else _dtype_code(dev_k)
     direction = PA_SWAP_OUT if src_k.is_cuda else PA_SWAP_IN
     _check(L.pa_swap_blocks(_ptr(pairs), pairs.numel() // 2, direction, _ptr(dev_k), _ptr(dev_v),
                             nbd, ctypes.c_void_p(host_k.data_ptr()),
@@ -335,6 +391,201 @@ def pa_decode_fp8(q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v
                            _ptr(out), _ptr(workspace),
                            workspace.numel() * workspace.element_size(), int(flags),
                            int(num_ctas), _ptr(err), _stream()), "pa_decode_fp8")
+    return out
+
+
+def _token_rows(t, name, n_tok, heads, D):
+    """A [num_tokens, heads, D] tensor whose rows are contiguous within a token;
+    tokens may lie any multiple of 8 elements apart.  Returns that distance."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.shape != (n_tok, heads, D):
+        raise ValueError("%s must be [num_tokens, heads, D] = %s" % (name, (n_tok, heads, D)))
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != D):
+        raise ValueError("the heads of a token must be contiguous in %s" % name)
+    return s0 if n_tok > 1 else heads * D
+
+
+def pa_append_rope(q, k, v, cos_sin, block_tables, token_seq, token_pos, k_cache, v_cache,
+                   interleaved=False, q_norm=None, k_norm=None, eps=1e-6, k_scale=1.0,
+                   v_scale=1.0, q_out=None, slot_mapping=None, err=None):
+    """A step's projections into the attention in one launch: RMS norms of the
+    query and key heads (when q_norm / k_norm, [D], are given), the position
+    rotation, the rotated queries returned ([num_tokens, Hq, D]) and keys and
+    values stored at slot block_tables[seq][pos // B] * B + pos % B.
+
+    q [num_tokens, Hq, D] (or None), k, v [num_tokens, H_kv, D]: float16 or
+    bfloat16, heads contiguous, tokens any multiple of 8 elements apart (views
+    of a fused projection's output).  cos_sin: float32 [max_pos, rotary_dim],
+    the row of a position holding rotary_dim / 2 cosines, then as many sines
+    (None: no rotation).  Element i pairs with i + rotary_dim / 2, or 2 i with
+    2 i + 1 when interleaved.  The pools are of the inputs' dtype
+    [num_blocks, B, H_kv, D], uint8 E4M3 codes of that shape, or 4-bit pools
+    (pa_fp4_pool_shape); k_scale and v_scale apply to the last two.  Tokens of
+    sequence -1 are padding: they write nothing, and their rows of q_out keep
+    what they held (zeros when q_out is made here)."""
+    L = _lib.load()
+    nb, B, H, D, code = _block_pools(k_cache, v_cache)
+    _i32(block_tables, "block_tables")
+    _i32(token_seq, "token_seq")
+    _i32(token_pos, "token_pos")
+    n_tok = token_seq.numel()
+    if token_pos.numel() != n_tok:
+        raise ValueError("token_seq and token_pos differ in length")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, stride]")
+    ks, vs = _token_rows(k, "k", n_tok, H, D), _token_rows(v, "v", n_tok, H, D)
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise TypeError("q, k and v must share a dtype")
+    if k_cache.dtype not in (k.dtype, torch.uint8):
+        raise TypeError("the pools must be of k's dtype, or uint8")
+    Hq, qs = 0, 0
+    if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must be [num_tokens, Hq, D]")
+        Hq = q.shape[1]
+        qs = _token_rows(q, "q", n_tok, Hq, D)
+        if q_out is None:
+            q_out = torch.zeros((n_tok, Hq, D), dtype=q.dtype, device=q.device)
+        _cuda(q_out, "q_out")
+        if q_out.shape != (n_tok, Hq, D) or q_out.dtype != q.dtype:
+            raise ValueError("q_out must be [num_tokens, Hq, D] of q's dtype")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rot = max_pos = 0
+    if cos_sin is not None:
+        _cuda(cos_sin, "cos_sin")
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+            raise TypeError("cos_sin must be float32 [max_pos, rotary_dim]")
+        max_pos, rot = cos_sin.shape
+    for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is not None:
+            _cuda(t, n)
+            if t.shape != (D,) or t.dtype != k.dtype:
+                raise ValueError("%s must be [D] of k's dtype" % n)
+    _slots_out(slot_mapping, n_tok)
+    _here(q, k, v, cos_sin, q_norm, k_norm, block_tables, token_seq, token_pos, k_cache, v_cache,
+          q_out, slot_mapping, _err_word(err))
+    _check(L.pa_append_rope(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _dtype_code(k), _ptr(cos_sin),
+                            rot, max_pos, int(bool(interleaved)), _ptr(q_norm), _ptr(k_norm),
+                            float(eps), _ptr(block_tables), block_tables.shape[1],
+                            block_tables.shape[0], _ptr(token_seq), _ptr(token_pos), n_tok,
+                            _ptr(q_out), _ptr(k_cache), _ptr(v_cache), nb, B, Hq, H, D, code,
+                            float(k_scale), float(v_scale), _ptr(slot_mapping), _ptr(err),
+                            _stream()), "pa_append_rope")
+    return q_out
+
+
+def pa_cache_write_fp4(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, err=None):
+    """Quantize k[n], v[n] ([n_tok, H_kv, D], float16 / bfloat16) to E2M1 codes
+    with an E4M3 scale per 16 head_dim values (value = code * scale16 * scale)
+    at pool slot slot_mapping[n] of the 4-bit pools (pa_fp4_pool_shape)."""
+    L = _lib.load()
+    nb, B, H, D = _fp4_pools(k_cache, v_cache)
+    _cuda(k, "k")
+    _cuda(v, "v")
+    _cuda(slot_mapping, "slot_mapping")
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    n_tok = slot_mapping.numel()
+    if k.shape != (n_tok, H, D) or v.shape != (n_tok, H, D) or k.dtype != v.dtype:
+        raise ValueError("k, v must be [num_tokens, H_kv, D] of one dtype")
+    _here(k, v, slot_mapping, k_cache, v_cache, _err_word(err))
+    _check(L.pa_cache_write_fp4(_ptr(k), _ptr(v), _dtype_code(k), _ptr(slot_mapping), n_tok,
+                                _ptr(k_cache), _ptr(v_cache), nb, B, H, D, float(k_scale),
+                                float(v_scale), _ptr(err), _stream()), "pa_cache_write_fp4")
+
+
+def pa_cache_write_fp4_mapped(k, v, block_tables, token_seq, token_pos, k_cache, v_cache,
+                              k_scale, v_scale, slot_mapping=None, err=None):
+    """Slot mapping and pa_cache_write_fp4 in one launch: new token n goes to
+    slot block_tables[seq][pos // B] * B + pos % B; the int64 slots go to
+    slot_mapping when given.  Tokens of sequence -1 are padding (slot -1)."""
+    L = _lib.load()
+    nb, B, H, D = _fp4_pools(k_cache, v_cache)
+    _i32(block_tables, "block_tables")
+    _i32(token_seq, "token_seq")
+    _i32(token_pos, "token_pos")
+    _cuda(k, "k")
+    _cuda(v, "v")
+    n_tok = token_seq.numel()
+    if token_pos.numel() != n_tok:
+        raise ValueError("token_seq and token_pos differ in length")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, stride]")
+    if k.shape != (n_tok, H, D) or v.shape != (n_tok, H, D) or k.dtype != v.dtype:
+        raise ValueError("k, v must be [num_tokens, H_kv, D] of one dtype")
+    _slots_out(slot_mapping, n_tok)
+    _here(k, v, block_tables, token_seq, token_pos, k_cache, v_cache, slot_mapping, _err_word(err))
+    _check(L.pa_cache_write_fp4_mapped(_ptr(k), _ptr(v), _dtype_code(k), _ptr(block_tables),
+                                       block_tables.shape[1], block_tables.shape[0],
+                                       _ptr(token_seq), _ptr(token_pos), n_tok, _ptr(k_cache),
+                                       _ptr(v_cache), nb, B, H, D, float(k_scale), float(v_scale),
+                                       _ptr(slot_mapping), _ptr(err), _stream()),
+           "pa_cache_write_fp4_mapped")
+    return slot_mapping
+
+
+def pa_cache_read_fp4(slot_mapping, k_cache, v_cache, k_scale, v_scale, dtype=torch.bfloat16,
+                      k_out=None, v_out=None, err=None):
+    """The rows at pool slots slot_mapping[n] of 4-bit pools as 16-bit values
+    (k, v), each [n, H_kv, D].  Rows of negative slots keep what the outputs
+    held (zeros when the outputs are made here)."""
+    L = _lib.load()
+    nb, B, H, D = _fp4_pools(k_cache, v_cache)
+    _cuda(slot_mapping, "slot_mapping")
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    n_tok = slot_mapping.numel()
+    if (k_out is None) != (v_out is None):
+        raise ValueError("give both of k_out and v_out, or neither")
+    if k_out is None:
+        k_out = torch.zeros((n_tok, H, D), dtype=dtype, device=k_cache.device)
+        v_out = torch.zeros_like(k_out)
+    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
+        _cuda(t, n)
+        if t.shape != (n_tok, H, D) or t.dtype != k_out.dtype:
+            raise ValueError("k_out, v_out must be [n, H_kv, D] of one dtype")
+    _here(slot_mapping, k_cache, v_cache, k_out, v_out, _err_word(err))
+    _check(L.pa_cache_read_fp4(_ptr(slot_mapping), n_tok, _ptr(k_cache), _ptr(v_cache), nb, B, H,
+                               D, float(k_scale), float(v_scale), _ptr(k_out), _ptr(v_out),
+                               _dtype_code(k_out), _ptr(err), _stream()), "pa_cache_read_fp4")
+    return k_out, v_out
+
+
+def pa_decode_fp4(q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v_scale, window=0,
+                  out=None, workspace=None, flags=PA_DECODE_AUTO, num_ctas=0, err=None):
+    """Paged decode over 4-bit pools (value = code * scale16 * scale): out
+    [N, Hq, D] in q's dtype.  window >= 1: the query of position T - 1 attends
+    to tokens [max(0, T - window), T); 0: to all of them."""
+    L = _lib.load()
+    nb, B, H, D = _fp4_pools(k_cache, v_cache)
+    _cuda(q, "q")
+    _i32(block_tables, "block_tables")
+    _i32(seq_lens, "seq_lens")
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError("q must be [N, Hq, D]")
+    N, Hq, _ = q.shape
+    if block_tables.dim() != 2 or block_tables.shape[0] != N or seq_lens.numel() != N:
+        raise ValueError("block_tables must be [N, stride] and seq_lens [N]")
+    code = _dtype_code(q)
+    if out is None:
+        out = torch.empty_like(q)
+    _cuda(out, "out")
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must be [N, Hq, D] of q's dtype")
+    if workspace is None:
+        nbytes = pa_decode_workspace_size(Hq, H, D, B, PA_FP4_E2M1, flags, num_ctas)
+        # zero-filled once; the decode leaves it ready for the next call
+        workspace = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    _cuda(workspace, "workspace")
+    _here(q, k_cache, v_cache, block_tables, seq_lens, out, workspace, _err_word(err))
+    _check(L.pa_decode_fp4(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+                           block_tables.shape[1], _ptr(seq_lens), N, Hq, H, D, B, nb, code,
+                           float(scale), float(k_scale), float(v_scale), int(window), _ptr(out),
+                           _ptr(workspace), workspace.numel() * workspace.element_size(),
+                           int(flags), int(num_ctas), _ptr(err), _stream()), "pa_decode_fp4")
     return out
 
 
