@@ -391,8 +391,8 @@ def test_steps_of_append_and_decode(cuda_device):
     decode, every step against the oracle's decode of the pool's own codes."""
     rng = np.random.default_rng(800)
     Hq, H, D, B, N, nb = 8, 2, 128, 16, 3, 40
-    perm = rng.permutation(nb).astype(np.int32).reshape(N, -1)[:, :12]
-    bt = torch.from_numpy(np.ascontiguousarray(perm)).cuda()
+    perm = rng.permutation(nb)[:12 * N].astype(np.int32).reshape(N, 12)
+    bt = torch.from_numpy(perm).cuda()
     ang = np.arange(200)[:, None] * 1e4 ** (-np.arange(0, D, 2) / D)
     cs = torch.from_numpy(np.concatenate((np.cos(ang), np.sin(ang)), -1).astype(np.float32)).cuda()
     kc, vc = _pools(nb, B, H, D, fill=0x7F)
