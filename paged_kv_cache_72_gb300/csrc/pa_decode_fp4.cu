@@ -50,14 +50,15 @@ namespace pa {
 
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;                 // tokens per tile
 constexpr uint32_t kFull = 0xffffffffu;
-// Weights are exp2(x - max + kShift): binary16 keeps its full precision down
-// to 2^-14, so the shift moves the loss of small weights from 2^-14 to 2^-24
-// of the largest.  It cancels in o / l.
-constexpr float kShift = 10.f;
+// Weights are exp2(x - base) with base = a maximum less kShift, and a new base
+// once they pass exp2(kShift + kLag) = 2^15, inside binary16's range.  binary16
+// keeps its full precision down to 2^-14, so the shift moves the loss of small
+// weights from 2^-14 to 2^-22 of that maximum.  It cancels in o / l.
+constexpr float kShift = 8.f, kLag = 7.f;
 
 struct Args {
   const uint16_t* q;
@@ -107,6 +108,15 @@ __device__ __forceinline__ void ld_stream(const uint8_t* p, uint32_t* r) {
     asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(r[0]) : "l"(p));
 }
 
+// Where a lane's part of a tile lies: for each half of 16 tokens the offset of
+// the plane in its pool (negative: nothing is read) and the row of the lane's
+// token group, for K and for V.  With blocks of at least 16 tokens a half lies
+// in one block, and both are the same for the whole warp (row: the half's).
+struct Place {
+  long long k[2], v[2];
+  int kr[2], vr[2];
+};
+
 // One warp's state over a range of one context's tiles.
 template <int D, bool kBF16, int NH>
 struct Context {
@@ -118,11 +128,12 @@ struct Context {
   uint32_t qb[NH][KS][2];
   float sl[NH][2];                         // score factor of heads 8 nh + 2 tig + e (log2)
   float o[NH][MT][4];
-  float m[NH][2], l[NH][2];
+  float l[NH][4];                          // sums of the weights (rows alike)
+  float base[NH][2];                       // weights are exp2(score - base)
+  float limit;                             // weights above exp2(limit) move the base
   // the tile being loaded: per half of 16 tokens
   uint32_t kw[2][2][KW], ksc[2][KW / 2];
   uint32_t vw[2][4][VW], vsc[2];
-  bool kok[2];
 
   // The G query rows of this KV head as f16 fragments.  A bfloat16 row is
   // brought into binary16's range by a power of two (its largest magnitude
@@ -170,55 +181,36 @@ struct Context {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         sl[nh][e] = scale_log2 * __shfl_sync(kFull, back, 4 * (2 * tig + e));
-        m[nh][e] = -INFINITY;
-        l[nh][e] = 0.f;
+        base[nh][e] = 0.f;
       }
+      l[nh][0] = l[nh][1] = l[nh][2] = l[nh][3] = 0.f;
 #pragma unroll
       for (int i = 0; i < MT; ++i) o[nh][i][0] = o[nh][i][1] = o[nh][i][2] = o[nh][i][3] = 0.f;
     }
+    limit = -INFINITY;
   }
 
-  // K of one tile: plane[hf] is the plane of the block of this lane's token
-  // group gid / 2 of half hf, or null (nothing is read); row[hf] the group's
-  // first row in the block
-  __device__ __forceinline__ void load_k(const uint8_t* const (&plane)[2], const int (&row)[2],
-                                         int B) {
-    const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  // kl: the K pool from this lane's bytes of a group's first row on
+  __device__ __forceinline__ void load_k(const uint8_t* kl, const uint8_t* ksl, const Place& p) {
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      kok[hf] = plane[hf] != nullptr;
-      if (kok[hf]) {
-        const uint8_t* p = plane[hf] + (row[hf] + (gid & 1)) * (D / 2) + tig * (D / 8);
-        ld_stream<D / 8>(p, kw[hf][0]);
-        ld_stream<D / 8>(p + D, kw[hf][1]);
-        // the group's four tokens' scales: D / 64 words, of groups (D/64) tig ..
-        const uint8_t* sp = plane[hf] + B * (D / 2) + row[hf] * (D / 16) + tig * (D / 16);
-        ld_stream<D / 16>(sp, ksc[hf]);
+    for (int hf = 0; hf < 2; ++hf)
+      if (p.k[hf] >= 0) {
+        const uint8_t* c = kl + p.k[hf] + p.kr[hf] * (D / 2);
+        ld_stream<D / 8>(c, kw[hf][0]);
+        ld_stream<D / 8>(c + D, kw[hf][1]);
+        ld_stream<D / 16>(ksl + p.k[hf] + p.kr[hf] * (D / 16), ksc[hf]);
       }
-    }
   }
 
-  // V of one tile: the lane's token group is tig
-  __device__ __forceinline__ void load_v(const uint8_t* const (&plane)[2], const int (&row)[2],
-                                         int B) {
-    const int lane = threadIdx.x & 31, gid = lane >> 2;
+  __device__ __forceinline__ void load_v(const uint8_t* vl, const uint8_t* vsl, const Place& p) {
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      if (plane[hf] != nullptr) {
-        const uint8_t* p = plane[hf] + row[hf] * (D / 2) + gid * (D / 16);
+    for (int hf = 0; hf < 2; ++hf)
+      if (p.v[hf] >= 0) {
+        const uint8_t* c = vl + p.v[hf] + p.vr[hf] * (D / 2);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) ld_stream<D / 16>(p + t * (D / 2), vw[hf][t]);
-        const uint8_t* sp =
-            plane[hf] + B * (D / 2) + row[hf] * (D / 16) + (D == 128 ? gid : gid >> 1) * 4;
-        ld_stream<4>(sp, &vsc[hf]);
-      } else {
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int w = 0; w < VW; ++w) vw[hf][t][w] = 0u;
-        vsc[hf] = 0u;
+        for (int t = 0; t < 4; ++t) ld_stream<D / 16>(c + t * (D / 2), vw[hf][t]);
+        ld_stream<4>(vsl + p.v[hf] + p.vr[hf] * (D / 16), &vsc[hf]);
       }
-    }
   }
 
   // scores of the loaded K
@@ -256,59 +248,62 @@ struct Context {
     }
   }
 
-  // online softmax of the tile's scores; pb: the weights as B fragments
-  // (pl: what their rounding to binary16 left, for binary16 outputs).  ok: the
-  // K of each half was read; tokens [lo, hi) of the tile are attended.
+  // Weights of the tile's scores, exp2(s - base) as B fragments pb (pl: what
+  // their rounding to binary16 left, for binary16 outputs), and their sums.
+  // The base is the largest score less kShift when it is set and stays until a
+  // weight would pass exp2(kShift + kLag), so most tiles need neither the
+  // maximum over lanes nor a rescale of o: one vote says so.
+  // kEdge: tokens outside [lo, hi), or of a half that was not read, get no weight.
+  template <bool kEdge>
   __device__ __forceinline__ void weights(float (&s)[2][NH][4], const bool (&ok)[2], int lo, int hi,
                                           uint32_t (&pb)[2][NH][2], uint32_t (&pl)[2][NH][2]) {
     const int gid = (threadIdx.x & 31) >> 2;
     const int tok = 4 * (gid >> 1) + (gid & 1);
+    float mx[NH][2], top = -INFINITY;
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
-      float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int t = 16 * hf + tok + (e >> 1) * 2;
-          const bool in = ok[hf] && t >= lo && t < hi;
-          s[hf][nh][e] = in ? s[hf][nh][e] * sl[nh][e & 1] : -INFINITY;
-          mx[e & 1] = fmaxf(mx[e & 1], s[hf][nh][e]);
+          s[hf][nh][e] = fmaf(s[hf][nh][e], sl[nh][e & 1], -base[nh][e & 1]);
+          if constexpr (kEdge) {
+            const int t = 16 * hf + tok + (e >> 1) * 2;
+            if (!(ok[hf] && t >= lo && t < hi)) s[hf][nh][e] = -INFINITY;
+          }
         }
-      float alpha[2], base[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], 4));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], 8));
-        mx[e] = fmaxf(mx[e], __shfl_xor_sync(kFull, mx[e], 16));
-        const float mn = fmaxf(m[nh][e], mx[e]);
-        // nothing attended so far: any finite base gives weights of zero
-        base[e] = (mn == -INFINITY ? 0.f : mn) - kShift;
-        alpha[e] = m[nh][e] == mn ? 1.f : ex2_approx(m[nh][e] - mn);
-        m[nh][e] = mn;
+        mx[nh][e] = fmaxf(max3f(s[0][nh][e], s[0][nh][2 + e], s[1][nh][e]), s[1][nh][2 + e]);
       }
-      float sum[2] = {0.f, 0.f};
+      top = max3f(top, mx[nh][0], mx[nh][1]);
+    }
+    if (__any_sync(kFull, top > limit)) {
+      bool set = true;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
+      for (int nh = 0; nh < NH; ++nh) {
+        float alpha[2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float p0 = ex2_approx(s[hf][nh][2 * r] - base[0]);
-          const float p1 = ex2_approx(s[hf][nh][2 * r + 1] - base[1]);
-          const uint32_t pk = pack2<false>(p0, p1);
-          const float2 f = unpack2<false>(pk);
-          if constexpr (kPair) {
-            sum[0] += p0;
-            sum[1] += p1;
-            pl[hf][nh][r] = movmatrix_trans(pack2<false>(p0 - f.x, p1 - f.y));
-          } else {   // the weights that are used
-            sum[0] += f.x;
-            sum[1] += f.y;
+        for (int e = 0; e < 2; ++e) {
+          float x = mx[nh][e];
+          x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+          // without weights so far the base goes anywhere, else only up
+          const bool fresh = l[nh][e] == 0.f;
+          float d = x - kShift;
+          if (x == -INFINITY || (!fresh && d < 0.f)) d = 0.f;
+          set = set && (!fresh || x > -INFINITY);
+          alpha[e] = fresh ? 1.f : ex2_approx(-d);
+          base[nh][e] += d;
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            s[hf][nh][e] -= d;
+            s[hf][nh][2 + e] -= d;
           }
-          pb[hf][nh][r] = movmatrix_trans(pk);
+          l[nh][e] *= alpha[e];
+          l[nh][2 + e] *= alpha[e];
         }
-      l[nh][0] = l[nh][0] * alpha[0] + sum[0];
-      l[nh][1] = l[nh][1] * alpha[1] + sum[1];
-      if (__any_sync(kFull, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
           o[nh][i][0] *= alpha[0];
@@ -317,23 +312,46 @@ struct Context {
           o[nh][i][3] *= alpha[1];
         }
       }
+      limit = __all_sync(kFull, set) ? kShift + kLag : -INFINITY;
     }
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float p0 = ex2_approx(s[hf][nh][2 * r]), p1 = ex2_approx(s[hf][nh][2 * r + 1]);
+          const uint32_t pk = pack2<false>(p0, p1);
+          if constexpr (kPair) {
+            const float2 f = unpack2<false>(pk);
+            pl[hf][nh][r] = movmatrix_trans(pack2<false>(p0 - f.x, p1 - f.y));
+          }
+          pb[hf][nh][r] = movmatrix_trans(pk);
+        }
+        // their sums, by a row of ones: the weights as they are used
+        constexpr uint32_t kOnes = 0x3c003c00u;
+        mma_16816<false>(l[nh], kOnes, kOnes, kOnes, kOnes, pb[hf][nh][0], pb[hf][nh][1]);
+        if constexpr (kPair)
+          mma_16816<false>(l[nh], kOnes, kOnes, kOnes, kOnes, pl[hf][nh][0], pl[hf][nh][1]);
+      }
   }
 
-  // O^T += V^T P^T of the loaded V; tokens [lo, hi) of the tile are attended
-  // (the others' weights are zero, and their scales, which may be NaN codes,
-  // are cleared)
+  // O^T += V^T P^T of the loaded V.  kEdge: tokens outside [lo, hi), or whose
+  // V was not read, have weight zero; their bytes, which may be NaN scales or
+  // an earlier tile's, are cleared.
+  template <bool kEdge>
   __device__ __forceinline__ void values(const uint32_t (&pb)[2][NH][2],
-                                         const uint32_t (&pl)[2][NH][2], int lo, int hi) {
+                                         const uint32_t (&pl)[2][NH][2], const bool (&ok)[2],
+                                         int lo, int hi) {
     const int tig = threadIdx.x & 3;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t sc = vsc[hf];
-      const int t0 = 16 * hf + 4 * tig;
-      if (t0 < lo || t0 + 4 > hi) {
+      if constexpr (kEdge) {
+        const int t0 = 16 * hf + 4 * tig;
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-          if (t0 + b < lo || t0 + b >= hi) sc &= ~(0xffu << (8 * b));
+          if (!ok[hf] || t0 + b < lo || t0 + b >= hi) sc &= ~(0xffu << (8 * b));
       }
       uint32_t s01, s23;
       e4m3x4_to_f16x2x2(sc, s01, s23);
@@ -362,14 +380,6 @@ struct Context {
     }
   }
 
-  __device__ __forceinline__ float total_l(int nh, int e) const {
-    float lt = l[nh][e];
-    lt += __shfl_xor_sync(kFull, lt, 4);
-    lt += __shfl_xor_sync(kFull, lt, 8);
-    lt += __shfl_xor_sync(kFull, lt, 16);
-    return lt;
-  }
-
   // the whole context: its output rows
   __device__ __forceinline__ void write(uint16_t* out, int G, float v_scale) const {
     const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
@@ -377,7 +387,7 @@ struct Context {
     for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float lt = total_l(nh, e);
+        const float lt = l[nh][e];
         const int h = 8 * nh + 2 * tig + e;
         if (h >= G) continue;
         const float mul = lt == 0.f ? 0.f : v_scale / lt;
@@ -401,11 +411,11 @@ struct Context {
     for (int nh = 0; nh < NH; ++nh)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float lt = total_l(nh, e);
+        const float lt = l[nh][e];
         const int h = 8 * nh + 2 * tig + e;
         if (h >= G) continue;
         if (gid == 0) {
-          rec[(size_t)G * D + h] = m[nh][e];
+          rec[(size_t)G * D + h] = lt == 0.f ? -INFINITY : base[nh][e];
           rec[(size_t)G * D + G + h] = lt;
         }
         float4* dst = reinterpret_cast<float4*>(rec + (size_t)h * D + (D / 8) * gid);
@@ -466,8 +476,8 @@ struct Shared {
   Part merge[2];
 };
 
-template <int D, bool kBF16, int NH>
-__global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_fp4_kernel(const Args a) {
+template <int D, bool kBF16, int NH, bool kSmall>
+__global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_fp4_kernel(const Args a) {
   extern __shared__ __align__(16) float slots[];   // [2 * kWarps] records
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -554,6 +564,14 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_fp4_kernel(c
 
     Context<D, kBF16, NH> cx;
     int segments = 0;
+    // this lane's bytes of a token group's rows and scales.  K: tokens (gid & 1)
+    // and (gid & 1) + 2 of group gid / 2; V: all four of group tig.  In large
+    // blocks a half's groups lie at fixed rows from its first.
+    const int gk = kSmall ? 0 : 4 * (gid >> 1), gv = kSmall ? 0 : 4 * tig;
+    const uint8_t* kl = a.kc + (gk + (gid & 1)) * (D / 2) + tig * (D / 8);
+    const uint8_t* ksl = a.kc + B * (D / 2) + gk * (D / 16) + tig * (D / 16);
+    const uint8_t* vl = a.vc + gv * (D / 2) + gid * (D / 16);
+    const uint8_t* vsl = a.vc + B * (D / 2) + gv * (D / 16) + (D == 128 ? gid : gid >> 1) * 4;
     while (g < g_end && i < a.num_seqs) {
       if (g < g_seq) {   // only if seq_lens changes during the call: never walk blind
         set_error(a.err, PA_DEVERR_SEQ_LEN);
@@ -566,10 +584,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_fp4_kernel(c
       const int tile_base = first / kTile;
       const int32_t* row_bt = a.bt + (size_t)i * a.stride;
       int win = -1, ent = -1;   // entries [32 win, 32 win + 32) of the table row, one a lane
-      // the planes and rows of tile k: K by token group gid / 2 of each half, V by group tig
-      const uint8_t *kp[2], *vp[2];
-      int kr[2], vr[2];
-      auto locate = [&](int k) {
+      auto locate = [&](int k, Place& p) {
         const int t0 = (tile_base + k) * kTile;
         const int w = (t0 >> a.log2B) >> 5;
         if (w != win) {
@@ -587,37 +602,48 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_fp4_kernel(c
         }
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const int tk = t0 + 16 * hf + 4 * (gid >> 1), tv = t0 + 16 * hf + 4 * tig;
-          const int bk = __shfl_sync(kFull, ent, (tk >> a.log2B) & 31);
-          const int bv = __shfl_sync(kFull, ent, (tv >> a.log2B) & 31);
-          kr[hf] = tk & (B - 1);
-          vr[hf] = tv & (B - 1);
-          kp[hf] = (bk < 0 || tk >= T || tk + 4 <= first)
-                       ? nullptr
-                       : a.kc + fp4_plane(bk, a.H, h, a.plane);
-          vp[hf] = (bv < 0 || tv >= T || tv + 4 <= first)
-                       ? nullptr
-                       : a.vc + fp4_plane(bv, a.H, h, a.plane);
+          if constexpr (kSmall) {
+            const int tk = t0 + 16 * hf + 4 * (gid >> 1), tv = t0 + 16 * hf + 4 * tig;
+            const int bk = __shfl_sync(kFull, ent, (tk >> a.log2B) & 31);
+            const int bv = __shfl_sync(kFull, ent, (tv >> a.log2B) & 31);
+            p.kr[hf] = tk & (B - 1);
+            p.vr[hf] = tv & (B - 1);
+            p.k[hf] = bk < 0 ? -1 : (long long)fp4_plane(bk, a.H, h, a.plane);
+            p.v[hf] = bv < 0 ? -1 : (long long)fp4_plane(bv, a.H, h, a.plane);
+          } else {
+            const int t = t0 + 16 * hf;
+            const int e = __shfl_sync(kFull, ent, (t >> a.log2B) & 31);
+            p.kr[hf] = p.vr[hf] = t & (B - 1);
+            p.k[hf] = p.v[hf] = e < 0 ? -1 : (long long)fp4_plane(e, a.H, h, a.plane);
+          }
         }
       };
-      locate(ta);
-      cx.load_k(kp, kr, B);
-      cx.load_v(vp, vr, B);
+      Place at;
+      locate(ta, at);
+      cx.load_k(kl, ksl, at);
+      cx.load_v(vl, vsl, at);
       cx.begin(a.q + ((size_t)i * a.Hq + (size_t)h * a.G) * D, a.G, a.scale_log2);
       for (int k = ta; k < tb; ++k) {
         const int t0 = (tile_base + k) * kTile;
         float s[2][NH][4];
         uint32_t pb[2][NH][2], pl[2][NH][2];
-        const bool ok[2] = {cx.kok[0], cx.kok[1]};
+        const bool kok[2] = {at.k[0] >= 0, at.k[1] >= 0}, vok[2] = {at.v[0] >= 0, at.v[1] >= 0};
+        const bool edge = t0 < first || t0 + kTile > T ||
+                          (kSmall ? __any_sync(kFull, !(kok[0] && kok[1])) : !(kok[0] && kok[1]));
         cx.scores(s);
         const bool more = k + 1 < tb;
         if (more) {
-          locate(k + 1);
-          cx.load_k(kp, kr, B);
+          locate(k + 1, at);
+          cx.load_k(kl, ksl, at);
         }
-        cx.weights(s, ok, first - t0, T - t0, pb, pl);
-        cx.values(pb, pl, first - t0, T - t0);
-        if (more) cx.load_v(vp, vr, B);
+        if (edge) {
+          cx.template weights<true>(s, kok, first - t0, T - t0, pb, pl);
+          cx.template values<true>(pb, pl, vok, first - t0, T - t0);
+        } else {
+          cx.template weights<false>(s, kok, 0, kTile, pb, pl);
+          cx.template values<false>(pb, pl, vok, 0, kTile);
+        }
+        if (more) cx.load_v(vl, vsl, at);
       }
       if (ta == 0 && tb == nt) {
         cx.write(a.out + ((size_t)i * a.Hq + (size_t)h * a.G) * D, a.G, a.v_scale);
@@ -716,12 +742,16 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 2 : 1) decode_fp4_kernel(c
 
 typedef void (*Kernel)(const Args);
 
-Kernel pick(int D, bool bf16, bool hi) {
-  if (D == 64)
-    return bf16 ? (hi ? decode_fp4_kernel<64, true, 2> : decode_fp4_kernel<64, true, 1>)
-                : (hi ? decode_fp4_kernel<64, false, 2> : decode_fp4_kernel<64, false, 1>);
-  return bf16 ? (hi ? decode_fp4_kernel<128, true, 2> : decode_fp4_kernel<128, true, 1>)
-              : (hi ? decode_fp4_kernel<128, false, 2> : decode_fp4_kernel<128, false, 1>);
+template <int D, bool kSmall>
+Kernel pick_d(bool bf16, bool hi) {
+  return bf16 ? (hi ? decode_fp4_kernel<D, true, 2, kSmall> : decode_fp4_kernel<D, true, 1, kSmall>)
+              : (hi ? decode_fp4_kernel<D, false, 2, kSmall>
+                    : decode_fp4_kernel<D, false, 1, kSmall>);
+}
+
+Kernel pick(int D, bool bf16, bool hi, bool small) {
+  if (D == 64) return small ? pick_d<64, true>(bf16, hi) : pick_d<64, false>(bf16, hi);
+  return small ? pick_d<128, true>(bf16, hi) : pick_d<128, false>(bf16, hi);
 }
 
 struct Plan {
@@ -733,7 +763,7 @@ struct Plan {
 // Blocks per SM depend on the kernel, the group size and the device: looked up
 // once each, with the kernel's opt-in to its shared memory.
 constexpr int kMaxDevices = 64;
-int g_per_sm[kMaxDevices][2][2][17];   // [device][D == 128][bf16][G], 0 = not yet
+int g_per_sm[kMaxDevices][2][2][2][17];   // [device][D == 128][bf16][B < 16][G], 0 = not yet
 std::mutex g_mu;
 
 int make_plan(int Hq, int H, int D, int B, int q_dtype, int flags, int num_ctas, Plan* p) {
@@ -749,14 +779,14 @@ int make_plan(int Hq, int H, int D, int B, int q_dtype, int flags, int num_ctas,
   if (flags == PA_DECODE_SIMT) return PA_ERR_UNSUPPORTED;
   if (flags != PA_DECODE_AUTO && flags != PA_DECODE_MMA) return PA_ERR_INVALID_ARG;
   const bool bf16 = q_dtype == PA_BF16;
-  p->kern = pick(D, bf16, G > 8);
+  p->kern = pick(D, bf16, G > 8, B < 16);
   p->smem = 2 * kWarps * rec_floats(G, D) * sizeof(float);
   DeviceInfo di;
   if (int rc = current_device_info(&di)) return rc;
   int per_sm;
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    int& c = g_per_sm[di.device][D == 128][bf16][G];
+    int& c = g_per_sm[di.device][D == 128][bf16][B < 16][G];
     if (c == 0) {
       const size_t most = 2 * kWarps * rec_floats(G > 8 ? 16 : 8, D) * sizeof(float);
       int n = 0;
