@@ -53,6 +53,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;                 // tokens per tile
+constexpr int kStages = 2;                // tiles in shared memory per warp
+constexpr int kBlocksPerSm = 4;
 constexpr uint32_t kFull = 0xffffffffu;
 // Weights are exp2(x - base) with base = a maximum less kShift, and a new base
 // once they pass exp2(kShift + kLag) = 2^15, inside binary16's range.  binary16
@@ -95,26 +97,37 @@ __device__ __forceinline__ int num_tiles(int T, const Args& a) {
 }
 
 template <int kBytes>
-__device__ __forceinline__ void ld_stream(const uint8_t* p, uint32_t* r) {
+__device__ __forceinline__ void ld_part(uint32_t addr, uint32_t* r) {
   if constexpr (kBytes == 16)
-    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "l"(p));
+                 : "r"(addr));
   else if constexpr (kBytes == 8)
-    asm volatile("ld.global.nc.L1::no_allocate.v2.b32 {%0, %1}, [%2];"
-                 : "=r"(r[0]), "=r"(r[1])
-                 : "l"(p));
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
   else
-    asm volatile("ld.global.nc.L1::no_allocate.b32 %0, [%1];" : "=r"(r[0]) : "l"(p));
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr));
 }
 
-// Where a lane's part of a tile lies: for each half of 16 tokens the offset of
-// the plane in its pool (negative: nothing is read) and the row of the lane's
-// token group, for K and for V.  With blocks of at least 16 tokens a half lies
-// in one block, and both are the same for the whole warp (row: the half's).
-struct Place {
-  long long k[2], v[2];
-  int kr[2], vr[2];
+// A place in the list of tiles: tile k of head h of sequence i, and that
+// sequence's length and tiles.
+struct Walk {
+  int i, h, k, T, nt;
+
+  __device__ __forceinline__ void load_seq(const Args& a) {
+    T = i < a.num_seqs ? clamp_len(__ldg(a.seq_lens + i), a) : 0;
+    nt = num_tiles(T, a);
+  }
+  // the next tile; past the last sequence nt is 0
+  __device__ __forceinline__ void advance(const Args& a) {
+    if (++k < nt) return;
+    k = 0;
+    if (++h < a.H) return;
+    h = 0;
+    do {
+      ++i;
+      load_seq(a);
+    } while (nt == 0 && i < a.num_seqs);
+  }
 };
 
 // One warp's state over a range of one context's tiles.
@@ -131,9 +144,6 @@ struct Context {
   float l[NH][4];                          // sums of the weights (rows alike)
   float base[NH][2];                       // weights are exp2(score - base)
   float limit;                             // weights above exp2(limit) move the base
-  // the tile being loaded: per half of 16 tokens
-  uint32_t kw[2][2][KW], ksc[2][KW / 2];
-  uint32_t vw[2][4][VW], vsc[2];
 
   // The G query rows of this KV head as f16 fragments.  A bfloat16 row is
   // brought into binary16's range by a power of two (its largest magnitude
@@ -190,47 +200,30 @@ struct Context {
     limit = -INFINITY;
   }
 
-  // kl: the K pool from this lane's bytes of a group's first row on
-  __device__ __forceinline__ void load_k(const uint8_t* kl, const uint8_t* ksl, const Place& p) {
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
-      if (p.k[hf] >= 0) {
-        const uint8_t* c = kl + p.k[hf] + p.kr[hf] * (D / 2);
-        ld_stream<D / 8>(c, kw[hf][0]);
-        ld_stream<D / 8>(c + D, kw[hf][1]);
-        ld_stream<D / 16>(ksl + p.k[hf] + p.kr[hf] * (D / 16), ksc[hf]);
-      }
-  }
-
-  __device__ __forceinline__ void load_v(const uint8_t* vl, const uint8_t* vsl, const Place& p) {
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf)
-      if (p.v[hf] >= 0) {
-        const uint8_t* c = vl + p.v[hf] + p.vr[hf] * (D / 2);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) ld_stream<D / 16>(c + t * (D / 2), vw[hf][t]);
-        ld_stream<4>(vsl + p.v[hf] + p.vr[hf] * (D / 16), &vsc[hf]);
-      }
-  }
-
-  // scores of the loaded K
-  __device__ __forceinline__ void scores(float (&s)[2][NH][4]) {
+  // scores of a tile: kc[hf] is the shared address of this lane's codes of half
+  // hf (its first row; the second lies D bytes on), ks[hf] of its scale words
+  __device__ __forceinline__ void scores(float (&s)[2][NH][4], const uint32_t (&kc)[2],
+                                         const uint32_t (&ks)[2]) {
     const int gid = (threadIdx.x & 31) >> 2;
     // bytes e and e + 2 of the lane's scale words: its tokens (rows gid, gid + 8)
     const uint32_t sel = (gid & 1) ? 0x7351u : 0x6240u;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
+      uint32_t kw[2][KW], ksc[KW / 2];
+      ld_part<D / 8>(kc[hf], kw[0]);
+      ld_part<D / 8>(kc[hf] + D, kw[1]);
+      ld_part<D / 16>(ks[hf], ksc);
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh)
         s[hf][nh][0] = s[hf][nh][1] = s[hf][nh][2] = s[hf][nh][3] = 0.f;
       // f16 scale pairs: sa = row gid's groups, sb = row gid + 8's
       uint32_t sa, sb;
-      e4m3x4_to_f16x2x2(prmt(ksc[hf][0], ksc[hf][KW / 2 - 1], sel), sa, sb);
+      e4m3x4_to_f16x2x2(prmt(ksc[0], ksc[KW / 2 - 1], sel), sa, sb);
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
         uint32_t a[4], b[4];
-        e2m1x8_to_f16x2(kw[hf][0][w], a);
-        e2m1x8_to_f16x2(kw[hf][1][w], b);
+        e2m1x8_to_f16x2(kw[0][w], a);
+        e2m1x8_to_f16x2(kw[1][w], b);
         const uint32_t dup = w < 2 ? 0x1010u : 0x3232u;   // 16 codes are two words
         const uint32_t s0 = prmt(sa, sa, dup), s1 = prmt(sb, sb, dup);
 #pragma unroll
@@ -253,9 +246,9 @@ struct Context {
   // The base is the largest score less kShift when it is set and stays until a
   // weight would pass exp2(kShift + kLag), so most tiles need neither the
   // maximum over lanes nor a rescale of o: one vote says so.
-  // kEdge: tokens outside [lo, hi), or of a half that was not read, get no weight.
+  // kEdge: only the tokens of `live` (a bit each) get a weight.
   template <bool kEdge>
-  __device__ __forceinline__ void weights(float (&s)[2][NH][4], const bool (&ok)[2], int lo, int hi,
+  __device__ __forceinline__ void weights(float (&s)[2][NH][4], uint32_t live,
                                           uint32_t (&pb)[2][NH][2], uint32_t (&pl)[2][NH][2]) {
     const int gid = (threadIdx.x & 31) >> 2;
     const int tok = 4 * (gid >> 1) + (gid & 1);
@@ -269,7 +262,7 @@ struct Context {
           s[hf][nh][e] = fmaf(s[hf][nh][e], sl[nh][e & 1], -base[nh][e & 1]);
           if constexpr (kEdge) {
             const int t = 16 * hf + tok + (e >> 1) * 2;
-            if (!(ok[hf] && t >= lo && t < hi)) s[hf][nh][e] = -INFINITY;
+            if (!((live >> t) & 1u)) s[hf][nh][e] = -INFINITY;
           }
         }
 #pragma unroll
@@ -336,28 +329,31 @@ struct Context {
       }
   }
 
-  // O^T += V^T P^T of the loaded V.  kEdge: tokens outside [lo, hi), or whose
-  // V was not read, have weight zero; their bytes, which may be NaN scales or
-  // an earlier tile's, are cleared.
+  // O^T += V^T P^T of a tile: vc[hf] is the shared address of this lane's codes
+  // of the first of its four rows, D / 2 bytes apart, vs[hf] of their scales.
+  // kEdge: the scales of tokens outside `live`, which have weight zero, are
+  // cleared: they may be NaN codes.
   template <bool kEdge>
   __device__ __forceinline__ void values(const uint32_t (&pb)[2][NH][2],
-                                         const uint32_t (&pl)[2][NH][2], const bool (&ok)[2],
-                                         int lo, int hi) {
+                                         const uint32_t (&pl)[2][NH][2], uint32_t live,
+                                         const uint32_t (&vc)[2], const uint32_t (&vs)[2]) {
     const int tig = threadIdx.x & 3;
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
-      uint32_t sc = vsc[hf];
+      uint32_t vw[4][VW], sc[1];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) ld_part<D / 16>(vc[hf] + t * (D / 2), vw[t]);
+      ld_part<4>(vs[hf], sc);
       if constexpr (kEdge) {
-        const int t0 = 16 * hf + 4 * tig;
 #pragma unroll
         for (int b = 0; b < 4; ++b)
-          if (!ok[hf] || t0 + b < lo || t0 + b >= hi) sc &= ~(0xffu << (8 * b));
+          if (!((live >> (16 * hf + 4 * tig + b)) & 1u)) sc[0] &= ~(0xffu << (8 * b));
       }
       uint32_t s01, s23;
-      e4m3x4_to_f16x2x2(sc, s01, s23);
+      e4m3x4_to_f16x2x2(sc[0], s01, s23);
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
-        const uint32_t v0 = vw[hf][0][w], v1 = vw[hf][1][w], v2 = vw[hf][2][w], v3 = vw[hf][3][w];
+        const uint32_t v0 = vw[0][w], v1 = vw[1][w], v2 = vw[2][w], v3 = vw[3][w];
         constexpr uint32_t kLow = 0x0f0f0f0fu;
         // bytes of two tokens' codes of one head_dim: even and odd elements
         uint32_t a0[4], a1[4], a2[4], a3[4];
@@ -464,26 +460,37 @@ struct Part {
   long long g0;       // index of the context's first tile
   int nt;             // its tiles
   int begins, ends;   // the part starts / ends with the context
+  int rec;            // its record, in floats from the start of shared memory
 };
 
 struct Shared {
   long long run_pref[kThreads];   // tiles (of one head) before each thread's run of sequences
   long long warp_tot[kWarps];
   Part part[2 * kWarps];
+  unsigned long long full[kWarps][kStages];   // a stage's copies have landed
+  uint32_t bad[kWarps][kStages];              // its blocks without a valid table entry
   int group_first[2 * kWarps + 1];
   int groups;
   int merges;                     // contexts this block owes the merge of
   Part merge[2];
 };
 
-template <int D, bool kBF16, int NH, bool kSmall>
-__global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_fp4_kernel(const Args a) {
-  extern __shared__ __align__(16) float slots[];   // [2 * kWarps] records
+template <int D, bool kBF16, int NH>
+__global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
+    decode_fp4_kernel(const Args a) {
+  // per warp kStages tiles of K and V; after the last tile: [2 * kWarps] records
+  extern __shared__ __align__(128) uint8_t dyn[];
   __shared__ Shared sh;
+  constexpr int kRow = fp4_row_bytes(D), kPart = kTile * kRow, kStage = 2 * kPart;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, tig = lane & 3;
   const int B = 1 << a.log2B;
   const size_t rf = rec_floats(a.G, D);
+  float* const slots = reinterpret_cast<float*>(dyn);
+  if (lane == 0) {
+    for (int st = 0; st < kStages; ++st) mbar_init(smem_u32(&sh.full[warp][st]), 1);
+    fence_barrier_init();
+  }
 
   if (!a.early_tables) grid_dep_wait();
   // ---- every thread counts the tiles of a run of sequences -----------------
@@ -545,124 +552,168 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_fp4_kernel(c
 #pragma unroll
     for (int b = kThreads / 2; b > 0; b >>= 1)
       if (sh.run_pref[r + b] * a.H <= g) r += b;
-    int i = r * per;
-    long long g_seq = sh.run_pref[r] * a.H;   // first tile of sequence i
-    int T = 0, nt = 0;
-    auto load_seq = [&]() {
-      T = i < a.num_seqs ? clamp_len(__ldg(a.seq_lens + i), a) : 0;
-      nt = num_tiles(T, a);
-    };
-    load_seq();
-    auto skip_to = [&]() {   // the sequence that holds tile g
-      while (i < a.num_seqs && g >= g_seq + (long long)nt * a.H) {
-        g_seq += (long long)nt * a.H;
-        ++i;
-        load_seq();
+    Walk w;   // the tile being computed
+    w.i = r * per;
+    w.load_seq(a);
+    long long rem = g - sh.run_pref[r] * a.H;
+    while (w.i < a.num_seqs && rem >= (long long)w.nt * a.H) {
+      rem -= (long long)w.nt * a.H;
+      ++w.i;
+      w.load_seq(a);
+    }
+    const bool sound = w.i < a.num_seqs && rem >= 0;
+    w.h = sound ? (int)(rem / w.nt) : 0;
+    w.k = sound ? (int)(rem % w.nt) : 0;
+    // only if seq_lens changes during the call: never walk blind
+    if (!sound) set_error(a.err, PA_DEVERR_SEQ_LEN);
+    const int n_tiles = sound ? (int)(g_end - g) : 0;
+
+    // ---- the copies: K and V of a tile into stage n % kStages --------------
+    // A block of up to 32 tokens is copied whole, plane by plane; of a larger
+    // one the tile's rows of codes and of scales.  Lanes 0..7 copy K's pieces,
+    // 8..15 V's.  In shared memory a tile is a plane of min(B, 32) tokens, or
+    // several.
+    const uint32_t ring = smem_u32(dyn) + (uint32_t)(warp * kStages * kStage);
+    const uint32_t full = smem_u32(&sh.full[warp][0]);
+    Walk ld = w;
+    int win_i = -1, win = -1, ent = -1;   // entries [32 win, 32 win + 32) of sequence win_i's row
+    const int piece = lane & 7;
+    const bool large = B > kTile;
+    const int bs = large ? kTile : B;
+    auto issue = [&](int st) {
+      const int first = first_token(ld.T, a);
+      const int t0 = (first / kTile + ld.k) * kTile;
+      const int wn = (t0 >> a.log2B) >> 5;
+      if (wn != win || ld.i != win_i) {
+        win = wn;
+        win_i = ld.i;
+        const int idx = 32 * wn + lane;
+        ent = -2;   // no entry
+        // entries of blocks that hold an attended token
+        if (idx >= (first >> a.log2B) && idx <= ((ld.T - 1) >> a.log2B)) {
+          ent = __ldg(a.bt + (size_t)ld.i * a.stride + idx);
+          if (ent < 0 || (long long)ent >= a.num_blocks) {
+            set_error(a.err, PA_DEVERR_BLOCK_ID);
+            ent = -1;
+          }
+        }
       }
+      const int blk = (t0 >> a.log2B) + (large ? 0 : piece);
+      int e = __shfl_sync(kFull, ent, blk & 31);
+      const bool mine = lane < 16 && piece < (large ? 2 : kTile / bs);
+      const uint32_t bad = __ballot_sync(kFull, mine && e == -1) & 0xffu;
+      const uint32_t got = __ballot_sync(kFull, mine && e >= 0);
+      if (lane == 0) {
+        sh.bad[warp][st] = bad;
+        mbar_arrive_expect_tx(full + 8 * st, large ? (got ? kStage : 0) : __popc(got) * bs * kRow);
+      }
+      __syncwarp();
+      if (mine && e >= 0) {
+        const uint8_t* src = (lane < 8 ? a.kc : a.vc) + fp4_plane(e, a.H, ld.h, a.plane);
+        uint32_t dst = ring + (uint32_t)(st * kStage + (lane < 8 ? 0 : kPart));
+        uint32_t bytes = (uint32_t)(bs * kRow);
+        if (large) {
+          const int row = t0 & (B - 1);
+          src += piece == 0 ? row * (D / 2) : B * (D / 2) + row * (D / 16);
+          dst += piece == 0 ? 0 : kTile * (D / 2);
+          bytes = piece == 0 ? kTile * (D / 2) : kTile * (D / 16);
+        } else {
+          dst += piece * bytes;
+        }
+        bulk_load(dst, src, bytes, full + 8 * st);
+      }
+      ld.advance(a);
     };
-    skip_to();
+    // this lane's bytes of a tile.  K: rows (gid & 1) and (gid & 1) + 2 of token
+    // group gid / 2 of each half; V: the four of group tig.
+    uint32_t ok[2], os[2], ov[2], ow[2];
+    {
+      const uint32_t pl_bytes = (uint32_t)(bs * kRow);
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int tk = 16 * hf + 4 * (gid >> 1), tv = 16 * hf + 4 * tig;
+        const int rk = tk & (bs - 1), rv = tv & (bs - 1);
+        const uint32_t pk = (uint32_t)(tk / bs) * pl_bytes, pv = (uint32_t)(tv / bs) * pl_bytes;
+        ok[hf] = ring + pk + (rk + (gid & 1)) * (D / 2) + tig * (D / 8);
+        os[hf] = ring + pk + bs * (D / 2) + rk * (D / 16) + tig * (D / 16);
+        ov[hf] = ring + kPart + pv + rv * (D / 2) + gid * (D / 16);
+        ow[hf] = ring + kPart + pv + bs * (D / 2) + rv * (D / 16) + (D == 128 ? gid : gid >> 1) * 4;
+      }
+    }
 
     Context<D, kBF16, NH> cx;
-    int segments = 0;
-    // this lane's bytes of a token group's rows and scales.  K: tokens (gid & 1)
-    // and (gid & 1) + 2 of group gid / 2; V: all four of group tig.  In large
-    // blocks a half's groups lie at fixed rows from its first.
-    const int gk = kSmall ? 0 : 4 * (gid >> 1), gv = kSmall ? 0 : 4 * tig;
-    const uint8_t* kl = a.kc + (gk + (gid & 1)) * (D / 2) + tig * (D / 8);
-    const uint8_t* ksl = a.kc + B * (D / 2) + gk * (D / 16) + tig * (D / 16);
-    const uint8_t* vl = a.vc + gv * (D / 2) + gid * (D / 16);
-    const uint8_t* vsl = a.vc + B * (D / 2) + gv * (D / 16) + (D == 128 ? gid : gid >> 1) * 4;
-    while (g < g_end && i < a.num_seqs) {
-      if (g < g_seq) {   // only if seq_lens changes during the call: never walk blind
-        set_error(a.err, PA_DEVERR_SEQ_LEN);
-        break;
+    const int ahead = min(kStages, n_tiles);
+    for (int n = 0; n < ahead; ++n) issue(n);
+    int st = 0, seg_k0 = w.k, segments = 0;
+    uint32_t ph = 0;
+    bool live_warp = true;
+    for (int n = 0; n < n_tiles; ++n) {
+      if (n == 0 || w.k == 0) {
+        seg_k0 = w.k;
+        cx.begin(a.q + ((size_t)w.i * a.Hq + (size_t)w.h * a.G) * D, a.G, a.scale_log2);
       }
-      const int h = (int)((g - g_seq) / nt);
-      const long long g0 = g_seq + (long long)h * nt;
-      const int ta = (int)(g - g0), tb = (int)min((long long)nt, g_end - g0);
-      const int first = first_token(T, a);
-      const int tile_base = first / kTile;
-      const int32_t* row_bt = a.bt + (size_t)i * a.stride;
-      int win = -1, ent = -1;   // entries [32 win, 32 win + 32) of the table row, one a lane
-      auto locate = [&](int k, Place& p) {
-        const int t0 = (tile_base + k) * kTile;
-        const int w = (t0 >> a.log2B) >> 5;
-        if (w != win) {
-          win = w;
-          const int idx = 32 * w + lane;
-          ent = -1;
-          // entries of blocks that hold an attended token
-          if (idx >= (first >> a.log2B) && idx <= ((T - 1) >> a.log2B)) {
-            ent = __ldg(row_bt + idx);
-            if (ent < 0 || (long long)ent >= a.num_blocks) {
-              set_error(a.err, PA_DEVERR_BLOCK_ID);
-              ent = -1;
-            }
-          }
-        }
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          if constexpr (kSmall) {
-            const int tk = t0 + 16 * hf + 4 * (gid >> 1), tv = t0 + 16 * hf + 4 * tig;
-            const int bk = __shfl_sync(kFull, ent, (tk >> a.log2B) & 31);
-            const int bv = __shfl_sync(kFull, ent, (tv >> a.log2B) & 31);
-            p.kr[hf] = tk & (B - 1);
-            p.vr[hf] = tv & (B - 1);
-            p.k[hf] = bk < 0 ? -1 : (long long)fp4_plane(bk, a.H, h, a.plane);
-            p.v[hf] = bv < 0 ? -1 : (long long)fp4_plane(bv, a.H, h, a.plane);
-          } else {
-            const int t = t0 + 16 * hf;
-            const int e = __shfl_sync(kFull, ent, (t >> a.log2B) & 31);
-            p.kr[hf] = p.vr[hf] = t & (B - 1);
-            p.k[hf] = p.v[hf] = e < 0 ? -1 : (long long)fp4_plane(e, a.H, h, a.plane);
-          }
-        }
-      };
-      Place at;
-      locate(ta, at);
-      cx.load_k(kl, ksl, at);
-      cx.load_v(vl, vsl, at);
-      cx.begin(a.q + ((size_t)i * a.Hq + (size_t)h * a.G) * D, a.G, a.scale_log2);
-      for (int k = ta; k < tb; ++k) {
-        const int t0 = (tile_base + k) * kTile;
+      if (live_warp && __any_sync(kFull, !mbar_wait_bounded(full + 8 * st, ph, nullptr))) {
+        if (lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
+        live_warp = false;   // copies may be in flight: nothing more is issued or read
+      }
+      if (live_warp) {
+        const uint32_t so = (uint32_t)(st * kStage);
+        const int first = first_token(w.T, a);
+        const int t0 = (first / kTile + w.k) * kTile;
+        const uint32_t bad = sh.bad[warp][st];
+        const bool edge = t0 < first || t0 + kTile > w.T || bad != 0u;
         float s[2][NH][4];
         uint32_t pb[2][NH][2], pl[2][NH][2];
-        const bool kok[2] = {at.k[0] >= 0, at.k[1] >= 0}, vok[2] = {at.v[0] >= 0, at.v[1] >= 0};
-        const bool edge = t0 < first || t0 + kTile > T ||
-                          (kSmall ? __any_sync(kFull, !(kok[0] && kok[1])) : !(kok[0] && kok[1]));
-        cx.scores(s);
-        const bool more = k + 1 < tb;
-        if (more) {
-          locate(k + 1, at);
-          cx.load_k(kl, ksl, at);
-        }
+        const uint32_t kc[2] = {ok[0] + so, ok[1] + so}, ks[2] = {os[0] + so, os[1] + so};
+        const uint32_t vc[2] = {ov[0] + so, ov[1] + so}, vs[2] = {ow[0] + so, ow[1] + so};
+        cx.scores(s, kc, ks);
         if (edge) {
-          cx.template weights<true>(s, kok, first - t0, T - t0, pb, pl);
-          cx.template values<true>(pb, pl, vok, first - t0, T - t0);
+          uint32_t live = kFull;
+          if (t0 < first) live &= kFull << (first - t0);
+          if (t0 + kTile > w.T) live &= kFull >> (t0 + kTile - w.T);
+          if (bad)
+            for (int b = 0; b < kTile / bs; ++b)
+              if ((bad >> b) & 1u) live &= ~((bs == 32 ? kFull : (1u << bs) - 1u) << (b * bs));
+          cx.template weights<true>(s, live, pb, pl);
+          cx.template values<true>(pb, pl, live, vc, vs);
         } else {
-          cx.template weights<false>(s, kok, 0, kTile, pb, pl);
-          cx.template values<false>(pb, pl, vok, 0, kTile);
+          cx.template weights<false>(s, kFull, pb, pl);
+          cx.template values<false>(pb, pl, kFull, vc, vs);
         }
-        if (more) cx.load_v(vl, vsl, at);
+        __syncwarp();   // every lane has read the stage
+        if (n + kStages < n_tiles) issue(st);
       }
-      if (ta == 0 && tb == nt) {
-        cx.write(a.out + ((size_t)i * a.Hq + (size_t)h * a.G) * D, a.G, a.v_scale);
-      } else {
-        const int k = 2 * warp + (segments > 0 ? 1 : 0);
-        cx.store(slots + (size_t)k * rf, a.G);
-        if (lane == 0) {
-          Part& p = sh.part[k];
-          p.pair = (long long)i * a.H + h;
-          p.g0 = g0;
-          p.nt = nt;
-          p.begins = ta == 0;
-          p.ends = tb == nt;
+      if (n == n_tiles - 1 || w.k == w.nt - 1) {
+        // the end of the context, or of this warp's part of it.  The warp's last
+        // part goes where its tiles were, an earlier one to the warp's slot.
+        if (seg_k0 == 0 && w.k == w.nt - 1) {
+          cx.write(a.out + ((size_t)w.i * a.Hq + (size_t)w.h * a.G) * D, a.G, a.v_scale);
+        } else {
+          const int rec = n == n_tiles - 1
+                              ? warp * (kStages * kStage / 4)
+                              : kWarps * (kStages * kStage / 4) + warp * (int)rf;
+          if (live_warp) cx.store(slots + rec, a.G);
+          if (lane == 0) {
+            Part& p = sh.part[2 * warp + (segments > 0 ? 1 : 0)];
+            p.pair = (long long)w.i * a.H + w.h;
+            p.g0 = g + n - w.k;
+            p.nt = w.nt;
+            p.begins = seg_k0 == 0;
+            p.ends = w.k == w.nt - 1;
+            p.rec = rec;
+          }
         }
+        ++segments;
       }
-      ++segments;
-      g = g0 + tb;
-      skip_to();
+      if (++st == kStages) {
+        st = 0;
+        ph ^= 1u;
+      }
+      w.advance(a);
     }
+    if (!live_warp)   // leave with no copy in flight
+      for (int k = 0; k < kStages; ++k)
+        mbar_wait_bounded(full + 8 * k, k < st ? ph ^ 1u : ph, nullptr);
   }
   __syncthreads();
 
@@ -689,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_fp4_kernel(c
     for (int k = k0; k < k1; ++k) {
       if (sh.part[k].pair < 0) continue;
       k_last = k;
-      x.fold_record(slots + (size_t)k * rf, a.G, D, r, c);
+      x.fold_record(slots + sh.part[k].rec, a.G, D, r, c);
     }
     const long long pair = sh.part[k0].pair;
     if (sh.part[k0].begins && sh.part[k_last].ends) {
@@ -742,17 +793,25 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? 3 : 2) decode_fp4_kernel(c
 
 typedef void (*Kernel)(const Args);
 
-template <int D, bool kSmall>
+template <int D>
 Kernel pick_d(bool bf16, bool hi) {
-  return bf16 ? (hi ? decode_fp4_kernel<D, true, 2, kSmall> : decode_fp4_kernel<D, true, 1, kSmall>)
-              : (hi ? decode_fp4_kernel<D, false, 2, kSmall>
-                    : decode_fp4_kernel<D, false, 1, kSmall>);
+  return bf16 ? (hi ? decode_fp4_kernel<D, true, 2> : decode_fp4_kernel<D, true, 1>)
+              : (hi ? decode_fp4_kernel<D, false, 2> : decode_fp4_kernel<D, false, 1>);
 }
 
-Kernel pick(int D, bool bf16, bool hi, bool small) {
-  if (D == 64) return small ? pick_d<64, true>(bf16, hi) : pick_d<64, false>(bf16, hi);
-  return small ? pick_d<128, true>(bf16, hi) : pick_d<128, false>(bf16, hi);
+Kernel pick(int D, bool bf16, bool hi) {
+  return D == 64 ? pick_d<64>(bf16, hi) : pick_d<128>(bf16, hi);
 }
+
+// the ring of every warp (which its last part's record shares) and a slot each
+// for an earlier part
+size_t smem_bytes(int D, int G) {
+  return (size_t)kWarps * kStages * 2 * kTile * fp4_row_bytes(D) +
+         kWarps * rec_floats(G, D) * sizeof(float);
+}
+static_assert(rec_floats(16, 128) * 4 <= kStages * 2 * kTile * fp4_row_bytes(128) &&
+                  rec_floats(16, 64) * 4 <= kStages * 2 * kTile * fp4_row_bytes(64),
+              "a record fits in a warp's ring");
 
 struct Plan {
   Kernel kern;
@@ -763,7 +822,7 @@ struct Plan {
 // Blocks per SM depend on the kernel, the group size and the device: looked up
 // once each, with the kernel's opt-in to its shared memory.
 constexpr int kMaxDevices = 64;
-int g_per_sm[kMaxDevices][2][2][2][17];   // [device][D == 128][bf16][B < 16][G], 0 = not yet
+int g_per_sm[kMaxDevices][2][2][17];   // [device][D == 128][bf16][G], 0 = not yet
 std::mutex g_mu;
 
 int make_plan(int Hq, int H, int D, int B, int q_dtype, int flags, int num_ctas, Plan* p) {
@@ -779,16 +838,16 @@ int make_plan(int Hq, int H, int D, int B, int q_dtype, int flags, int num_ctas,
   if (flags == PA_DECODE_SIMT) return PA_ERR_UNSUPPORTED;
   if (flags != PA_DECODE_AUTO && flags != PA_DECODE_MMA) return PA_ERR_INVALID_ARG;
   const bool bf16 = q_dtype == PA_BF16;
-  p->kern = pick(D, bf16, G > 8, B < 16);
-  p->smem = 2 * kWarps * rec_floats(G, D) * sizeof(float);
+  p->kern = pick(D, bf16, G > 8);
+  p->smem = smem_bytes(D, G);
   DeviceInfo di;
   if (int rc = current_device_info(&di)) return rc;
   int per_sm;
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    int& c = g_per_sm[di.device][D == 128][bf16][B < 16][G];
+    int& c = g_per_sm[di.device][D == 128][bf16][G];
     if (c == 0) {
-      const size_t most = 2 * kWarps * rec_floats(G > 8 ? 16 : 8, D) * sizeof(float);
+      const size_t most = smem_bytes(D, G > 8 ? 16 : 8);
       int n = 0;
       cudaError_t e = cudaFuncSetAttribute(p->kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                            (int)most);
