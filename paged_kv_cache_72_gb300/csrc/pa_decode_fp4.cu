@@ -54,7 +54,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;                 // tokens per tile
 constexpr int kStages = 2;                // tiles in shared memory per warp
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 3;
 constexpr uint32_t kFull = 0xffffffffu;
 // Weights are exp2(x - base) with base = a maximum less kShift, and a new base
 // once they pass exp2(kShift + kLag) = 2^15, inside binary16's range.  binary16
@@ -96,16 +96,19 @@ __device__ __forceinline__ int num_tiles(int T, const Args& a) {
   return (int)(((long long)T + kTile - 1) / kTile) - first_token(T, a) / kTile;
 }
 
-template <int kBytes>
+// kBytes from shared address addr + kOff
+template <int kBytes, int kOff = 0>
 __device__ __forceinline__ void ld_part(uint32_t addr, uint32_t* r) {
   if constexpr (kBytes == 16)
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4 + %5];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr));
+                 : "r"(addr), "n"(kOff));
   else if constexpr (kBytes == 8)
-    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr));
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2 + %3];"
+                 : "=r"(r[0]), "=r"(r[1])
+                 : "r"(addr), "n"(kOff));
   else
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r[0]) : "r"(addr));
+    asm volatile("ld.shared.b32 %0, [%1 + %2];" : "=r"(r[0]) : "r"(addr), "n"(kOff));
 }
 
 // A place in the list of tiles: tile k of head h of sequence i, and that
@@ -211,7 +214,7 @@ struct Context {
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t kw[2][KW], ksc[KW / 2];
       ld_part<D / 8>(kc[hf], kw[0]);
-      ld_part<D / 8>(kc[hf] + D, kw[1]);
+      ld_part<D / 8, D>(kc[hf], kw[1]);
       ld_part<D / 16>(ks[hf], ksc);
 #pragma unroll
       for (int nh = 0; nh < NH; ++nh)
@@ -224,12 +227,10 @@ struct Context {
         uint32_t a[4], b[4];
         e2m1x8_to_f16x2(kw[0][w], a);
         e2m1x8_to_f16x2(kw[1][w], b);
-        const uint32_t dup = w < 2 ? 0x1010u : 0x3232u;   // 16 codes are two words
-        const uint32_t s0 = prmt(sa, sa, dup), s1 = prmt(sb, sb, dup);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = hmul2(a[i], s0);
-          b[i] = hmul2(b[i], s1);
+        for (int i = 0; i < 4; ++i) {   // 16 codes are two words
+          a[i] = w < 2 ? hmul2_lo(a[i], sa) : hmul2_hi(a[i], sa);
+          b[i] = w < 2 ? hmul2_lo(b[i], sb) : hmul2_hi(b[i], sb);
         }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -341,8 +342,10 @@ struct Context {
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf) {
       uint32_t vw[4][VW], sc[1];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) ld_part<D / 16>(vc[hf] + t * (D / 2), vw[t]);
+      ld_part<D / 16>(vc[hf], vw[0]);
+      ld_part<D / 16, D / 2>(vc[hf], vw[1]);
+      ld_part<D / 16, D>(vc[hf], vw[2]);
+      ld_part<D / 16, 3 * D / 2>(vc[hf], vw[3]);
       ld_part<4>(vs[hf], sc);
       if constexpr (kEdge) {
 #pragma unroll
@@ -576,21 +579,35 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
     const uint32_t ring = smem_u32(dyn) + (uint32_t)(warp * kStages * kStage);
     const uint32_t full = smem_u32(&sh.full[warp][0]);
     Walk ld = w;
-    int win_i = -1, win = -1, ent = -1;   // entries [32 win, 32 win + 32) of sequence win_i's row
     const int piece = lane & 7;
     const bool large = B > kTile;
-    const int bs = large ? kTile : B;
+    const int bs = large ? kTile : B, per_tile = large ? 1 : kTile / bs;
+    const int pieces = large ? 2 : per_tile;
+    const bool mine = lane < 16 && piece < pieces;
+    const uint8_t* const pool = lane < 8 ? a.kc : a.vc;
+    const uint32_t bytes = !large ? bs * kRow : (piece == 0 ? kTile * (D / 2) : kTile * (D / 16));
+    const uint32_t dst0 = ring + (lane < 8 ? 0 : kPart) + (large ? piece * (kTile * (D / 2)) : piece * bytes);
+    const long long block_bytes = (long long)a.H * a.plane;
+    int l_first = 0, l_t0 = 0, l_last = 0;   // of the context being loaded
+    int win = -1, ent = -1;                  // entries [32 win, 32 win + 32) of its table row
+    const uint8_t* l_src = nullptr;          // its head's plane in block 0
+    auto load_context = [&]() {
+      l_first = first_token(ld.T, a);
+      l_t0 = (l_first / kTile + ld.k) * kTile;
+      l_last = (ld.T - 1) >> a.log2B;
+      l_src = pool + (size_t)ld.h * a.plane + (large && piece ? B * (D / 2) : 0);
+      win = -1;
+    };
+    load_context();
+    uint32_t odd_stages = 0;   // stages with a block that was not copied
     auto issue = [&](int st) {
-      const int first = first_token(ld.T, a);
-      const int t0 = (first / kTile + ld.k) * kTile;
-      const int wn = (t0 >> a.log2B) >> 5;
-      if (wn != win || ld.i != win_i) {
-        win = wn;
-        win_i = ld.i;
-        const int idx = 32 * wn + lane;
+      const int blk0 = l_t0 >> a.log2B;
+      if ((blk0 >> 5) != win) {
+        win = blk0 >> 5;
+        const int idx = 32 * win + lane;
         ent = -2;   // no entry
         // entries of blocks that hold an attended token
-        if (idx >= (first >> a.log2B) && idx <= ((ld.T - 1) >> a.log2B)) {
+        if (idx >= (l_first >> a.log2B) && idx <= l_last) {
           ent = __ldg(a.bt + (size_t)ld.i * a.stride + idx);
           if (ent < 0 || (long long)ent >= a.num_blocks) {
             set_error(a.err, PA_DEVERR_BLOCK_ID);
@@ -598,31 +615,30 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
           }
         }
       }
-      const int blk = (t0 >> a.log2B) + (large ? 0 : piece);
-      int e = __shfl_sync(kFull, ent, blk & 31);
-      const bool mine = lane < 16 && piece < (large ? 2 : kTile / bs);
-      const uint32_t bad = __ballot_sync(kFull, mine && e == -1) & 0xffu;
-      const uint32_t got = __ballot_sync(kFull, mine && e >= 0);
-      if (lane == 0) {
-        sh.bad[warp][st] = bad;
-        mbar_arrive_expect_tx(full + 8 * st, large ? (got ? kStage : 0) : __popc(got) * bs * kRow);
+      const int e = __shfl_sync(kFull, ent, (blk0 + (large ? 0 : piece)) & 31);
+      const bool copy = mine && e >= 0;
+      uint32_t total = kStage;
+      odd_stages &= ~(1u << st);
+      if (__any_sync(kFull, mine && e < 0)) {
+        total = __popc(__ballot_sync(kFull, copy)) * bytes;
+        if (large) total = 0;   // one block: all pieces or none
+        const uint32_t bad = __ballot_sync(kFull, mine && e == -1) & 0xffu;
+        if (lane == 0) sh.bad[warp][st] = bad;
+        odd_stages |= 1u << st;
       }
+      if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, total);
       __syncwarp();
-      if (mine && e >= 0) {
-        const uint8_t* src = (lane < 8 ? a.kc : a.vc) + fp4_plane(e, a.H, ld.h, a.plane);
-        uint32_t dst = ring + (uint32_t)(st * kStage + (lane < 8 ? 0 : kPart));
-        uint32_t bytes = (uint32_t)(bs * kRow);
-        if (large) {
-          const int row = t0 & (B - 1);
-          src += piece == 0 ? row * (D / 2) : B * (D / 2) + row * (D / 16);
-          dst += piece == 0 ? 0 : kTile * (D / 2);
-          bytes = piece == 0 ? kTile * (D / 2) : kTile * (D / 16);
-        } else {
-          dst += piece * bytes;
-        }
-        bulk_load(dst, src, bytes, full + 8 * st);
+      if (copy) {
+        const uint8_t* src = l_src + e * block_bytes;
+        if (large) src += (l_t0 & (B - 1)) * (piece == 0 ? D / 2 : D / 16);
+        bulk_load(dst0 + st * kStage, src, bytes, full + 8 * st);
       }
-      ld.advance(a);
+      l_t0 += kTile;
+      if (++ld.k == ld.nt) {
+        --ld.k;
+        ld.advance(a);
+        if (ld.nt > 0) load_context();
+      }
     };
     // this lane's bytes of a tile.  K: rows (gid & 1) and (gid & 1) + 2 of token
     // group gid / 2 of each half; V: the four of group tig.
@@ -645,11 +661,14 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
     const int ahead = min(kStages, n_tiles);
     for (int n = 0; n < ahead; ++n) issue(n);
     int st = 0, seg_k0 = w.k, segments = 0;
+    int first = 0, t0 = 0;   // of the tile's context and tile
     uint32_t ph = 0;
     bool live_warp = true;
     for (int n = 0; n < n_tiles; ++n) {
       if (n == 0 || w.k == 0) {
         seg_k0 = w.k;
+        first = first_token(w.T, a);
+        t0 = (first / kTile + w.k) * kTile;
         cx.begin(a.q + ((size_t)w.i * a.Hq + (size_t)w.h * a.G) * D, a.G, a.scale_log2);
       }
       if (live_warp && __any_sync(kFull, !mbar_wait_bounded(full + 8 * st, ph, nullptr))) {
@@ -658,9 +677,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
       }
       if (live_warp) {
         const uint32_t so = (uint32_t)(st * kStage);
-        const int first = first_token(w.T, a);
-        const int t0 = (first / kTile + w.k) * kTile;
-        const uint32_t bad = sh.bad[warp][st];
+        const uint32_t bad = (odd_stages >> st) & 1u ? sh.bad[warp][st] : 0u;
         const bool edge = t0 < first || t0 + kTile > w.T || bad != 0u;
         float s[2][NH][4];
         uint32_t pb[2][NH][2], pl[2][NH][2];
@@ -709,7 +726,11 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
         st = 0;
         ph ^= 1u;
       }
-      w.advance(a);
+      t0 += kTile;
+      if (++w.k == w.nt) {
+        --w.k;
+        w.advance(a);
+      }
     }
     if (!live_warp)   // leave with no copy in flight
       for (int k = 0; k < kStages; ++k)

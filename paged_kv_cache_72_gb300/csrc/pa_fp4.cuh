@@ -54,4 +54,16 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// a times the low / the high half of s in both halves (the multiply selects it)
+__device__ __forceinline__ uint32_t hmul2_lo(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a),
+                            __low2half2(*reinterpret_cast<__half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t hmul2_hi(uint32_t a, uint32_t s) {
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a),
+                            __high2half2(*reinterpret_cast<__half2*>(&s)));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 }  // namespace pa
