@@ -53,15 +53,15 @@ struct AppendArgs {
   int32_t* err;
 };
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;   // of a block of every kernel here
 
 // The slot of token `tok`, or -1 for a token that writes nothing: a padding
 // token (sequence -1, or a negative given slot), or a bad one, which sets an
-// error bit (thread 0 reports).  pos receives its position.
-__device__ __forceinline__ long long append_slot(const AppendArgs& a, long long tok, int& pos) {
-  const bool report = threadIdx.x == 0 && blockIdx.y == 0;
+// error bit (when `report`).  pos receives its position.
+__device__ __forceinline__ long long append_slot(const AppendArgs& a, long long tok, bool report,
+                                                 int& pos) {
   if (a.slots_in) {
-    const long long s = a.slots_in[tok];
+    const long long s = __ldg(a.slots_in + tok);
     pos = 0;
     if (s >= (a.num_blocks << a.log2B)) {
       if (report) set_error(a.err, PA_DEVERR_SLOT);
@@ -69,15 +69,15 @@ __device__ __forceinline__ long long append_slot(const AppendArgs& a, long long 
     }
     return s < 0 ? -1 : s;
   }
-  const int i = a.tok_seq[tok];
-  pos = a.tok_pos[tok];
+  const int i = __ldg(a.tok_seq + tok);
+  pos = __ldg(a.tok_pos + tok);
   if (i == -1) return -1;
   if (i < 0 || i >= a.num_seqs || pos < 0 || (long long)pos >= ((long long)a.stride << a.log2B) ||
       (a.rot > 0 && pos >= a.max_pos)) {
     if (report) set_error(a.err, PA_DEVERR_POSITION);
     return -1;
   }
-  const int p = a.bt[(size_t)i * a.stride + (pos >> a.log2B)];
+  const int p = __ldg(a.bt + (size_t)i * a.stride + (pos >> a.log2B));
   if (p < 0 || (long long)p >= a.num_blocks) {
     if (report) set_error(a.err, PA_DEVERR_BLOCK_ID);
     return -1;
@@ -85,8 +85,211 @@ __device__ __forceinline__ long long append_slot(const AppendArgs& a, long long 
   return ((long long)p << a.log2B) + (pos & ((1 << a.log2B) - 1));
 }
 
-// One block per token (blockIdx.x) and share of its rows (blockIdx.y).  Rows
-// are the Hq query heads, then the H key heads, then the H value heads.
+// x / d rounded to nearest, from r = 1 / d rounded to nearest: one residual
+// step on x r gives the correctly rounded quotient (P. Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990) where
+// nothing under- or overflows: d within 2^+-100; an x so small that its residual
+// is lost is far below the smallest code.
+__device__ __forceinline__ float div_by(float x, float d, float r, bool exact) {
+  if (!exact) return __fdiv_rn(x, d);
+  const float y = __fmul_rn(x, r);
+  return __fmaf_rn(__fmaf_rn(-y, d, x), r, y);
+}
+__device__ __forceinline__ bool plain_divisor(float d) { return d > 0x1p-100f && d < 0x1p100f; }
+
+// Two fp32 values at a time, each rounded as alone.
+struct F2 {
+  float x, y;
+};
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+  F2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 c, a, b;\n\tmov.b64 {%0, %1}, c;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+// scalar: a packed product and a packed sum may be contracted to one fused
+// operation, __fadd_rn never is
+__device__ __forceinline__ F2 add2(F2 a, F2 b) { return {__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)}; }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+template <bool kBF16>
+__device__ __forceinline__ void widen(const uint4& x, F2 (&y)[4]) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<kBF16>(w[i]);
+    y[i].x = f.x;
+    y[i].y = f.y;
+  }
+}
+template <bool kBF16>
+__device__ __forceinline__ uint4 narrow(const F2 (&y)[4]) {
+  return make_uint4(pack2<kBF16>(y[0].x, y[0].y), pack2<kBF16>(y[1].x, y[1].y),
+                    pack2<kBF16>(y[2].x, y[2].y), pack2<kBF16>(y[3].x, y[3].y));
+}
+
+// What a lane needs to turn a position's rows: its 8 elements' cosines, the
+// sines with the sign of their products, and the lane that holds the partners.
+struct Turn {
+  F2 c[4], s[4];
+  int from;        // partner lane
+  bool on, swap;   // this lane's elements turn; partners are neighbours
+
+  __device__ __forceinline__ void load(const AppendArgs& a, int pos, int d0) {
+    const int half = a.rot >> 1, lane = threadIdx.x & 31;
+    on = d0 < a.rot;
+    swap = a.interleaved != 0;
+    from = lane;
+    if (!on) return;
+    const float* cs = a.cos_sin + (size_t)pos * a.rot;
+    if (swap) {
+      const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs + d0 / 2));
+      const float4 s4 = __ldg(reinterpret_cast<const float4*>(cs + half + d0 / 2));
+      c[0] = {c4.x, c4.x}; c[1] = {c4.y, c4.y}; c[2] = {c4.z, c4.z}; c[3] = {c4.w, c4.w};
+      s[0] = {-s4.x, s4.x}; s[1] = {-s4.y, s4.y}; s[2] = {-s4.z, s4.z}; s[3] = {-s4.w, s4.w};
+      return;
+    }
+    const bool first = d0 < half;
+    from = first ? lane + (half >> 3) : lane - (half >> 3);
+    const int i0 = first ? d0 : d0 - half;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs + i0 + 4 * u));
+      float4 s4 = __ldg(reinterpret_cast<const float4*>(cs + half + i0 + 4 * u));
+      if (first) s4 = make_float4(-s4.x, -s4.y, -s4.z, -s4.w);
+      c[2 * u] = {c4.x, c4.y};
+      c[2 * u + 1] = {c4.z, c4.w};
+      s[2 * u] = {s4.x, s4.y};
+      s[2 * u + 1] = {s4.z, s4.w};
+    }
+  }
+
+  // the partner elements of a row whose 16 bytes are x (every lane takes part)
+  template <bool kBF16>
+  __device__ __forceinline__ void partners(const uint4& x, const F2 (&y)[4], F2 (&p)[4]) const {
+    if (swap) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) p[i] = {y[i].y, y[i].x};
+    } else {
+      widen<kBF16>(make_uint4(__shfl_sync(0xffffffffu, x.x, from), __shfl_sync(0xffffffffu, x.y, from),
+                              __shfl_sync(0xffffffffu, x.z, from), __shfl_sync(0xffffffffu, x.w, from)),
+                   p);
+    }
+  }
+};
+
+// One query or key row: norm with the weights g (when given), rotation, one
+// rounding to 16 bits.  Without a norm the products are rounded before they are
+// added, as the header of this file says; with one the weights join the angles
+// (gc = g c, gs = g_partner s), the row is a' = r (x gc + p gs).
+template <int D, bool kBF16, bool kNorm>
+__device__ __forceinline__ uint4 turned(const AppendArgs& a, const uint4& x, const Turn& t,
+                                        const uint16_t* g, const F2 (&gc)[4], const F2 (&gs)[4]) {
+  const bool rotates = a.rot > 0;
+  F2 y[4], p[4];
+  widen<kBF16>(x, y);
+  if (rotates) t.partners<kBF16>(x, y, p);
+  if (kNorm && g) {
+    F2 q = mul2(y[0], y[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) q = fma2(y[i], y[i], q);
+    float ss = q.x + q.y;
+#pragma unroll
+    for (int k = 1; k < D / 8; k <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, k);
+    const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = mul2(y[i], gc[i]);
+      if (rotates && t.on) y[i] = fma2(p[i], gs[i], y[i]);
+      y[i] = mul2(y[i], {r, r});
+    }
+  } else if (rotates && t.on) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = add2(mul2(y[i], t.c[i]), mul2(p[i], t.s[i]));
+  } else {
+    return x;
+  }
+  return narrow<kBF16>(y);
+}
+
+// gc and gs of a norm's weights
+template <bool kBF16>
+__device__ __forceinline__ void join(const uint16_t* g, const Turn& t, bool rotates, int d0,
+                                     F2 (&gc)[4], F2 (&gs)[4]) {
+  const uint4 w = __ldg(reinterpret_cast<const uint4*>(g + d0));
+  F2 p[4];
+  widen<kBF16>(w, gc);
+  if (!rotates) return;
+  t.partners<kBF16>(w, gc, p);
+  if (!t.on) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    gc[i] = mul2(gc[i], t.c[i]);
+    gs[i] = mul2(p[i], t.s[i]);
+  }
+}
+
+// One key or value row into its pool, this lane's 16 bytes x of head h: as it
+// is, as E4M3 codes, or as E2M1 codes whose group of 16 is this lane's 8 values
+// and its neighbour's (every lane takes part).
+template <int D, bool kBF16, int kPool>
+__device__ __forceinline__ void store_row(uint8_t* pool, const uint4& x, long long slot, int H,
+                                          int log2B, int h, float scale, bool in) {
+  const int j = threadIdx.x % (D / 8), d0 = 8 * j;
+  if constexpr (kPool == kPool16) {
+    if (in) *reinterpret_cast<uint4*>(pool + (((size_t)slot * H + h) * D + d0) * 2) = x;
+    return;
+  }
+  F2 z[4];
+  widen<kBF16>(x, z);
+  if constexpr (kPool == kPoolE4M3) {
+    const float rs = __frcp_rn(scale);
+    const bool exact = plain_divisor(scale);
+    uint32_t e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      e[i] = f32x2_to_e4m3x2(div_by(z[i].x, scale, rs, exact), div_by(z[i].y, scale, rs, exact));
+    if (in)
+      *reinterpret_cast<uint2*>(pool + ((size_t)slot * H + h) * D + d0) =
+          make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+  } else if constexpr (kPool == kPoolE2M1) {
+    float m = fmaxf(fabsf(z[0].x), fabsf(z[0].y));
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = max3f(m, fabsf(z[i].x), fabsf(z[i].y));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    const uint32_t s8 = f32x2_to_e4m3x2(__fdiv_rn(m, __fmul_rn(6.f, scale)), 0.f) & 0xffu;
+    const float d = __fmul_rn(unpack2<false>(e4m3x2_to_f16x2(s8)).x, scale);
+    uint32_t code = 0u;
+    if (d > 0.f) {
+      const float rd = __frcp_rn(d);
+      const bool exact = plain_divisor(d);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        code |= f32x2_to_e2m1x2(div_by(z[i].x, d, rd, exact), div_by(z[i].y, d, rd, exact))
+                << (8 * i);
+    }
+    if (in) {
+      const int B = 1 << log2B, row = (int)(slot & (B - 1));
+      uint8_t* plane = pool + fp4_plane(slot >> log2B, H, h, B * fp4_row_bytes(D));
+      *reinterpret_cast<uint32_t*>(plane + row * (D / 2) + 4 * j) = code;
+      if ((j & 1) == 0) plane[fp4_scale_off<D>(B, row, j >> 1)] = (uint8_t)s8;
+    }
+  }
+}
+
+constexpr int kBatch = 4;   // rows a thread group loads before it works on the first
+
+// One block per token (blockIdx.x) and share of its rows (blockIdx.y): query
+// rows, then key rows, then value rows, each D / 8 lanes wide.  The first rows
+// of each kind are loaded before the token's slot is known.
 template <int D, bool kBF16, int kPool, bool kNorm>
 __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   constexpr int LPR = D / 8;               // lanes per row
@@ -94,160 +297,118 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   const long long tok = blockIdx.x;
-  const int j = threadIdx.x % LPR;         // this lane's head_dim 8 j .. 8 j + 7
-  const int d0 = 8 * j;
-  const int rows = a.Hq + 2 * a.H;
+  const int d0 = 8 * (threadIdx.x % LPR);
+  const int r0 = blockIdx.y * RPP + threadIdx.x / LPR, step = gridDim.y * RPP;
+  const uint16_t* const qr = a.q + tok * a.q_stride + d0;
+  const uint16_t* const kr = a.k + tok * a.k_stride + d0;
+  const uint16_t* const vr = a.v + tok * a.v_stride + d0;
+  const uint4 none = make_uint4(0u, 0u, 0u, 0u);
+  uint4 xq[kBatch], xk = none, xv = none;
+#pragma unroll
+  for (int b = 0; b < kBatch; ++b) {
+    const int h = r0 + b * step;
+    xq[b] = h < a.Hq ? *reinterpret_cast<const uint4*>(qr + h * D) : none;
+  }
+  if (r0 < a.H) {
+    xk = *reinterpret_cast<const uint4*>(kr + r0 * D);
+    xv = *reinterpret_cast<const uint4*>(vr + r0 * D);
+  }
   int pos;
-  const long long slot = append_slot(a, tok, pos);
-  if (a.slots && threadIdx.x == 0 && blockIdx.y == 0) a.slots[tok] = slot;
+  const bool lead = threadIdx.x == 0 && blockIdx.y == 0;
+  const long long slot = append_slot(a, tok, lead, pos);
+  if (a.slots && lead) a.slots[tok] = slot;
   if (slot < 0) return;                    // the whole block: every thread found the same slot
-
-  // this lane's angles, the sine with the sign of its own product
-  const int half = a.rot >> 1;
-  const bool turns = d0 < a.rot;
-  float c[8], s[8];
+  Turn t;
+  t.load(a, pos, d0);
+  F2 gc[4], gs[4];
+  // rows in lockstep over the block (the shuffles need every lane)
+  if (kNorm && a.q_norm) join<kBF16>(a.q_norm, t, a.rot > 0, d0, gc, gs);
+  uint16_t* const qo = a.q_out + (size_t)tok * a.Hq * D + d0;
+  for (int first = blockIdx.y * RPP; first < a.Hq; first += kBatch * step) {
+    const int hb = first + threadIdx.x / LPR;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) c[e] = s[e] = 0.f;
-  if (turns) {
-    const float* cs = a.cos_sin + (size_t)pos * a.rot;
-    if (a.interleaved) {
-      const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs + d0 / 2));
-      const float4 s4 = __ldg(reinterpret_cast<const float4*>(cs + half + d0 / 2));
-      c[0] = c[1] = c4.x; c[2] = c[3] = c4.y; c[4] = c[5] = c4.z; c[6] = c[7] = c4.w;
-      s[0] = -s4.x; s[1] = s4.x; s[2] = -s4.y; s[3] = s4.y;
-      s[4] = -s4.z; s[5] = s4.z; s[6] = -s4.w; s[7] = s4.w;
-    } else {
-      const bool first = d0 < half;
-      const int i0 = first ? d0 : d0 - half;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const float4 c4 = __ldg(reinterpret_cast<const float4*>(cs + i0 + 4 * u));
-        const float4 s4 = __ldg(reinterpret_cast<const float4*>(cs + half + i0 + 4 * u));
-        c[4 * u] = c4.x; c[4 * u + 1] = c4.y; c[4 * u + 2] = c4.z; c[4 * u + 3] = c4.w;
-        s[4 * u] = first ? -s4.x : s4.x;
-        s[4 * u + 1] = first ? -s4.y : s4.y;
-        s[4 * u + 2] = first ? -s4.z : s4.z;
-        s[4 * u + 3] = first ? -s4.w : s4.w;
-      }
+    for (int b = 0; b < kBatch; ++b) {
+      if (first + b * step >= a.Hq) break;
+      const int h = hb + b * step;
+      const uint4 o = turned<D, kBF16, kNorm>(a, xq[b], t, a.q_norm, gc, gs);
+      if (h < a.Hq) *reinterpret_cast<uint4*>(qo + h * D) = o;
+      const int next = h + kBatch * step;
+      if (next < a.Hq) xq[b] = *reinterpret_cast<const uint4*>(qr + next * D);
     }
   }
-  // the lane that holds the partner elements (this one when interleaved)
-  const int lane = threadIdx.x & 31;
-  int partner = lane;
-  if (turns && !a.interleaved) partner = d0 < half ? lane + half / 8 : lane - half / 8;
+  if (kNorm && a.k_norm) join<kBF16>(a.k_norm, t, a.rot > 0, d0, gc, gs);
+  for (int first = blockIdx.y * RPP; first < a.H; first += step) {
+    const int h = first + threadIdx.x / LPR;
+    const bool in = h < a.H;
+    const uint4 k = xk, v = xv;
+    if (h + step < a.H) {
+      xk = *reinterpret_cast<const uint4*>(kr + (h + step) * D);
+      xv = *reinterpret_cast<const uint4*>(vr + (h + step) * D);
+    }
+    const uint4 o = turned<D, kBF16, kNorm>(a, k, t, a.k_norm, gc, gs);
+    store_row<D, kBF16, kPool>(a.kc, o, slot, a.H, a.log2B, h, a.k_scale, in);
+    store_row<D, kBF16, kPool>(a.vc, v, slot, a.H, a.log2B, h, a.v_scale, in);
+  }
+}
 
-  const int r0 = blockIdx.y * RPP + threadIdx.x / LPR, step = gridDim.y * RPP;
-  // rows in lockstep over the warp (the shuffles need every lane)
-  const int passes = (rows - (int)(blockIdx.y * RPP) + step - 1) / step;
-  for (int it = 0; it < passes; ++it) {
-    const int r = r0 + it * step;
-    const bool in = r < rows;
-    const int h = r < a.Hq ? r : (r < a.Hq + a.H ? r - a.Hq : r - a.Hq - a.H);
-    const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.H;
-    uint4 x4 = make_uint4(0u, 0u, 0u, 0u);
-    if (in) {
-      const uint16_t* src = is_q ? a.q + tok * a.q_stride
-                                 : (is_v ? a.v + tok * a.v_stride : a.k + tok * a.k_stride);
-      x4 = *reinterpret_cast<const uint4*>(src + h * D + d0);
+// Rows of several tokens as one list, for kernels whose tokens have few rows:
+// item i of a block's list is row i % rows of token i / rows, a thread group
+// takes items RPP apart.
+struct Items {
+  int t, r, dt, dr, rows;
+  __device__ __forceinline__ Items(int i, int stride, int rows_)
+      : t(i / rows_), r(i % rows_), dt(stride / rows_), dr(stride % rows_), rows(rows_) {}
+  __device__ __forceinline__ void next() {
+    t += dt;
+    r += dr;
+    if (r >= rows) {
+      r -= rows;
+      ++t;
     }
-    const uint32_t w[4] = {x4.x, x4.y, x4.z, x4.w};
-    float y[8];
+  }
+};
+
+// The 4-bit write of rows that are rotated already: H key rows, then H value
+// rows of each of a block's per_block tokens.  kBatch rows a thread are in
+// flight: their data and slots are loaded before the first is quantized.
+template <int D, bool kBF16>
+__global__ void __launch_bounds__(kThreads) write_fp4_kernel(const AppendArgs a, int per_block,
+                                                             long long n) {
+  constexpr int LPR = D / 8, RPP = kThreads / LPR;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int rows = 2 * a.H, j = threadIdx.x % LPR;
+  const long long tok0 = (long long)blockIdx.x * per_block;
+  const int tokens = (int)min((long long)per_block, n - tok0), count = tokens * rows;
+  Items it(threadIdx.x / LPR, RPP, rows);
+  for (int i0 = 0; i0 < count; i0 += kBatch * RPP) {
+    uint4 x[kBatch];
+    long long slot[kBatch];
+    int h[kBatch];
+    bool v[kBatch];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2<kBF16>(w[i]);
-      y[2 * i] = f.x;
-      y[2 * i + 1] = f.y;
+    for (int b = 0; b < kBatch; ++b) {
+      const bool in = it.t < tokens;
+      const long long tok = tok0 + it.t;
+      v[b] = it.r >= a.H;
+      h[b] = v[b] ? it.r - a.H : it.r;
+      x[b] = make_uint4(0u, 0u, 0u, 0u);
+      slot[b] = -1;
+      if (in) {
+        x[b] = *reinterpret_cast<const uint4*>((v[b] ? a.v : a.k) + tok * a.k_stride + h[b] * D +
+                                               8 * j);
+        const bool lead = j == 0 && it.r == 0;   // one thread a token
+        int pos;
+        slot[b] = append_slot(a, tok, lead, pos);
+        if (a.slots && lead) a.slots[tok] = slot[b];
+      }
+      it.next();
     }
-    if constexpr (kNorm) {
-      float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-#pragma unroll
-      for (int o = 1; o < LPR; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const uint16_t* nw = is_q ? a.q_norm : a.k_norm;
-      if (in && !is_v && nw) {
-        const float inv = __frsqrt_rn(ss * (1.f / D) + a.eps);
-        const uint4 g4 = __ldg(reinterpret_cast<const uint4*>(nw + d0));
-        const uint32_t gw[4] = {g4.x, g4.y, g4.z, g4.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 g = unpack2<kBF16>(gw[i]);
-          y[2 * i] = y[2 * i] * inv * g.x;
-          y[2 * i + 1] = y[2 * i + 1] * inv * g.y;
-        }
-      }
-    }
-    if (a.rot > 0) {
-      float p[8];
-      if (a.interleaved) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = y[e ^ 1];
-      } else if constexpr (kNorm) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, y[e], partner);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 f = unpack2<kBF16>(__shfl_sync(0xffffffffu, w[i], partner));
-          p[2 * i] = f.x;
-          p[2 * i + 1] = f.y;
-        }
-      }
-      if (turns && !is_v) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          y[e] = __fadd_rn(__fmul_rn(y[e], c[e]), __fmul_rn(p[e], s[e]));
-      }
-    }
-    uint32_t o[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = pack2<kBF16>(y[2 * i], y[2 * i + 1]);
-    if (in && is_q)
-      *reinterpret_cast<uint4*>(a.q_out + ((size_t)tok * a.Hq + h) * D + d0) =
-          make_uint4(o[0], o[1], o[2], o[3]);
-    if constexpr (kPool == kPool16) {
-      if (in && !is_q)
-        *reinterpret_cast<uint4*>((is_v ? a.vc : a.kc) + (((size_t)slot * a.H + h) * D + d0) * 2) =
-            make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
-      const float scale = is_v ? a.v_scale : a.k_scale;
-      float z[8];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<kBF16>(o[i]);
-        z[2 * i] = f.x;
-        z[2 * i + 1] = f.y;
-      }
-      if constexpr (kPool == kPoolE4M3) {
-        uint32_t e[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          e[i] = f32x2_to_e4m3x2(__fdiv_rn(z[2 * i], scale), __fdiv_rn(z[2 * i + 1], scale));
-        if (in && !is_q)
-          *reinterpret_cast<uint2*>((is_v ? a.vc : a.kc) + ((size_t)slot * a.H + h) * D + d0) =
-              make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
-      } else {
-        // the group of 16 is this lane's 8 values and its neighbour's
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(z[e]));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        const uint32_t s8 = f32x2_to_e4m3x2(__fdiv_rn(m, __fmul_rn(6.f, scale)), 0.f) & 0xffu;
-        const float d = __fmul_rn(unpack2<false>(e4m3x2_to_f16x2(s8)).x, scale);
-        uint32_t code = 0u;
-        if (d > 0.f) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            code |= f32x2_to_e2m1x2(__fdiv_rn(z[2 * i], d), __fdiv_rn(z[2 * i + 1], d)) << (8 * i);
-        }
-        if (in && !is_q) {
-          const int B = 1 << a.log2B, row = (int)(slot & (B - 1));
-          uint8_t* plane =
-              (is_v ? a.vc : a.kc) + fp4_plane(slot >> a.log2B, a.H, h, B * fp4_row_bytes(D));
-          *reinterpret_cast<uint32_t*>(plane + row * (D / 2) + 4 * j) = code;
-          if ((j & 1) == 0) plane[fp4_scale_off<D>(B, row, j >> 1)] = (uint8_t)s8;
-        }
-      }
+    for (int b = 0; b < kBatch; ++b) {
+      if (i0 + b * RPP >= count) break;
+      store_row<D, kBF16, kPoolE2M1>(v[b] ? a.vc : a.kc, x[b], slot[b], a.H, a.log2B, h[b],
+                                     v[b] ? a.v_scale : a.k_scale, slot[b] >= 0);
     }
   }
 }
@@ -265,77 +426,109 @@ struct ReadArgs {
 };
 
 // Rows at given slots of 4-bit pools as 16-bit values, code * scale16 (exact in
-// fp32) * tensor scale, rounded to fp32 and then to 16 bits.  One block per
-// token, D / 8 lanes per row as in the write.
+// fp32) * tensor scale, rounded to fp32 and then to 16 bits.  A block takes
+// per_block tokens, D / 8 lanes a row as in the write, kBatch rows a thread:
+// their slots, then their codes, then their values.
 template <int D, bool kBF16>
-__global__ void __launch_bounds__(kThreads) read_fp4_kernel(const ReadArgs a) {
-  constexpr int LPR = D / 8;
+__global__ void __launch_bounds__(kThreads) read_fp4_kernel(const ReadArgs a, int per_block) {
+  constexpr int LPR = D / 8, RPP = kThreads / LPR;
   grid_dep_wait();
   grid_dep_launch();
-  const long long tok = blockIdx.x;
-  const long long s = a.slots[tok];
-  if (s < 0) return;
-  if (s >= (a.num_blocks << a.log2B)) {
-    if (threadIdx.x == 0) set_error(a.err, PA_DEVERR_SLOT);
-    return;
-  }
-  const int B = 1 << a.log2B, row = (int)(s & (B - 1));
-  const int j = threadIdx.x % LPR;
-  for (int r = threadIdx.x / LPR; r < 2 * a.H; r += kThreads / LPR) {
-    const bool is_v = r >= a.H;
-    const int h = is_v ? r - a.H : r;
-    const uint8_t* plane =
-        (is_v ? a.vc : a.kc) + fp4_plane(s >> a.log2B, a.H, h, B * fp4_row_bytes(D));
-    const uint32_t code = *reinterpret_cast<const uint32_t*>(plane + row * (D / 2) + 4 * j);
-    const uint32_t s8 = plane[fp4_scale_off<D>(B, row, j >> 1)];
-    const float s16 = unpack2<false>(e4m3x2_to_f16x2(s8)).x;
-    const float scale = is_v ? a.v_scale : a.k_scale;
-    uint32_t f[4], o[4];
-    e2m1x8_to_f16x2(code, f);
+  const int B = 1 << a.log2B, rows = 2 * a.H, j = threadIdx.x % LPR;
+  const long long tok0 = (long long)blockIdx.x * per_block;
+  const int tokens = (int)min((long long)per_block, a.n - tok0), count = tokens * rows;
+  Items it(threadIdx.x / LPR, RPP, rows);
+  for (int i0 = 0; i0 < count; i0 += kBatch * RPP) {
+    uint32_t code[kBatch], s8[kBatch];
+    uint16_t* dst[kBatch];
+    bool v[kBatch];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 g = unpack2<false>(f[i]);
-      o[i] = pack2<kBF16>(g.x * s16 * scale, g.y * s16 * scale);
+    for (int b = 0; b < kBatch; ++b) {
+      const long long tok = tok0 + it.t;
+      v[b] = it.r >= a.H;
+      const int h = v[b] ? it.r - a.H : it.r;
+      dst[b] = nullptr;
+      code[b] = s8[b] = 0u;
+      if (it.t < tokens) {
+        const long long slot = __ldg(a.slots + tok);
+        if (slot >= (a.num_blocks << a.log2B)) {
+          if (j == 0 && it.r == 0) set_error(a.err, PA_DEVERR_SLOT);
+        } else if (slot >= 0) {
+          const uint8_t* plane = (v[b] ? a.vc : a.kc) +
+                                 fp4_plane(slot >> a.log2B, a.H, h, B * fp4_row_bytes(D));
+          const int row = (int)(slot & (B - 1));
+          code[b] = __ldg(reinterpret_cast<const uint32_t*>(plane + row * (D / 2) + 4 * j));
+          s8[b] = __ldg(plane + fp4_scale_off<D>(B, row, j >> 1));
+          dst[b] = (v[b] ? a.v_out : a.k_out) + ((size_t)tok * a.H + h) * D + 8 * j;
+        }
+      }
+      it.next();
     }
-    *reinterpret_cast<uint4*>((is_v ? a.v_out : a.k_out) + ((size_t)tok * a.H + h) * D + 8 * j) =
-        make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (!dst[b]) continue;
+      const float s16 = unpack2<false>(e4m3x2_to_f16x2(s8[b])).x;
+      const float scale = v[b] ? a.v_scale : a.k_scale;
+      uint32_t f[4], o[4];
+      e2m1x8_to_f16x2(code[b], f);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 g = unpack2<false>(f[k]);
+        o[k] = pack2<kBF16>(g.x * s16 * scale, g.y * s16 * scale);
+      }
+      *reinterpret_cast<uint4*>(dst[b]) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
   }
 }
 
-template <int D, bool kBF16, int kPool>
-cudaError_t launch_append_n(const AppendArgs& a, bool norm, dim3 grid, cudaStream_t s) {
-  return norm ? launch_pdl(append_kernel<D, kBF16, kPool, true>, grid, dim3(kThreads), 0, s, a)
-              : launch_pdl(append_kernel<D, kBF16, kPool, false>, grid, dim3(kThreads), 0, s, a);
+// Tokens a block takes when a token has `rows` rows of D: as many as fill
+// kBatch rows a thread, as long as two blocks an SM remain.
+int tokens_per_block(int D, int rows, long long n, int sm_count) {
+  long long t = (long long)kBatch * (kThreads / (D / 8)) / rows;
+  const long long most = n / (2LL * sm_count);
+  if (t > most) t = most;
+  return t < 1 ? 1 : (int)t;
+}
+
+template <int D, bool kBF16, int kPool, bool kNorm>
+cudaError_t launch_append_n(const AppendArgs& a, long long n, int sm_count, cudaStream_t s) {
+  // few tokens: a token's rows spread over several blocks, so that the step
+  // takes one pass; many tokens fill the GPU by themselves
+  const int per_pass = kThreads / (D / 8), most = a.Hq > a.H ? a.Hq : a.H;
+  const int passes = (most + per_pass - 1) / per_pass;
+  long long y = (2LL * sm_count + n - 1) / n;
+  if (y > passes) y = passes;
+  if (y < 1) y = 1;
+  return launch_pdl(append_kernel<D, kBF16, kPool, kNorm>, dim3((unsigned)n, (unsigned)y),
+                    dim3(kThreads), 0, s, a);
 }
 
 template <int D, bool kBF16>
-cudaError_t launch_append_p(const AppendArgs& a, int pool, bool norm, dim3 grid, cudaStream_t s) {
-  if (pool == kPoolE2M1) return launch_append_n<D, kBF16, kPoolE2M1>(a, norm, grid, s);
-  if (pool == kPoolE4M3) return launch_append_n<D, kBF16, kPoolE4M3>(a, norm, grid, s);
-  return launch_append_n<D, kBF16, kPool16>(a, norm, grid, s);
+cudaError_t launch_append_p(const AppendArgs& a, int pool, long long n, int sm_count,
+                            cudaStream_t s) {
+  const bool norm = a.q_norm || a.k_norm;
+  if (pool == kPoolE2M1)
+    return norm ? launch_append_n<D, kBF16, kPoolE2M1, true>(a, n, sm_count, s)
+                : launch_append_n<D, kBF16, kPoolE2M1, false>(a, n, sm_count, s);
+  if (pool == kPoolE4M3)
+    return norm ? launch_append_n<D, kBF16, kPoolE4M3, true>(a, n, sm_count, s)
+                : launch_append_n<D, kBF16, kPoolE4M3, false>(a, n, sm_count, s);
+  return norm ? launch_append_n<D, kBF16, kPool16, true>(a, n, sm_count, s)
+              : launch_append_n<D, kBF16, kPool16, false>(a, n, sm_count, s);
 }
 
 int launch_append(const AppendArgs& a, int D, bool bf16, int pool, long long n, cudaStream_t s,
                   const char* what) {
   DeviceInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  // few tokens: a token's rows spread over several blocks, so that the step
-  // takes one pass; many tokens fill the GPU by themselves
-  const int per_pass = kThreads / (D / 8);
-  const int passes = (a.Hq + 2 * a.H + per_pass - 1) / per_pass;
-  long long y = n > 0 ? (2LL * di.sm_count + n - 1) / n : 1;
-  if (y > passes) y = passes;
-  if (y < 1) y = 1;
-  const dim3 grid((unsigned)n, (unsigned)y);
-  const bool norm = a.q_norm || a.k_norm;
   clear_stale_error();
   cudaError_t e;
   if (D == 64)
-    e = bf16 ? launch_append_p<64, true>(a, pool, norm, grid, s)
-             : launch_append_p<64, false>(a, pool, norm, grid, s);
+    e = bf16 ? launch_append_p<64, true>(a, pool, n, di.sm_count, s)
+             : launch_append_p<64, false>(a, pool, n, di.sm_count, s);
   else
-    e = bf16 ? launch_append_p<128, true>(a, pool, norm, grid, s)
-             : launch_append_p<128, false>(a, pool, norm, grid, s);
+    e = bf16 ? launch_append_p<128, true>(a, pool, n, di.sm_count, s)
+             : launch_append_p<128, false>(a, pool, n, di.sm_count, s);
   return launch_status(e, what);
 }
 
@@ -353,8 +546,7 @@ int append_shape(int32_t block_size, int32_t num_kv_heads, int32_t head_dim, int
   return PA_OK;
 }
 
-// The 4-bit write behind its two entry points: an append without queries,
-// rotation or norms, of contiguous rows.
+// The 4-bit write behind its two entry points.
 int write_fp4(const void* k, const void* v, int32_t src_dtype, AppendArgs a, int64_t num_tokens,
               void* k_cache, void* v_cache, int64_t num_blocks, int32_t block_size,
               int32_t num_kv_heads, int32_t head_dim, float k_scale, float v_scale,
@@ -379,8 +571,22 @@ int write_fp4(const void* k, const void* v, int32_t src_dtype, AppendArgs a, int
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.err = err_word;
-  return launch_append(a, head_dim, src_dtype == PA_BF16, kPoolE2M1, num_tokens,
-                       static_cast<cudaStream_t>(stream), what);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  DeviceInfo di;
+  if (int rc = current_device_info(&di)) return rc;
+  const int per = tokens_per_block(head_dim, 2 * num_kv_heads, num_tokens, di.sm_count);
+  const long long n = num_tokens;
+  const dim3 grid((unsigned)((n + per - 1) / per)), block(kThreads);
+  const bool bf16 = src_dtype == PA_BF16;
+  clear_stale_error();
+  cudaError_t e;
+  if (head_dim == 64)
+    e = bf16 ? launch_pdl(write_fp4_kernel<64, true>, grid, block, 0, s, a, per, n)
+             : launch_pdl(write_fp4_kernel<64, false>, grid, block, 0, s, a, per, n);
+  else
+    e = bf16 ? launch_pdl(write_fp4_kernel<128, true>, grid, block, 0, s, a, per, n)
+             : launch_pdl(write_fp4_kernel<128, false>, grid, block, 0, s, a, per, n);
+  return launch_status(e, what);
 }
 
 }  // namespace
@@ -518,16 +724,19 @@ int pa_cache_read_fp4(const int64_t* slot_mapping, int64_t num_tokens, const voi
   a.v_scale = v_scale;
   a.err = err_word;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const dim3 grid((unsigned)num_tokens), block(kThreads);
+  DeviceInfo di;
+  if (int rc = current_device_info(&di)) return rc;
+  const int per = tokens_per_block(head_dim, 2 * num_kv_heads, num_tokens, di.sm_count);
+  const dim3 grid((unsigned)((num_tokens + per - 1) / per)), block(kThreads);
   const bool bf16 = out_dtype == PA_BF16;
   clear_stale_error();
   cudaError_t e;
   if (head_dim == 64)
-    e = bf16 ? launch_pdl(read_fp4_kernel<64, true>, grid, block, 0, s, a)
-             : launch_pdl(read_fp4_kernel<64, false>, grid, block, 0, s, a);
+    e = bf16 ? launch_pdl(read_fp4_kernel<64, true>, grid, block, 0, s, a, per)
+             : launch_pdl(read_fp4_kernel<64, false>, grid, block, 0, s, a, per);
   else
-    e = bf16 ? launch_pdl(read_fp4_kernel<128, true>, grid, block, 0, s, a)
-             : launch_pdl(read_fp4_kernel<128, false>, grid, block, 0, s, a);
+    e = bf16 ? launch_pdl(read_fp4_kernel<128, true>, grid, block, 0, s, a, per)
+             : launch_pdl(read_fp4_kernel<128, false>, grid, block, 0, s, a, per);
   return launch_status(e, "4-bit cache read launch");
 }
 

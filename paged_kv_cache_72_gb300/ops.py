@@ -96,11 +96,24 @@ def _block_pools(k_cache, v_cache):
 
 
 def _here(*tensors):
-    """Every tensor given is on the current device, whose stream the call uses."""
+    """The current device's index and its current stream (a raw handle), after
+    checking that every tensor given is on that device."""
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != dev:
+        if t is not None and t.get_device() != dev:
             raise ValueError("every tensor must be on the current device, cuda:%d" % dev)
+    return _raw_stream(dev)
+
+
+def _raw_stream(dev):
+    """The current stream's handle: the lookup behind torch.cuda.current_stream
+    without the stream object, which costs more than a launch."""
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _at(t):
+    """A tensor's address, as the calls take it (None: NULL)."""
+    return None if t is None else t.data_ptr()
 
 
 def _i32(t, name):
@@ -397,10 +410,9 @@ def pa_decode_fp8(q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v
 def _token_rows(t, name, n_tok, heads, D):
     """A [num_tokens, heads, D] tensor whose rows are contiguous within a token;
     tokens may lie any multiple of 8 elements apart.  Returns that distance."""
-    if not t.is_cuda:
-        raise ValueError("%s must be a CUDA tensor" % name)
-    if t.shape != (n_tok, heads, D):
-        raise ValueError("%s must be [num_tokens, heads, D] = %s" % (name, (n_tok, heads, D)))
+    if not t.is_cuda or t.shape != (n_tok, heads, D):
+        raise ValueError("%s must be a CUDA tensor [num_tokens, heads, D] = %s"
+                         % (name, (n_tok, heads, D)))
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != D):
         raise ValueError("the heads of a token must be contiguous in %s" % name)
@@ -465,15 +477,15 @@ def pa_append_rope(q, k, v, cos_sin, block_tables, token_seq, token_pos, k_cache
             if t.shape != (D,) or t.dtype != k.dtype:
                 raise ValueError("%s must be [D] of k's dtype" % n)
     _slots_out(slot_mapping, n_tok)
-    _here(q, k, v, cos_sin, q_norm, k_norm, block_tables, token_seq, token_pos, k_cache, v_cache,
+    stream = _here(q, k, v, cos_sin, q_norm, k_norm, block_tables, token_seq, token_pos, k_cache, v_cache,
           q_out, slot_mapping, _err_word(err))
-    _check(L.pa_append_rope(_ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _dtype_code(k), _ptr(cos_sin),
-                            rot, max_pos, int(bool(interleaved)), _ptr(q_norm), _ptr(k_norm),
-                            float(eps), _ptr(block_tables), block_tables.shape[1],
-                            block_tables.shape[0], _ptr(token_seq), _ptr(token_pos), n_tok,
-                            _ptr(q_out), _ptr(k_cache), _ptr(v_cache), nb, B, Hq, H, D, code,
-                            float(k_scale), float(v_scale), _ptr(slot_mapping), _ptr(err),
-                            _stream()), "pa_append_rope")
+    _check(L.pa_append_rope(_at(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(k), _at(cos_sin),
+                            rot, max_pos, int(bool(interleaved)), _at(q_norm), _at(k_norm),
+                            float(eps), block_tables.data_ptr(), block_tables.shape[1],
+                            block_tables.shape[0], token_seq.data_ptr(), token_pos.data_ptr(), n_tok,
+                            _at(q_out), k_cache.data_ptr(), v_cache.data_ptr(), nb, B, Hq, H, D, code,
+                            float(k_scale), float(v_scale), _at(slot_mapping), _at(err),
+                            stream), "pa_append_rope")
     return q_out
 
 
@@ -491,10 +503,10 @@ def pa_cache_write_fp4(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, e
     n_tok = slot_mapping.numel()
     if k.shape != (n_tok, H, D) or v.shape != (n_tok, H, D) or k.dtype != v.dtype:
         raise ValueError("k, v must be [num_tokens, H_kv, D] of one dtype")
-    _here(k, v, slot_mapping, k_cache, v_cache, _err_word(err))
-    _check(L.pa_cache_write_fp4(_ptr(k), _ptr(v), _dtype_code(k), _ptr(slot_mapping), n_tok,
-                                _ptr(k_cache), _ptr(v_cache), nb, B, H, D, float(k_scale),
-                                float(v_scale), _ptr(err), _stream()), "pa_cache_write_fp4")
+    stream = _here(k, v, slot_mapping, k_cache, v_cache, _err_word(err))
+    _check(L.pa_cache_write_fp4(k.data_ptr(), v.data_ptr(), _dtype_code(k), slot_mapping.data_ptr(), n_tok,
+                                k_cache.data_ptr(), v_cache.data_ptr(), nb, B, H, D, float(k_scale),
+                                float(v_scale), _at(err), stream), "pa_cache_write_fp4")
 
 
 def pa_cache_write_fp4_mapped(k, v, block_tables, token_seq, token_pos, k_cache, v_cache,
@@ -517,12 +529,12 @@ def pa_cache_write_fp4_mapped(k, v, block_tables, token_seq, token_pos, k_cache,
     if k.shape != (n_tok, H, D) or v.shape != (n_tok, H, D) or k.dtype != v.dtype:
         raise ValueError("k, v must be [num_tokens, H_kv, D] of one dtype")
     _slots_out(slot_mapping, n_tok)
-    _here(k, v, block_tables, token_seq, token_pos, k_cache, v_cache, slot_mapping, _err_word(err))
-    _check(L.pa_cache_write_fp4_mapped(_ptr(k), _ptr(v), _dtype_code(k), _ptr(block_tables),
+    stream = _here(k, v, block_tables, token_seq, token_pos, k_cache, v_cache, slot_mapping, _err_word(err))
+    _check(L.pa_cache_write_fp4_mapped(k.data_ptr(), v.data_ptr(), _dtype_code(k), block_tables.data_ptr(),
                                        block_tables.shape[1], block_tables.shape[0],
-                                       _ptr(token_seq), _ptr(token_pos), n_tok, _ptr(k_cache),
-                                       _ptr(v_cache), nb, B, H, D, float(k_scale), float(v_scale),
-                                       _ptr(slot_mapping), _ptr(err), _stream()),
+                                       token_seq.data_ptr(), token_pos.data_ptr(), n_tok, k_cache.data_ptr(),
+                                       v_cache.data_ptr(), nb, B, H, D, float(k_scale), float(v_scale),
+                                       _at(slot_mapping), _at(err), stream),
            "pa_cache_write_fp4_mapped")
     return slot_mapping
 
@@ -547,10 +559,10 @@ def pa_cache_read_fp4(slot_mapping, k_cache, v_cache, k_scale, v_scale, dtype=to
         _cuda(t, n)
         if t.shape != (n_tok, H, D) or t.dtype != k_out.dtype:
             raise ValueError("k_out, v_out must be [n, H_kv, D] of one dtype")
-    _here(slot_mapping, k_cache, v_cache, k_out, v_out, _err_word(err))
-    _check(L.pa_cache_read_fp4(_ptr(slot_mapping), n_tok, _ptr(k_cache), _ptr(v_cache), nb, B, H,
-                               D, float(k_scale), float(v_scale), _ptr(k_out), _ptr(v_out),
-                               _dtype_code(k_out), _ptr(err), _stream()), "pa_cache_read_fp4")
+    stream = _here(slot_mapping, k_cache, v_cache, k_out, v_out, _err_word(err))
+    _check(L.pa_cache_read_fp4(slot_mapping.data_ptr(), n_tok, k_cache.data_ptr(), v_cache.data_ptr(), nb, B, H,
+                               D, float(k_scale), float(v_scale), k_out.data_ptr(), v_out.data_ptr(),
+                               _dtype_code(k_out), _at(err), stream), "pa_cache_read_fp4")
     return k_out, v_out
 
 
@@ -580,12 +592,12 @@ def pa_decode_fp4(q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v
         # zero-filled once; the decode leaves it ready for the next call
         workspace = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=q.device)
     _cuda(workspace, "workspace")
-    _here(q, k_cache, v_cache, block_tables, seq_lens, out, workspace, _err_word(err))
-    _check(L.pa_decode_fp4(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-                           block_tables.shape[1], _ptr(seq_lens), N, Hq, H, D, B, nb, code,
-                           float(scale), float(k_scale), float(v_scale), int(window), _ptr(out),
-                           _ptr(workspace), workspace.numel() * workspace.element_size(),
-                           int(flags), int(num_ctas), _ptr(err), _stream()), "pa_decode_fp4")
+    stream = _here(q, k_cache, v_cache, block_tables, seq_lens, out, workspace, _err_word(err))
+    _check(L.pa_decode_fp4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
+                           block_tables.shape[1], seq_lens.data_ptr(), N, Hq, H, D, B, nb, code,
+                           float(scale), float(k_scale), float(v_scale), int(window), out.data_ptr(),
+                           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                           int(flags), int(num_ctas), _at(err), stream), "pa_decode_fp4")
     return out
 
 
