@@ -172,6 +172,21 @@ struct Turn {
     }
   }
 
+  // the angles times a norm's weights: gc = g c, gs = g_partner s (c is g where
+  // nothing turns); every lane takes part
+  template <bool kBF16>
+  __device__ __forceinline__ void join(const uint16_t* weights, bool rotates, int d0) {
+    const uint4 w = __ldg(reinterpret_cast<const uint4*>(weights + d0));
+    F2 g[4], p[4];
+    widen<kBF16>(w, g);
+    if (rotates) partners<kBF16>(w, g, p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = rotates && on ? mul2(g[i], c[i]) : g[i];
+      if (rotates && on) s[i] = mul2(p[i], s[i]);
+    }
+  }
+
   // the partner elements of a row whose 16 bytes are x (every lane takes part)
   template <bool kBF16>
   __device__ __forceinline__ void partners(const uint4& x, const F2 (&y)[4], F2 (&p)[4]) const {
@@ -186,18 +201,18 @@ struct Turn {
   }
 };
 
-// One query or key row: norm with the weights g (when given), rotation, one
-// rounding to 16 bits.  Without a norm the products are rounded before they are
-// added, as the header of this file says; with one the weights join the angles
-// (gc = g c, gs = g_partner s), the row is a' = r (x gc + p gs).
+// One query or key row: norm (when `normed`), rotation, one rounding to 16
+// bits.  Without a norm the products are rounded before they are added, as the
+// header of this file says; with one t holds the angles times the weights
+// (Turn::join) and the row is a' = r (x gc + p gs).
 template <int D, bool kBF16, bool kNorm>
 __device__ __forceinline__ uint4 turned(const AppendArgs& a, const uint4& x, const Turn& t,
-                                        const uint16_t* g, const F2 (&gc)[4], const F2 (&gs)[4]) {
+                                        bool normed) {
   const bool rotates = a.rot > 0;
   F2 y[4], p[4];
   widen<kBF16>(x, y);
   if (rotates) t.partners<kBF16>(x, y, p);
-  if (kNorm && g) {
+  if (kNorm && normed) {
     F2 q = mul2(y[0], y[0]);
 #pragma unroll
     for (int i = 1; i < 4; ++i) q = fma2(y[i], y[i], q);
@@ -207,8 +222,8 @@ __device__ __forceinline__ uint4 turned(const AppendArgs& a, const uint4& x, con
     const float r = rsqrtf(fmaf(ss, 1.f / D, a.eps));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      y[i] = mul2(y[i], gc[i]);
-      if (rotates && t.on) y[i] = fma2(p[i], gs[i], y[i]);
+      y[i] = mul2(y[i], t.c[i]);
+      if (rotates && t.on) y[i] = fma2(p[i], t.s[i], y[i]);
       y[i] = mul2(y[i], {r, r});
     }
   } else if (rotates && t.on) {
@@ -218,23 +233,6 @@ __device__ __forceinline__ uint4 turned(const AppendArgs& a, const uint4& x, con
     return x;
   }
   return narrow<kBF16>(y);
-}
-
-// gc and gs of a norm's weights
-template <bool kBF16>
-__device__ __forceinline__ void join(const uint16_t* g, const Turn& t, bool rotates, int d0,
-                                     F2 (&gc)[4], F2 (&gs)[4]) {
-  const uint4 w = __ldg(reinterpret_cast<const uint4*>(g + d0));
-  F2 p[4];
-  widen<kBF16>(w, gc);
-  if (!rotates) return;
-  t.partners<kBF16>(w, gc, p);
-  if (!t.on) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    gc[i] = mul2(gc[i], t.c[i]);
-    gs[i] = mul2(p[i], t.s[i]);
-  }
 }
 
 // One key or value row into its pool, this lane's 16 bytes x of head h: as it
@@ -291,7 +289,7 @@ constexpr int kBatch = 4;   // rows a thread group loads before it works on the 
 // rows, then key rows, then value rows, each D / 8 lanes wide.  The first rows
 // of each kind are loaded before the token's slot is known.
 template <int D, bool kBF16, int kPool, bool kNorm>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) append_kernel(const AppendArgs a) {
   constexpr int LPR = D / 8;               // lanes per row
   constexpr int RPP = kThreads / LPR;      // rows per pass of the block
   grid_dep_wait();
@@ -320,9 +318,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
   if (slot < 0) return;                    // the whole block: every thread found the same slot
   Turn t;
   t.load(a, pos, d0);
-  F2 gc[4], gs[4];
   // rows in lockstep over the block (the shuffles need every lane)
-  if (kNorm && a.q_norm) join<kBF16>(a.q_norm, t, a.rot > 0, d0, gc, gs);
+  if (kNorm && a.q_norm) t.join<kBF16>(a.q_norm, a.rot > 0, d0);
   uint16_t* const qo = a.q_out + (size_t)tok * a.Hq * D + d0;
   for (int first = blockIdx.y * RPP; first < a.Hq; first += kBatch * step) {
     const int hb = first + threadIdx.x / LPR;
@@ -330,13 +327,16 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
     for (int b = 0; b < kBatch; ++b) {
       if (first + b * step >= a.Hq) break;
       const int h = hb + b * step;
-      const uint4 o = turned<D, kBF16, kNorm>(a, xq[b], t, a.q_norm, gc, gs);
+      const uint4 o = turned<D, kBF16, kNorm>(a, xq[b], t, a.q_norm != nullptr);
       if (h < a.Hq) *reinterpret_cast<uint4*>(qo + h * D) = o;
       const int next = h + kBatch * step;
       if (next < a.Hq) xq[b] = *reinterpret_cast<const uint4*>(qr + next * D);
     }
   }
-  if (kNorm && a.k_norm) join<kBF16>(a.k_norm, t, a.rot > 0, d0, gc, gs);
+  if constexpr (kNorm) {   // the keys' weights: the angles are read again (from L1)
+    if (a.q_norm) t.load(a, pos, d0);
+    if (a.k_norm) t.join<kBF16>(a.k_norm, a.rot > 0, d0);
+  }
   for (int first = blockIdx.y * RPP; first < a.H; first += step) {
     const int h = first + threadIdx.x / LPR;
     const bool in = h < a.H;
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendArgs a) {
       xk = *reinterpret_cast<const uint4*>(kr + (h + step) * D);
       xv = *reinterpret_cast<const uint4*>(vr + (h + step) * D);
     }
-    const uint4 o = turned<D, kBF16, kNorm>(a, k, t, a.k_norm, gc, gs);
+    const uint4 o = turned<D, kBF16, kNorm>(a, k, t, a.k_norm != nullptr);
     store_row<D, kBF16, kPool>(a.kc, o, slot, a.H, a.log2B, h, a.k_scale, in);
     store_row<D, kBF16, kPool>(a.vc, v, slot, a.H, a.log2B, h, a.v_scale, in);
   }
