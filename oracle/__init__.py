@@ -512,7 +512,8 @@ def e2m1_encode(x):
     """Values -> E2M1 codes 0..15: the nearest magnitude, a tie to the even
     code, magnitudes beyond 6 to 6."""
     x = np.asarray(x, np.float64)
-    dist = np.abs(np.abs(x)[..., None] - _E2M1)
+    # beyond 8 every value is nearest to 6 (and a huge one would swallow the grid)
+    dist = np.abs(np.minimum(np.abs(x), 8.0)[..., None] - _E2M1)
     near = dist == dist.min(-1, keepdims=True)   # one code, or the two of a tie
     even = near & (np.arange(8) % 2 == 0)
     mag = np.where(even.any(-1), even.argmax(-1), near.argmax(-1)).astype(np.uint8)
@@ -529,9 +530,9 @@ def fp4_quantize(x, scale):
     x = np.ascontiguousarray(x, np.float32)
     g = x.reshape(x.shape[:-1] + (x.shape[-1] // 16, 16))
     s = np.float32(scale)
-    s16 = e4m3_encode(np.abs(g).max(-1) / (np.float32(6) * s))
-    d = e4m3_decode(s16).astype(np.float32) * s
-    with np.errstate(divide="ignore", invalid="ignore"):
+    with np.errstate(all="ignore"):
+        s16 = e4m3_encode(np.abs(g).max(-1) / (np.float32(6) * s))
+        d = e4m3_decode(s16).astype(np.float32) * s
         y = np.where(d[..., None] > 0, g / d[..., None], np.float32(0))
     return e2m1_encode(y).reshape(x.shape), s16
 

@@ -85,18 +85,6 @@ __device__ __forceinline__ long long append_slot(const AppendArgs& a, long long 
   return ((long long)p << a.log2B) + (pos & ((1 << a.log2B) - 1));
 }
 
-// x / d rounded to nearest, from r = 1 / d rounded to nearest: one residual
-// step on x r gives the correctly rounded quotient (P. Markstein, "Computation
-// of elementary functions on the IBM RISC System/6000 processor", 1990) where
-// nothing under- or overflows: d within 2^+-100; an x so small that its residual
-// is lost is far below the smallest code.
-__device__ __forceinline__ float div_by(float x, float d, float r, bool exact) {
-  if (!exact) return __fdiv_rn(x, d);
-  const float y = __fmul_rn(x, r);
-  return __fmaf_rn(__fmaf_rn(-y, d, x), r, y);
-}
-__device__ __forceinline__ bool plain_divisor(float d) { return d > 0x1p-100f && d < 0x1p100f; }
-
 // Two fp32 values at a time, each rounded as alone.
 struct F2 {
   float x, y;
@@ -120,6 +108,34 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
+// x / d rounded to nearest, from r = 1 / d rounded to nearest: one residual
+// step on x r gives the correctly rounded quotient (P. Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990) where
+// nothing under- or overflows: d within 2^+-100 and |x| at most 2^27 d
+// (plain_quotient); an x so small that its residual is lost is far below the
+// smallest code.
+__device__ __forceinline__ F2 div_by(F2 x, float d, float r) {
+  const F2 y = mul2(x, {r, r});
+  return fma2(fma2({-y.x, -y.y}, {d, d}, x), {r, r}, y);
+}
+__device__ __forceinline__ bool plain_quotient(float largest, float d) {
+  return d > 0x1p-100f && d < 0x1p100f && largest <= 0x1p27f * d;
+}
+// x / d for the others, off the common path (0 for d = 0)
+__device__ __noinline__ float div_any(float x, float d) { return d > 0.f ? __fdiv_rn(x, d) : 0.f; }
+
+// z / d, four pairs of magnitudes up to `largest`; r is 1 / d rounded to nearest
+__device__ __forceinline__ void quotients(const F2 (&z)[4], float largest, float d, float r,
+                                          F2 (&y)[4]) {
+  if (plain_quotient(largest, d)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = div_by(z[i], d, r);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = {div_any(z[i].x, d), div_any(z[i].y, d)};
+  }
+}
+
 template <bool kBF16>
 __device__ __forceinline__ void widen(const uint4& x, F2 (&y)[4]) {
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -248,32 +264,30 @@ __device__ __forceinline__ void store_row(uint8_t* pool, const uint4& x, long lo
   }
   F2 z[4];
   widen<kBF16>(x, z);
+  F2 y[4];
+  float m = fmaxf(fabsf(z[0].x), fabsf(z[0].y));
+#pragma unroll
+  for (int i = 1; i < 4; ++i) m = max3f(m, fabsf(z[i].x), fabsf(z[i].y));
+  // the scale's own reciprocals are the call's: the compiler hoists them
   if constexpr (kPool == kPoolE4M3) {
-    const float rs = __frcp_rn(scale);
-    const bool exact = plain_divisor(scale);
+    quotients(z, m, scale, __frcp_rn(scale), y);
     uint32_t e[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      e[i] = f32x2_to_e4m3x2(div_by(z[i].x, scale, rs, exact), div_by(z[i].y, scale, rs, exact));
+    for (int i = 0; i < 4; ++i) e[i] = f32x2_to_e4m3x2(y[i].x, y[i].y);
     if (in)
       *reinterpret_cast<uint2*>(pool + ((size_t)slot * H + h) * D + d0) =
           make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
   } else if constexpr (kPool == kPoolE2M1) {
-    float m = fmaxf(fabsf(z[0].x), fabsf(z[0].y));
-#pragma unroll
-    for (int i = 1; i < 4; ++i) m = max3f(m, fabsf(z[i].x), fabsf(z[i].y));
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    const uint32_t s8 = f32x2_to_e4m3x2(__fdiv_rn(m, __fmul_rn(6.f, scale)), 0.f) & 0xffu;
+    const float six = __fmul_rn(6.f, scale);
+    const float s16 =
+        plain_quotient(m, six) ? div_by({m, m}, six, __frcp_rn(six)).x : div_any(m, six);
+    const uint32_t s8 = f32x2_to_e4m3x2(s16, 0.f) & 0xffu;
     const float d = __fmul_rn(unpack2<false>(e4m3x2_to_f16x2(s8)).x, scale);
+    quotients(z, m, d, __frcp_rn(d), y);
     uint32_t code = 0u;
-    if (d > 0.f) {
-      const float rd = __frcp_rn(d);
-      const bool exact = plain_divisor(d);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        code |= f32x2_to_e2m1x2(div_by(z[i].x, d, rd, exact), div_by(z[i].y, d, rd, exact))
-                << (8 * i);
-    }
+    for (int i = 0; i < 4; ++i) code |= f32x2_to_e2m1x2(y[i].x, y[i].y) << (8 * i);
     if (in) {
       const int B = 1 << log2B, row = (int)(slot & (B - 1));
       uint8_t* plane = pool + fp4_plane(slot >> log2B, H, h, B * fp4_row_bytes(D));

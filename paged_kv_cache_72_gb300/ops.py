@@ -77,7 +77,10 @@ _FP4_HEAD_DIM = {36: 64, 72: 128}
 
 def _fp4_pools(k_cache, v_cache):
     """(num_blocks, B, H_kv, D) of a pair of 4-bit pools."""
-    nb, H, B, row = _pool_shape(k_cache, v_cache)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or k_cache.dtype != v_cache.dtype:
+        raise ValueError("k_cache and v_cache must share one shape [num_blocks, H_kv, B, 9 D / 16]")
+    nb, H, B, row = shape
     if k_cache.dtype != torch.uint8:
         raise TypeError("4-bit pools must be uint8 tensors of codes and scales")
     if row not in _FP4_HEAD_DIM:
@@ -95,44 +98,44 @@ def _block_pools(k_cache, v_cache):
     return a, b, c, d, PA_FP8_E4M3
 
 
-def _here(*tensors):
-    """The current device's index and its current stream (a raw handle), after
-    checking that every tensor given is on that device."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("every tensor must be on the current device, cuda:%d" % dev)
-    return _raw_stream(dev)
-
-
 def _raw_stream(dev):
     """The current stream's handle: the lookup behind torch.cuda.current_stream
     without the stream object, which costs more than a launch."""
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _at(t):
-    """A tensor's address, as the calls take it (None: NULL)."""
-    return None if t is None else t.data_ptr()
+def _here(names, *tensors):
+    """The current stream, after checking that every tensor given (not None) is
+    contiguous and on the current device.  names: theirs, space-separated."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
+            for n, u in zip(names.split(), tensors):
+                if u is t:
+                    _cuda(u, n)
+                    raise ValueError("%s must be on the current device, cuda:%d" % (n, dev))
+    return _raw_stream(dev)
 
 
-def _i32(t, name):
-    _cuda(t, name)
-    if t.dtype != torch.int32:
-        raise TypeError("%s must be int32" % name)
+def _tables(block_tables, token_seq, token_pos):
+    """The number of tokens, of slots given by table, sequence and position."""
+    i32 = torch.int32
+    if block_tables.dtype != i32 or token_seq.dtype != i32 or token_pos.dtype != i32:
+        raise TypeError("block_tables, token_seq and token_pos must be int32")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be [num_seqs, stride]")
+    n_tok = token_seq.numel()
+    if token_pos.numel() != n_tok:
+        raise ValueError("token_seq and token_pos differ in length")
+    return n_tok
 
 
-def _err_word(err):
-    if err is not None and (not err.is_cuda or err.dtype != torch.int32 or err.numel() < 1):
+def _outs(n_tok, slot_mapping, err):
+    if slot_mapping is not None and (slot_mapping.dtype != torch.int64
+                                     or slot_mapping.numel() != n_tok):
+        raise ValueError("slot_mapping must be int64 [num_tokens]")
+    if err is not None and (err.dtype != torch.int32 or err.numel() < 1):
         raise ValueError("err must be an int32 CUDA tensor")
-    return err
-
-
-def _slots_out(slot_mapping, n_tok):
-    if slot_mapping is not None:
-        _cuda(slot_mapping, "slot_mapping")
-        if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != n_tok:
-            raise ValueError("slot_mapping must be int64 [num_tokens]")
 
 
 def pa_version():
@@ -407,12 +410,15 @@ def pa_decode_fp8(q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v
     return out
 
 
-def _token_rows(t, name, n_tok, heads, D):
+def _token_rows(t, name, n_tok, heads, D, dtype, dev):
     """A [num_tokens, heads, D] tensor whose rows are contiguous within a token;
     tokens may lie any multiple of 8 elements apart.  Returns that distance."""
-    if not t.is_cuda or t.shape != (n_tok, heads, D):
-        raise ValueError("%s must be a CUDA tensor [num_tokens, heads, D] = %s"
-                         % (name, (n_tok, heads, D)))
+    if t.get_device() != dev:
+        raise ValueError("%s must be on the current device, cuda:%d" % (name, dev))
+    if t.dtype != dtype:
+        raise TypeError("q, k and v must share a dtype")
+    if t.shape != (n_tok, heads, D):
+        raise ValueError("%s must be [num_tokens, heads, D] = %s" % (name, (n_tok, heads, D)))
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != D):
         raise ValueError("the heads of a token must be contiguous in %s" % name)
@@ -439,54 +445,59 @@ def pa_append_rope(q, k, v, cos_sin, block_tables, token_seq, token_pos, k_cache
     what they held (zeros when q_out is made here)."""
     L = _lib.load()
     nb, B, H, D, code = _block_pools(k_cache, v_cache)
-    _i32(block_tables, "block_tables")
-    _i32(token_seq, "token_seq")
-    _i32(token_pos, "token_pos")
-    n_tok = token_seq.numel()
-    if token_pos.numel() != n_tok:
-        raise ValueError("token_seq and token_pos differ in length")
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must be [num_seqs, stride]")
-    ks, vs = _token_rows(k, "k", n_tok, H, D), _token_rows(v, "v", n_tok, H, D)
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
-        raise TypeError("q, k and v must share a dtype")
-    if k_cache.dtype not in (k.dtype, torch.uint8):
+    n_tok = _tables(block_tables, token_seq, token_pos)
+    _outs(n_tok, slot_mapping, err)
+    dtype = k.dtype
+    if k_cache.dtype != dtype and code not in (PA_FP8_E4M3, PA_FP4_E2M1):
         raise TypeError("the pools must be of k's dtype, or uint8")
-    Hq, qs = 0, 0
+    dev = torch.cuda.current_device()
+    ks = _token_rows(k, "k", n_tok, H, D, dtype, dev)
+    vs = _token_rows(v, "v", n_tok, H, D, dtype, dev)
+    Hq = qs = rot = max_pos = 0
     if q is not None:
         if q.dim() != 3:
             raise ValueError("q must be [num_tokens, Hq, D]")
         Hq = q.shape[1]
-        qs = _token_rows(q, "q", n_tok, Hq, D)
+        qs = _token_rows(q, "q", n_tok, Hq, D, dtype, dev)
         if q_out is None:
-            q_out = torch.zeros((n_tok, Hq, D), dtype=q.dtype, device=q.device)
-        _cuda(q_out, "q_out")
-        if q_out.shape != (n_tok, Hq, D) or q_out.dtype != q.dtype:
+            q_out = torch.zeros((n_tok, Hq, D), dtype=dtype, device=q.device)
+        elif q_out.shape != (n_tok, Hq, D) or q_out.dtype != dtype:
             raise ValueError("q_out must be [num_tokens, Hq, D] of q's dtype")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rot = max_pos = 0
     if cos_sin is not None:
-        _cuda(cos_sin, "cos_sin")
         if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
             raise TypeError("cos_sin must be float32 [max_pos, rotary_dim]")
         max_pos, rot = cos_sin.shape
-    for t, n in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is not None:
-            _cuda(t, n)
-            if t.shape != (D,) or t.dtype != k.dtype:
-                raise ValueError("%s must be [D] of k's dtype" % n)
-    _slots_out(slot_mapping, n_tok)
-    stream = _here(q, k, v, cos_sin, q_norm, k_norm, block_tables, token_seq, token_pos, k_cache, v_cache,
-          q_out, slot_mapping, _err_word(err))
-    _check(L.pa_append_rope(_at(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, _dtype_code(k), _at(cos_sin),
-                            rot, max_pos, int(bool(interleaved)), _at(q_norm), _at(k_norm),
-                            float(eps), block_tables.data_ptr(), block_tables.shape[1],
-                            block_tables.shape[0], token_seq.data_ptr(), token_pos.data_ptr(), n_tok,
-                            _at(q_out), k_cache.data_ptr(), v_cache.data_ptr(), nb, B, Hq, H, D, code,
-                            float(k_scale), float(v_scale), _at(slot_mapping), _at(err),
-                            stream), "pa_append_rope")
+    for g in (q_norm, k_norm):
+        if g is not None and (g.shape != (D,) or g.dtype != dtype):
+            raise ValueError("q_norm and k_norm must be [D] of k's dtype")
+    stream = _here("cos_sin q_norm k_norm block_tables token_seq token_pos k_cache v_cache q_out "
+                   "slot_mapping err", cos_sin, q_norm, k_norm, block_tables, token_seq, token_pos,
+                   k_cache, v_cache, q_out, slot_mapping, err)
+    stride = block_tables.shape
+    _check(L.pa_append_rope(
+        None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        _dtype_code(k), None if cos_sin is None else cos_sin.data_ptr(), rot, max_pos,
+        1 if interleaved else 0, None if q_norm is None else q_norm.data_ptr(),
+        None if k_norm is None else k_norm.data_ptr(), eps, block_tables.data_ptr(), stride[1],
+        stride[0], token_seq.data_ptr(), token_pos.data_ptr(), n_tok,
+        None if q_out is None else q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, B,
+        Hq, H, D, code, k_scale, v_scale,
+        None if slot_mapping is None else slot_mapping.data_ptr(),
+        None if err is None else err.data_ptr(), stream), "pa_append_rope")
     return q_out
+
+
+def _kv_rows(k, v, n_tok, H, D):
+    if k.shape != (n_tok, H, D) or v.shape != (n_tok, H, D) or k.dtype != v.dtype:
+        raise ValueError("k, v must be [num_tokens, H_kv, D] of one dtype")
+
+
+def _slots_in(slot_mapping):
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    return slot_mapping.numel()
 
 
 def pa_cache_write_fp4(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, err=None):
@@ -495,18 +506,16 @@ def pa_cache_write_fp4(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, e
     at pool slot slot_mapping[n] of the 4-bit pools (pa_fp4_pool_shape)."""
     L = _lib.load()
     nb, B, H, D = _fp4_pools(k_cache, v_cache)
-    _cuda(k, "k")
-    _cuda(v, "v")
-    _cuda(slot_mapping, "slot_mapping")
-    if slot_mapping.dtype != torch.int64:
-        raise TypeError("slot_mapping must be int64")
-    n_tok = slot_mapping.numel()
-    if k.shape != (n_tok, H, D) or v.shape != (n_tok, H, D) or k.dtype != v.dtype:
-        raise ValueError("k, v must be [num_tokens, H_kv, D] of one dtype")
-    stream = _here(k, v, slot_mapping, k_cache, v_cache, _err_word(err))
-    _check(L.pa_cache_write_fp4(k.data_ptr(), v.data_ptr(), _dtype_code(k), slot_mapping.data_ptr(), n_tok,
-                                k_cache.data_ptr(), v_cache.data_ptr(), nb, B, H, D, float(k_scale),
-                                float(v_scale), _at(err), stream), "pa_cache_write_fp4")
+    n_tok = _slots_in(slot_mapping)
+    _kv_rows(k, v, n_tok, H, D)
+    _outs(n_tok, None, err)
+    stream = _here("k v slot_mapping k_cache v_cache err", k, v, slot_mapping, k_cache, v_cache,
+                   err)
+    _check(L.pa_cache_write_fp4(k.data_ptr(), v.data_ptr(), _dtype_code(k),
+                                slot_mapping.data_ptr(), n_tok, k_cache.data_ptr(),
+                                v_cache.data_ptr(), nb, B, H, D, k_scale, v_scale,
+                                None if err is None else err.data_ptr(), stream),
+           "pa_cache_write_fp4")
 
 
 def pa_cache_write_fp4_mapped(k, v, block_tables, token_seq, token_pos, k_cache, v_cache,
@@ -516,26 +525,17 @@ def pa_cache_write_fp4_mapped(k, v, block_tables, token_seq, token_pos, k_cache,
     slot_mapping when given.  Tokens of sequence -1 are padding (slot -1)."""
     L = _lib.load()
     nb, B, H, D = _fp4_pools(k_cache, v_cache)
-    _i32(block_tables, "block_tables")
-    _i32(token_seq, "token_seq")
-    _i32(token_pos, "token_pos")
-    _cuda(k, "k")
-    _cuda(v, "v")
-    n_tok = token_seq.numel()
-    if token_pos.numel() != n_tok:
-        raise ValueError("token_seq and token_pos differ in length")
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must be [num_seqs, stride]")
-    if k.shape != (n_tok, H, D) or v.shape != (n_tok, H, D) or k.dtype != v.dtype:
-        raise ValueError("k, v must be [num_tokens, H_kv, D] of one dtype")
-    _slots_out(slot_mapping, n_tok)
-    stream = _here(k, v, block_tables, token_seq, token_pos, k_cache, v_cache, slot_mapping, _err_word(err))
-    _check(L.pa_cache_write_fp4_mapped(k.data_ptr(), v.data_ptr(), _dtype_code(k), block_tables.data_ptr(),
-                                       block_tables.shape[1], block_tables.shape[0],
-                                       token_seq.data_ptr(), token_pos.data_ptr(), n_tok, k_cache.data_ptr(),
-                                       v_cache.data_ptr(), nb, B, H, D, float(k_scale), float(v_scale),
-                                       _at(slot_mapping), _at(err), stream),
-           "pa_cache_write_fp4_mapped")
+    n_tok = _tables(block_tables, token_seq, token_pos)
+    _kv_rows(k, v, n_tok, H, D)
+    _outs(n_tok, slot_mapping, err)
+    stream = _here("k v block_tables token_seq token_pos k_cache v_cache slot_mapping err", k, v,
+                   block_tables, token_seq, token_pos, k_cache, v_cache, slot_mapping, err)
+    stride = block_tables.shape
+    _check(L.pa_cache_write_fp4_mapped(
+        k.data_ptr(), v.data_ptr(), _dtype_code(k), block_tables.data_ptr(), stride[1], stride[0],
+        token_seq.data_ptr(), token_pos.data_ptr(), n_tok, k_cache.data_ptr(), v_cache.data_ptr(),
+        nb, B, H, D, k_scale, v_scale, None if slot_mapping is None else slot_mapping.data_ptr(),
+        None if err is None else err.data_ptr(), stream), "pa_cache_write_fp4_mapped")
     return slot_mapping
 
 
@@ -546,23 +546,22 @@ def pa_cache_read_fp4(slot_mapping, k_cache, v_cache, k_scale, v_scale, dtype=to
     held (zeros when the outputs are made here)."""
     L = _lib.load()
     nb, B, H, D = _fp4_pools(k_cache, v_cache)
-    _cuda(slot_mapping, "slot_mapping")
-    if slot_mapping.dtype != torch.int64:
-        raise TypeError("slot_mapping must be int64")
-    n_tok = slot_mapping.numel()
+    n_tok = _slots_in(slot_mapping)
     if (k_out is None) != (v_out is None):
         raise ValueError("give both of k_out and v_out, or neither")
     if k_out is None:
         k_out = torch.zeros((n_tok, H, D), dtype=dtype, device=k_cache.device)
         v_out = torch.zeros_like(k_out)
-    for t, n in ((k_out, "k_out"), (v_out, "v_out")):
-        _cuda(t, n)
-        if t.shape != (n_tok, H, D) or t.dtype != k_out.dtype:
-            raise ValueError("k_out, v_out must be [n, H_kv, D] of one dtype")
-    stream = _here(slot_mapping, k_cache, v_cache, k_out, v_out, _err_word(err))
-    _check(L.pa_cache_read_fp4(slot_mapping.data_ptr(), n_tok, k_cache.data_ptr(), v_cache.data_ptr(), nb, B, H,
-                               D, float(k_scale), float(v_scale), k_out.data_ptr(), v_out.data_ptr(),
-                               _dtype_code(k_out), _at(err), stream), "pa_cache_read_fp4")
+    if k_out.shape != (n_tok, H, D) or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+        raise ValueError("k_out, v_out must be [n, H_kv, D] of one dtype")
+    _outs(n_tok, None, err)
+    stream = _here("slot_mapping k_cache v_cache k_out v_out err", slot_mapping, k_cache, v_cache,
+                   k_out, v_out, err)
+    _check(L.pa_cache_read_fp4(slot_mapping.data_ptr(), n_tok, k_cache.data_ptr(),
+                               v_cache.data_ptr(), nb, B, H, D, k_scale, v_scale,
+                               k_out.data_ptr(), v_out.data_ptr(), _dtype_code(k_out),
+                               None if err is None else err.data_ptr(), stream),
+           "pa_cache_read_fp4")
     return k_out, v_out
 
 
@@ -573,31 +572,32 @@ def pa_decode_fp4(q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v
     to tokens [max(0, T - window), T); 0: to all of them."""
     L = _lib.load()
     nb, B, H, D = _fp4_pools(k_cache, v_cache)
-    _cuda(q, "q")
-    _i32(block_tables, "block_tables")
-    _i32(seq_lens, "seq_lens")
-    if q.dim() != 3 or q.shape[2] != D:
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise TypeError("block_tables and seq_lens must be int32")
+    shape, table = q.shape, block_tables.shape
+    if len(shape) != 3 or shape[2] != D:
         raise ValueError("q must be [N, Hq, D]")
-    N, Hq, _ = q.shape
-    if block_tables.dim() != 2 or block_tables.shape[0] != N or seq_lens.numel() != N:
+    N, Hq, _ = shape
+    if len(table) != 2 or table[0] != N or seq_lens.numel() != N:
         raise ValueError("block_tables must be [N, stride] and seq_lens [N]")
     code = _dtype_code(q)
     if out is None:
         out = torch.empty_like(q)
-    _cuda(out, "out")
-    if out.shape != q.shape or out.dtype != q.dtype:
+    elif out.shape != shape or out.dtype != q.dtype:
         raise ValueError("out must be [N, Hq, D] of q's dtype")
     if workspace is None:
         nbytes = pa_decode_workspace_size(Hq, H, D, B, PA_FP4_E2M1, flags, num_ctas)
         # zero-filled once; the decode leaves it ready for the next call
         workspace = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=q.device)
-    _cuda(workspace, "workspace")
-    stream = _here(q, k_cache, v_cache, block_tables, seq_lens, out, workspace, _err_word(err))
-    _check(L.pa_decode_fp4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(),
-                           block_tables.shape[1], seq_lens.data_ptr(), N, Hq, H, D, B, nb, code,
-                           float(scale), float(k_scale), float(v_scale), int(window), out.data_ptr(),
+    _outs(N, None, err)
+    stream = _here("q k_cache v_cache block_tables seq_lens out workspace err", q, k_cache, v_cache,
+                   block_tables, seq_lens, out, workspace, err)
+    _check(L.pa_decode_fp4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                           block_tables.data_ptr(), table[1], seq_lens.data_ptr(), N, Hq, H, D, B,
+                           nb, code, scale, k_scale, v_scale, window, out.data_ptr(),
                            workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                           int(flags), int(num_ctas), _at(err), stream), "pa_decode_fp4")
+                           flags, num_ctas, None if err is None else err.data_ptr(), stream),
+           "pa_decode_fp4")
     return out
 
 

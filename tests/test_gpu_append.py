@@ -203,6 +203,43 @@ def test_append_norms(cuda_device, shape, norm):
             _same_pools(qt, qt.stored(k, qt.rows("v")))
 
 
+@pytest.mark.parametrize("kind", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("dtype", [W.BF16, W.F16])
+def test_quantized_stores_of_every_16_bit_value(cuda_device, dtype, kind):
+    """Every finite 16-bit pattern as a key, in groups of any neighbours and in
+    groups of like magnitudes, at scales in and far outside the common range:
+    the quotients are the correctly rounded ones, so every code is the oracle's."""
+    rng = np.random.default_rng(9)
+    bits = np.arange(65536, dtype=np.uint32).astype(np.uint16)
+    with np.errstate(invalid="ignore"):
+        finite = np.isfinite(bits_to_f64(bits, dtype))
+    bits[~finite] = W.to_bits(np.float32(1.0), dtype)
+    near = bits[np.argsort(np.abs(bits_to_f64(bits, dtype)), kind="stable")]
+    k = np.concatenate((rng.permutation(bits), near)).reshape(256, 4, 128)
+    n = len(k)
+    zeros = torch.zeros(n, dtype=torch.int32, device="cuda")
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    table = torch.arange(n // 16, dtype=torch.int32, device="cuda")[None].contiguous()
+    dk = to_dev(k, dtype)
+    for scale in (1.0, 0.0371, 2.0 ** -20, 1.5e-30, 3e-37, 7.7e8, 2e30, 5e37):
+        scale = float(np.float32(scale))
+        shape = (n // 16, 16, 4, 128) if kind == "e4m3" else pa.pa_fp4_pool_shape(n // 16, 16, 4, 128)
+        kc, vc = (torch.full(shape, 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2))
+        pa.pa_append_rope(None, dk, dk, None, table, zeros, pos, kc, vc, k_scale=scale, v_scale=1.0)
+        want = [np.full(shape, 0x7F, np.uint8) for _ in range(2)]
+        if kind == "e4m3":
+            oracle.cache_write_fp8(want[0], want[1], k, k, dtype, np.arange(n), scale, 1.0)
+            assert np.array_equal(kc.cpu().numpy() & 0x7F, want[0] & 0x7F), scale
+            assert np.array_equal(oracle.e4m3_decode(vc.cpu().numpy()), oracle.e4m3_decode(want[1]))
+        else:
+            x = bits_to_f64(k, dtype).astype(np.float32)
+            oracle.cache_write_fp4(want[0], want[1], x, x, np.arange(n), scale, 1.0)
+            got = kc.cpu().numpy()
+            assert np.array_equal(got.reshape(n // 16, 4, -1)[..., 16 * 64:],
+                                  want[0].reshape(n // 16, 4, -1)[..., 16 * 64:]), scale
+            assert np.array_equal(oracle.fp4_dequant(got, 128), oracle.fp4_dequant(want[0], 128)), scale
+
+
 def test_append_padding_and_bad_tokens_write_nothing(cuda_device):
     for kind in KINDS:
         st = Step(301, W.BF16, 8, 2, 128, 16, [5, 20, 100], [4, 30, 7], kind, 128, pad=(0, 11, 40))

@@ -14,6 +14,7 @@ def test_e2m1_codes_and_ties():
     assert oracle.e2m1_encode(np.array(mids) * (1 + 2.0 ** -20)).tolist() == [1, 2, 3, 4, 5, 6, 7]
     assert oracle.e2m1_encode(np.array(mids) * (1 - 2.0 ** -20)).tolist() == [0, 1, 2, 3, 4, 5, 6]
     assert oracle.e2m1_encode([7.0, 1e9, -6.5, -0.5]).tolist() == [7, 7, 15, 9]
+    assert oracle.e2m1_encode([1e30, -3e38, np.inf, -np.inf]).tolist() == [7, 15, 7, 15]
     assert np.array_equal(oracle.e2m1_decode(range(16))[8:], -oracle._E2M1)
 
 
