@@ -133,14 +133,17 @@ struct Walk {
   }
 };
 
-// One warp's state over a range of one context's tiles.
-template <int D, bool kBF16, int NH>
+// One warp's state over a range of one context's tiles.  kTwin (binary16
+// outputs, at most 4 query heads): the 8 head columns hold the heads twice, the
+// first copy's weights rounded to binary16, the second's what that rounding
+// left, so that the pair costs no second product; the two are added at the end.
+template <int D, bool kBF16, int NH, bool kTwin>
 struct Context {
   static constexpr int KS = D / 16;        // k-steps of S^T
   static constexpr int MT = D / 16;        // m-tiles of O^T
   static constexpr int KW = D / 32;        // words of K codes per lane and row
   static constexpr int VW = D / 64;        // words of V codes per lane and row
-  static constexpr bool kPair = !kBF16;    // weights as a pair of binary16 values
+  static constexpr bool kPair = !kBF16 && !kTwin;   // weights as a pair, two products
   uint32_t qb[NH][KS][2];
   float sl[NH][2];                         // score factor of heads 8 nh + 2 tig + e (log2)
   float o[NH][MT][4];
@@ -156,7 +159,7 @@ struct Context {
     const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
 #pragma unroll
     for (int nh = 0; nh < NH; ++nh) {
-      const int h = 8 * nh + gid;
+      const int h = kTwin ? (gid & 3) : 8 * nh + gid;
       uint32_t w[D / 8];
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -283,8 +286,11 @@ struct Context {
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
           x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-          // without weights so far the base goes anywhere, else only up
-          const bool fresh = l[nh][e] == 0.f;
+          // without weights so far the base goes anywhere, else only up (a
+          // second copy goes with its first)
+          float sum = l[nh][e];
+          if constexpr (kTwin) sum = __shfl_sync(kFull, sum, threadIdx.x & 29);
+          const bool fresh = sum == 0.f;
           float d = x - kShift;
           if (x == -INFINITY || (!fresh && d < 0.f)) d = 0.f;
           set = set && (!fresh || x > -INFINITY);
@@ -315,7 +321,12 @@ struct Context {
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const float p0 = ex2_approx(s[hf][nh][2 * r]), p1 = ex2_approx(s[hf][nh][2 * r + 1]);
-          const uint32_t pk = pack2<false>(p0, p1);
+          uint32_t pk = pack2<false>(p0, p1);
+          if constexpr (kTwin) {
+            const float2 f = unpack2<false>(pk);
+            const bool rest = (threadIdx.x & 2) != 0;   // the heads' second copy
+            pk = pack2<false>(p0 - (rest ? f.x : 0.f), p1 - (rest ? f.y : 0.f));
+          }
           if constexpr (kPair) {
             const float2 f = unpack2<false>(pk);
             pl[hf][nh][r] = movmatrix_trans(pack2<false>(p0 - f.x, p1 - f.y));
@@ -375,6 +386,21 @@ struct Context {
               mma_16816<false>(o[nh][4 * w + b], x0, x1, x2, x3, pl[hf][nh][0], pl[hf][nh][1]);
           }
         }
+      }
+    }
+  }
+
+  // the end of a context, or of a part: the heads' two copies become one
+  __device__ __forceinline__ void finish() {
+    if constexpr (kTwin) {
+#pragma unroll
+      for (int nh = 0; nh < NH; ++nh) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) l[nh][e] += __shfl_xor_sync(kFull, l[nh][e], 2);
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[nh][i][e] += __shfl_xor_sync(kFull, o[nh][i][e], 2);
       }
     }
   }
@@ -478,7 +504,7 @@ struct Shared {
   Part merge[2];
 };
 
-template <int D, bool kBF16, int NH>
+template <int D, bool kBF16, int NH, bool kTwin>
 __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
     decode_fp4_kernel(const Args a) {
   // per warp kStages tiles of K and V; after the last tile: [2 * kWarps] records
@@ -495,6 +521,20 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
     fence_barrier_init();
   }
 
+  // The small inputs towards L2 while the previous kernel in the stream drains
+  // (a prefetch returns no data: that kernel may still be writing them).
+  {
+    const size_t step = (size_t)gridDim.x * kThreads * 128;
+    const size_t at = ((size_t)blockIdx.x * kThreads + tid) * 128;
+    const size_t sl_bytes = (size_t)a.num_seqs * 4, bt_bytes = sl_bytes * a.stride;
+    const size_t q_bytes = (size_t)a.num_seqs * a.Hq * D * 2;
+    for (size_t o = at; o < sl_bytes; o += step)
+      prefetch_l2(reinterpret_cast<const char*>(a.seq_lens) + o);
+    for (size_t o = at; o < bt_bytes; o += step)
+      prefetch_l2(reinterpret_cast<const char*>(a.bt) + o);
+    for (size_t o = at; o < q_bytes; o += step)
+      prefetch_l2(reinterpret_cast<const char*>(a.q) + o);
+  }
   if (!a.early_tables) grid_dep_wait();
   // ---- every thread counts the tiles of a run of sequences -----------------
   const int per = (a.num_seqs + kThreads - 1) / kThreads;
@@ -657,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
       }
     }
 
-    Context<D, kBF16, NH> cx;
+    Context<D, kBF16, NH, kTwin> cx;
     const int ahead = min(kStages, n_tiles);
     for (int n = 0; n < ahead; ++n) issue(n);
     int st = 0, seg_k0 = w.k, segments = 0;
@@ -703,6 +743,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
       if (n == n_tiles - 1 || w.k == w.nt - 1) {
         // the end of the context, or of this warp's part of it.  The warp's last
         // part goes where its tiles were, an earlier one to the warp's slot.
+        cx.finish();
         if (seg_k0 == 0 && w.k == w.nt - 1) {
           cx.write(a.out + ((size_t)w.i * a.Hq + (size_t)w.h * a.G) * D, a.G, a.v_scale);
         } else {
@@ -740,16 +781,18 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
 
   // ---- parts of one context held by this block's warps ---------------------
   // parts are in tile order; those of one context follow each other
-  if (tid == 0) {
-    int n = 0;
-    long long last = -1;
-    for (int k = 0; k < 2 * kWarps; ++k) {
-      if (sh.part[k].pair < 0) continue;
-      if (sh.part[k].pair != last) sh.group_first[n++] = k;
-      last = sh.part[k].pair;
+  if (warp == 0) {
+    const bool held = lane < 2 * kWarps && sh.part[lane].pair >= 0;
+    const uint32_t all = __ballot_sync(kFull, held);
+    const uint32_t before = all & ((1u << lane) - 1u);
+    const bool starts =
+        held && (before == 0u || sh.part[31 - __clz(before)].pair != sh.part[lane].pair);
+    const uint32_t firsts = __ballot_sync(kFull, starts);
+    if (starts) sh.group_first[__popc(firsts & ((1u << lane) - 1u))] = lane;
+    if (lane == 0) {
+      sh.groups = __popc(firsts);
+      sh.group_first[__popc(firsts)] = 2 * kWarps;
     }
-    sh.group_first[n] = 2 * kWarps;
-    sh.groups = n;
   }
   __syncthreads();
   const int cols = D / 4, per_group = a.G * cols;
@@ -779,18 +822,16 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
   }
   __syncthreads();
   // ---- contexts cut between blocks: count this block's record --------------
-  if (tid == 0) {
-    for (int gr = 0; gr < sh.groups; ++gr) {
-      const Part p = sh.part[sh.group_first[gr]];
-      // inside this block's range: already written
-      if (p.g0 >= c0 && p.g0 + p.nt <= c1) continue;
+  if (tid < sh.groups) {
+    const Part p = sh.part[sh.group_first[tid]];
+    if (p.g0 < c0 || p.g0 + p.nt > c1) {   // else inside this block's range: already written
       const long long f = ((p.g0 + 1) * nb - 1) / U, e = ((p.g0 + p.nt) * nb - 1) / U;
       uint32_t* cnt = a.ws_count + e;
       // releases the block's record (ordered before by the barrier), acquires
       // those counted before it
       if (atom_add_acq_rel_gpu(cnt, 1u) + 1u == (uint32_t)(e - f + 1)) {
         *cnt = 0u;   // ready for the next call
-        sh.merge[sh.merges++] = p;
+        sh.merge[atomicAdd(&sh.merges, 1)] = p;
       }
     }
   }
@@ -815,13 +856,10 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
 typedef void (*Kernel)(const Args);
 
 template <int D>
-Kernel pick_d(bool bf16, bool hi) {
-  return bf16 ? (hi ? decode_fp4_kernel<D, true, 2> : decode_fp4_kernel<D, true, 1>)
-              : (hi ? decode_fp4_kernel<D, false, 2> : decode_fp4_kernel<D, false, 1>);
-}
-
-Kernel pick(int D, bool bf16, bool hi) {
-  return D == 64 ? pick_d<64>(bf16, hi) : pick_d<128>(bf16, hi);
+Kernel pick_d(bool bf16, int G) {
+  if (bf16) return G > 8 ? decode_fp4_kernel<D, true, 2, false> : decode_fp4_kernel<D, true, 1, false>;
+  return G > 8 ? decode_fp4_kernel<D, false, 2, false>
+               : (G > 4 ? decode_fp4_kernel<D, false, 1, false> : decode_fp4_kernel<D, false, 1, true>);
 }
 
 // the ring of every warp (which its last part's record shares) and a slot each
@@ -859,7 +897,7 @@ int make_plan(int Hq, int H, int D, int B, int q_dtype, int flags, int num_ctas,
   if (flags == PA_DECODE_SIMT) return PA_ERR_UNSUPPORTED;
   if (flags != PA_DECODE_AUTO && flags != PA_DECODE_MMA) return PA_ERR_INVALID_ARG;
   const bool bf16 = q_dtype == PA_BF16;
-  p->kern = pick(D, bf16, G > 8);
+  p->kern = D == 64 ? pick_d<64>(bf16, G) : pick_d<128>(bf16, G);
   p->smem = smem_bytes(D, G);
   DeviceInfo di;
   if (int rc = current_device_info(&di)) return rc;
