@@ -54,8 +54,17 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;                 // tokens per tile
 constexpr int kStages = 2;                // tiles in shared memory per warp
+// A context's share of the work is its tiles and kStart for its start and end
+// (queries to fragments, the write): without it a warp whose range holds many
+// short contexts finishes last (91.9 against 67.7 us for 64 contexts of 1 to
+// 2,048 tokens and 32 heads; 2 and 3 measured 69.2 and 70.7).
+constexpr int kStart = 1;
+// Contexts of at most kWhole tiles go to one warp each when there are warps
+// enough: a warp takes 0.3 us a tile alone, joining parts costs 3 us.
+constexpr int kWhole = 8;
 constexpr int kBlocksPerSm = 3;
 constexpr uint32_t kFull = 0xffffffffu;
+constexpr int kUnitBits = 44, kCounted = 1 << 18;   // of the scanned sums; sequences it counts
 // Weights are exp2(x - base) with base = a maximum less kShift, and a new base
 // once they pass exp2(kShift + kLag) = 2^15, inside binary16's range.  binary16
 // keeps its full precision down to 2^-14, so the shift moves the loss of small
@@ -486,7 +495,7 @@ struct Merged {
 // A context's part held by one warp.
 struct Part {
   long long pair;     // sequence * H + head, or -1
-  long long g0;       // index of the context's first tile
+  long long g0;       // unit of the context's first tile
   int nt;             // its tiles
   int begins, ends;   // the part starts / ends with the context
   int rec;            // its record, in floats from the start of shared memory
@@ -495,6 +504,7 @@ struct Part {
 struct Shared {
   long long run_pref[kThreads];   // tiles (of one head) before each thread's run of sequences
   long long warp_tot[kWarps];
+  int warp_longest[kWarps];
   Part part[2 * kWarps];
   unsigned long long full[kWarps][kStages];   // a stage's copies have landed
   uint32_t bad[kWarps][kStages];              // its blocks without a valid table entry
@@ -540,10 +550,14 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
   const int per = (a.num_seqs + kThreads - 1) / kThreads;
   const int run0 = min(a.num_seqs, tid * per), run1 = min(a.num_seqs, run0 + per);
   long long mine = 0;
+  int longest = 0;
   bool odd = false;   // this block has to report or zero one of the run's sequences
   for (int i = run0; i < run1; ++i) {
     const int T = clamp_len(__ldg(a.seq_lens + i), a);
-    mine += num_tiles(T, a);
+    // units, and above them the number of contexts that are not empty
+    const int nt = num_tiles(T, a);
+    longest = max(longest, nt);
+    if (nt > 0) mine += nt + kStart + (i < kCounted ? 1ll << kUnitBits : 0ll);
     odd |= T == 0 && (i % gridDim.x) == blockIdx.x;
   }
   long long incl = mine;
@@ -552,7 +566,11 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
     const long long n = __shfl_up_sync(kFull, incl, s);
     if (lane >= s) incl += n;
   }
-  if (lane == 31) sh.warp_tot[warp] = incl;
+  longest = __reduce_max_sync(kFull, longest);
+  if (lane == 31) {
+    sh.warp_tot[warp] = incl;
+    sh.warp_longest[warp] = longest;
+  }
   if (tid < 2 * kWarps) sh.part[tid].pair = -1;
   if (tid == 0) sh.merges = 0;
   __syncthreads();
@@ -561,8 +579,15 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) off += sh.warp_tot[w];
     total += sh.warp_tot[w];
+    longest = max(longest, sh.warp_longest[w]);
   }
-  sh.run_pref[tid] = off + incl - mine;
+  // one context a warp (a unit is a context then)?
+  const long long contexts = (total >> kUnitBits) * a.H;
+  const bool whole = longest <= kWhole && a.num_seqs <= kCounted &&
+                     contexts <= (long long)gridDim.x * kWarps;
+  const long long low = (1ll << kUnitBits) - 1;
+  const long long before = off + incl - mine;
+  sh.run_pref[tid] = whole ? before >> kUnitBits : before & low;
   __syncthreads();
   if (a.early_tables) grid_dep_wait();
   if (tid == 0) grid_dep_launch();
@@ -577,10 +602,10 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
       }
     }
 
-  // ---- this block's and this warp's range of tiles -------------------------
-  // at least kWarps tiles a block, so that small batches do not split contexts
+  // ---- this block's and this warp's range of units -------------------------
+  // at least kWarps units a block, so that small batches do not split contexts
   // between blocks for nothing
-  const long long U = total * a.H;
+  const long long U = whole ? contexts : (total & low) * a.H;
   const long long nb = min((long long)gridDim.x, (U + kWarps - 1) / kWarps);
   if ((long long)blockIdx.x >= nb) return;
   const long long c0 = U * blockIdx.x / nb, c1 = U * (blockIdx.x + 1) / nb;
@@ -589,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
   const long long g_end = c0 + n_cta * (warp + 1) / kWarps;
 
   if (g < g_end) {
-    // the sequence of tile g: the last run that starts at or before it, then
+    // the sequence of unit g: the last run that starts at or before it, then
     // along the run
     int r = 0;
 #pragma unroll
@@ -599,17 +624,31 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
     w.i = r * per;
     w.load_seq(a);
     long long rem = g - sh.run_pref[r] * a.H;
-    while (w.i < a.num_seqs && rem >= (long long)w.nt * a.H) {
-      rem -= (long long)w.nt * a.H;
+    auto units = [&]() { return w.nt == 0 ? 0 : (whole ? 1 : w.nt + kStart); };   // of a head
+    while (w.i < a.num_seqs && rem >= (long long)units() * a.H) {
+      rem -= (long long)units() * a.H;
       ++w.i;
       w.load_seq(a);
     }
     const bool sound = w.i < a.num_seqs && rem >= 0;
-    w.h = sound ? (int)(rem / w.nt) : 0;
-    w.k = sound ? (int)(rem % w.nt) : 0;
     // only if seq_lens changes during the call: never walk blind
     if (!sound) set_error(a.err, PA_DEVERR_SEQ_LEN);
-    const int n_tiles = sound ? (int)(g_end - g) : 0;
+    int left = 0;   // units to go, the tile's among them
+    w.h = w.k = 0;
+    if (sound) {
+      w.h = (int)(rem / units());
+      if (whole) {
+        left = w.nt;
+      } else {
+        // a context's first kStart units are its start: the range begins with
+        // its first tile, if it reaches that far.  g: the unit of the tile
+        const int in_head = (int)(rem % units());
+        w.k = max(0, in_head - kStart);
+        g += w.k + kStart - in_head;
+        if (g < g_end) left = (int)(g_end - g);
+      }
+    }
+    int ld_left = left;
 
     // ---- the copies: K and V of a tile into stage n % kStages --------------
     // A block of up to 32 tokens is copied whole, plane by plane; of a larger
@@ -674,9 +713,11 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
         bulk_load(dst0 + st * kStage, src, bytes, full + 8 * st);
       }
       l_t0 += kTile;
+      --ld_left;
       if (++ld.k == ld.nt) {
         --ld.k;
         ld.advance(a);
+        ld_left -= kStart;
         if (ld.nt > 0) load_context();
       }
     };
@@ -698,14 +739,15 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
     }
 
     Context<D, kBF16, NH, kTwin> cx;
-    const int ahead = min(kStages, n_tiles);
-    for (int n = 0; n < ahead; ++n) issue(n);
+    for (int n = 0; n < kStages; ++n)
+      if (ld_left > 0) issue(n);
     int st = 0, seg_k0 = w.k, segments = 0;
     int first = 0, t0 = 0;   // of the tile's context and tile
     uint32_t ph = 0;
-    bool live_warp = true;
-    for (int n = 0; n < n_tiles; ++n) {
-      if (n == 0 || w.k == 0) {
+    bool live_warp = true, fresh = true;
+    while (left > 0) {
+      if (fresh) {
+        fresh = false;
         seg_k0 = w.k;
         first = first_token(w.T, a);
         t0 = (first / kTile + w.k) * kTile;
@@ -738,26 +780,27 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
           cx.template values<false>(pb, pl, kFull, vc, vs);
         }
         __syncwarp();   // every lane has read the stage
-        if (n + kStages < n_tiles) issue(st);
+        if (ld_left > 0) issue(st);
       }
-      if (n == n_tiles - 1 || w.k == w.nt - 1) {
+      const bool ends = w.k == w.nt - 1;
+      if (ends || left == 1) {
         // the end of the context, or of this warp's part of it.  The warp's last
         // part goes where its tiles were, an earlier one to the warp's slot.
         cx.finish();
-        if (seg_k0 == 0 && w.k == w.nt - 1) {
+        if (seg_k0 == 0 && ends) {
           cx.write(a.out + ((size_t)w.i * a.Hq + (size_t)w.h * a.G) * D, a.G, a.v_scale);
         } else {
-          const int rec = n == n_tiles - 1
+          const int rec = left <= (ends ? 1 + kStart : 1)
                               ? warp * (kStages * kStage / 4)
                               : kWarps * (kStages * kStage / 4) + warp * (int)rf;
           if (live_warp) cx.store(slots + rec, a.G);
           if (lane == 0) {
             Part& p = sh.part[2 * warp + (segments > 0 ? 1 : 0)];
             p.pair = (long long)w.i * a.H + w.h;
-            p.g0 = g + n - w.k;
+            p.g0 = g - w.k;
             p.nt = w.nt;
             p.begins = seg_k0 == 0;
-            p.ends = w.k == w.nt - 1;
+            p.ends = ends;
             p.rec = rec;
           }
         }
@@ -768,9 +811,15 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
         ph ^= 1u;
       }
       t0 += kTile;
-      if (++w.k == w.nt) {
-        --w.k;
+      --left;
+      ++g;
+      if (ends) {
         w.advance(a);
+        left -= kStart;
+        g += kStart;
+        fresh = true;
+      } else {
+        ++w.k;
       }
     }
     if (!live_warp)   // leave with no copy in flight
