@@ -72,8 +72,8 @@ __device__ __forceinline__ long long append_slot(const AppendArgs& a, long long 
   const int i = __ldg(a.tok_seq + tok);
   pos = __ldg(a.tok_pos + tok);
   if (i == -1) return -1;
-  if (i < 0 || i >= a.num_seqs || pos < 0 || (long long)pos >= ((long long)a.stride << a.log2B) ||
-      (a.rot > 0 && pos >= a.max_pos)) {
+  if (i < 0 || i >= a.num_seqs || pos < 0 ||
+      (long long)pos >= ((long long)a.stride << a.log2B) || (a.rot > 0 && pos >= a.max_pos)) {
     if (report) set_error(a.err, PA_DEVERR_POSITION);
     return -1;
   }
@@ -210,9 +210,12 @@ struct Turn {
 #pragma unroll
       for (int i = 0; i < 4; ++i) p[i] = {y[i].y, y[i].x};
     } else {
-      widen<kBF16>(make_uint4(__shfl_sync(0xffffffffu, x.x, from), __shfl_sync(0xffffffffu, x.y, from),
-                              __shfl_sync(0xffffffffu, x.z, from), __shfl_sync(0xffffffffu, x.w, from)),
-                   p);
+      uint4 o;
+      o.x = __shfl_sync(0xffffffffu, x.x, from);
+      o.y = __shfl_sync(0xffffffffu, x.y, from);
+      o.z = __shfl_sync(0xffffffffu, x.z, from);
+      o.w = __shfl_sync(0xffffffffu, x.w, from);
+      widen<kBF16>(o, p);
     }
   }
 };

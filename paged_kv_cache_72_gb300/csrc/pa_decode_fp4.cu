@@ -665,7 +665,8 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
     const bool mine = lane < 16 && piece < pieces;
     const uint8_t* const pool = lane < 8 ? a.kc : a.vc;
     const uint32_t bytes = !large ? bs * kRow : (piece == 0 ? kTile * (D / 2) : kTile * (D / 16));
-    const uint32_t dst0 = ring + (lane < 8 ? 0 : kPart) + (large ? piece * (kTile * (D / 2)) : piece * bytes);
+    const uint32_t dst0 = ring + (lane < 8 ? 0 : kPart) +
+                          (large ? piece * (kTile * (D / 2)) : piece * bytes);
     const long long block_bytes = (long long)a.H * a.plane;
     int l_first = 0, l_t0 = 0, l_last = 0;   // of the context being loaded
     int win = -1, ent = -1;                  // entries [32 win, 32 win + 32) of its table row
@@ -906,9 +907,10 @@ typedef void (*Kernel)(const Args);
 
 template <int D>
 Kernel pick_d(bool bf16, int G) {
-  if (bf16) return G > 8 ? decode_fp4_kernel<D, true, 2, false> : decode_fp4_kernel<D, true, 1, false>;
-  return G > 8 ? decode_fp4_kernel<D, false, 2, false>
-               : (G > 4 ? decode_fp4_kernel<D, false, 1, false> : decode_fp4_kernel<D, false, 1, true>);
+  if (bf16)
+    return G > 8 ? decode_fp4_kernel<D, true, 2, false> : decode_fp4_kernel<D, true, 1, false>;
+  if (G > 8) return decode_fp4_kernel<D, false, 2, false>;
+  return G > 4 ? decode_fp4_kernel<D, false, 1, false> : decode_fp4_kernel<D, false, 1, true>;
 }
 
 // the ring of every warp (which its last part's record shares) and a slot each

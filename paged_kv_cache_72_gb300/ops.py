@@ -88,11 +88,19 @@ def _fp4_pools(k_cache, v_cache):
     return nb, B, H, _FP4_HEAD_DIM[row]
 
 
+_CODE = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
+
+
 def _block_pools(k_cache, v_cache):
     """(num_blocks, B, H_kv, D, dtype code) of pools of any element type."""
-    a, b, c, d = _pool_shape(k_cache, v_cache)
-    if k_cache.dtype != torch.uint8:
-        return a, b, c, d, _dtype_code(k_cache)
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype != dtype:
+        raise ValueError("k_cache and v_cache must share one shape [num_blocks, B, H_kv, D]")
+    a, b, c, d = shape
+    if dtype in _CODE:
+        return a, b, c, d, _CODE[dtype]
+    if dtype != torch.uint8:
+        raise TypeError("expected float16, bfloat16 or uint8 pools, got %s" % dtype)
     if d in _FP4_HEAD_DIM:
         return a, c, b, _FP4_HEAD_DIM[d], PA_FP4_E2M1
     return a, b, c, d, PA_FP8_E4M3
@@ -104,10 +112,9 @@ def _raw_stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _here(names, *tensors):
-    """The current stream, after checking that every tensor given (not None) is
-    contiguous and on the current device.  names: theirs, space-separated."""
-    dev = torch.cuda.current_device()
+def _here(dev, names, *tensors):
+    """The stream of the current device dev, after checking that every tensor
+    given (not None) is contiguous and on it.  names: theirs, space-separated."""
     for t in tensors:
         if t is not None and (t.get_device() != dev or not t.is_contiguous()):
             for n, u in zip(names.split(), tensors):
@@ -217,6 +224,7 @@ def pa_copy_blocks(pairs, k_cache, v_cache, err=None):
 
     Pools of float16 / bfloat16 elements, uint8 E4M3 codes, or 4-bit pools."""
     L = _lib.load()
+    _pool_shape(k_cache, v_cache)
     nb, B, H, D, code = _block_pools(k_cache, v_cache)
     _cuda(pairs, "pairs")
     if pairs.dtype != torch.int32:
@@ -243,6 +251,7 @@ def pa_swap_blocks(pairs, src_k, src_v, dst_k, dst_v, err=None):
     for t in (host_k, host_v):
         if not t.is_contiguous():
             raise ValueError("the host pools must be contiguous")
+    _pool_shape(dev_k, dev_v)
     nbd, B, H, D, code = _block_pools(dev_k, dev_v)
     if host_k.shape[1:] != dev_k.shape[1:] or host_k.dtype != dev_k.dtype or \
             host_v.shape != host_k.shape or host_v.dtype != host_k.dtype:
@@ -448,8 +457,8 @@ def pa_append_rope(q, k, v, cos_sin, block_tables, token_seq, token_pos, k_cache
     n_tok = _tables(block_tables, token_seq, token_pos)
     _outs(n_tok, slot_mapping, err)
     dtype = k.dtype
-    if k_cache.dtype != dtype and code not in (PA_FP8_E4M3, PA_FP4_E2M1):
-        raise TypeError("the pools must be of k's dtype, or uint8")
+    if dtype not in _CODE or (code < PA_FP8_E4M3 and code != _CODE[dtype]):
+        raise TypeError("k must be float16 or bfloat16, and the pools of its dtype or uint8")
     dev = torch.cuda.current_device()
     ks = _token_rows(k, "k", n_tok, H, D, dtype, dev)
     vs = _token_rows(v, "v", n_tok, H, D, dtype, dev)
@@ -472,13 +481,13 @@ def pa_append_rope(q, k, v, cos_sin, block_tables, token_seq, token_pos, k_cache
     for g in (q_norm, k_norm):
         if g is not None and (g.shape != (D,) or g.dtype != dtype):
             raise ValueError("q_norm and k_norm must be [D] of k's dtype")
-    stream = _here("cos_sin q_norm k_norm block_tables token_seq token_pos k_cache v_cache q_out "
-                   "slot_mapping err", cos_sin, q_norm, k_norm, block_tables, token_seq, token_pos,
-                   k_cache, v_cache, q_out, slot_mapping, err)
+    stream = _here(dev, "cos_sin q_norm k_norm block_tables token_seq token_pos k_cache v_cache "
+                   "q_out slot_mapping err", cos_sin, q_norm, k_norm, block_tables, token_seq,
+                   token_pos, k_cache, v_cache, q_out, slot_mapping, err)
     stride = block_tables.shape
     _check(L.pa_append_rope(
         None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-        _dtype_code(k), None if cos_sin is None else cos_sin.data_ptr(), rot, max_pos,
+        _CODE[dtype], None if cos_sin is None else cos_sin.data_ptr(), rot, max_pos,
         1 if interleaved else 0, None if q_norm is None else q_norm.data_ptr(),
         None if k_norm is None else k_norm.data_ptr(), eps, block_tables.data_ptr(), stride[1],
         stride[0], token_seq.data_ptr(), token_pos.data_ptr(), n_tok,
@@ -509,8 +518,8 @@ def pa_cache_write_fp4(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, e
     n_tok = _slots_in(slot_mapping)
     _kv_rows(k, v, n_tok, H, D)
     _outs(n_tok, None, err)
-    stream = _here("k v slot_mapping k_cache v_cache err", k, v, slot_mapping, k_cache, v_cache,
-                   err)
+    stream = _here(torch.cuda.current_device(), "k v slot_mapping k_cache v_cache err", k, v,
+                   slot_mapping, k_cache, v_cache, err)
     _check(L.pa_cache_write_fp4(k.data_ptr(), v.data_ptr(), _dtype_code(k),
                                 slot_mapping.data_ptr(), n_tok, k_cache.data_ptr(),
                                 v_cache.data_ptr(), nb, B, H, D, k_scale, v_scale,
@@ -528,8 +537,9 @@ def pa_cache_write_fp4_mapped(k, v, block_tables, token_seq, token_pos, k_cache,
     n_tok = _tables(block_tables, token_seq, token_pos)
     _kv_rows(k, v, n_tok, H, D)
     _outs(n_tok, slot_mapping, err)
-    stream = _here("k v block_tables token_seq token_pos k_cache v_cache slot_mapping err", k, v,
-                   block_tables, token_seq, token_pos, k_cache, v_cache, slot_mapping, err)
+    stream = _here(torch.cuda.current_device(), "k v block_tables token_seq token_pos k_cache "
+                   "v_cache slot_mapping err", k, v, block_tables, token_seq, token_pos, k_cache,
+                   v_cache, slot_mapping, err)
     stride = block_tables.shape
     _check(L.pa_cache_write_fp4_mapped(
         k.data_ptr(), v.data_ptr(), _dtype_code(k), block_tables.data_ptr(), stride[1], stride[0],
@@ -555,8 +565,8 @@ def pa_cache_read_fp4(slot_mapping, k_cache, v_cache, k_scale, v_scale, dtype=to
     if k_out.shape != (n_tok, H, D) or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
         raise ValueError("k_out, v_out must be [n, H_kv, D] of one dtype")
     _outs(n_tok, None, err)
-    stream = _here("slot_mapping k_cache v_cache k_out v_out err", slot_mapping, k_cache, v_cache,
-                   k_out, v_out, err)
+    stream = _here(torch.cuda.current_device(), "slot_mapping k_cache v_cache k_out v_out err",
+                   slot_mapping, k_cache, v_cache, k_out, v_out, err)
     _check(L.pa_cache_read_fp4(slot_mapping.data_ptr(), n_tok, k_cache.data_ptr(),
                                v_cache.data_ptr(), nb, B, H, D, k_scale, v_scale,
                                k_out.data_ptr(), v_out.data_ptr(), _dtype_code(k_out),
@@ -590,8 +600,8 @@ def pa_decode_fp4(q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v
         # zero-filled once; the decode leaves it ready for the next call
         workspace = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=q.device)
     _outs(N, None, err)
-    stream = _here("q k_cache v_cache block_tables seq_lens out workspace err", q, k_cache, v_cache,
-                   block_tables, seq_lens, out, workspace, err)
+    stream = _here(torch.cuda.current_device(), "q k_cache v_cache block_tables seq_lens out "
+                   "workspace err", q, k_cache, v_cache, block_tables, seq_lens, out, workspace, err)
     _check(L.pa_decode_fp4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                            block_tables.data_ptr(), table[1], seq_lens.data_ptr(), N, Hq, H, D, B,
                            nb, code, scale, k_scale, v_scale, window, out.data_ptr(),

@@ -223,7 +223,9 @@ def test_quantized_stores_of_every_16_bit_value(cuda_device, dtype, kind):
     dk = to_dev(k, dtype)
     for scale in (1.0, 0.0371, 2.0 ** -20, 1.5e-30, 3e-37, 7.7e8, 2e30, 5e37):
         scale = float(np.float32(scale))
-        shape = (n // 16, 16, 4, 128) if kind == "e4m3" else pa.pa_fp4_pool_shape(n // 16, 16, 4, 128)
+        shape = pa.pa_fp4_pool_shape(n // 16, 16, 4, 128)
+        if kind == "e4m3":
+            shape = (n // 16, 16, 4, 128)
         kc, vc = (torch.full(shape, 0x7F, dtype=torch.uint8, device="cuda") for _ in range(2))
         pa.pa_append_rope(None, dk, dk, None, table, zeros, pos, kc, vc, k_scale=scale, v_scale=1.0)
         want = [np.full(shape, 0x7F, np.uint8) for _ in range(2)]
@@ -237,7 +239,8 @@ def test_quantized_stores_of_every_16_bit_value(cuda_device, dtype, kind):
             got = kc.cpu().numpy()
             assert np.array_equal(got.reshape(n // 16, 4, -1)[..., 16 * 64:],
                                   want[0].reshape(n // 16, 4, -1)[..., 16 * 64:]), scale
-            assert np.array_equal(oracle.fp4_dequant(got, 128), oracle.fp4_dequant(want[0], 128)), scale
+            assert np.array_equal(oracle.fp4_dequant(got, 128),
+                                  oracle.fp4_dequant(want[0], 128)), scale
 
 
 def test_append_padding_and_bad_tokens_write_nothing(cuda_device):
@@ -378,7 +381,8 @@ def test_append_argument_checks(cuda_device):
         with pytest.raises(exc):
             call(**kw)
     # a token stride that is no multiple of 8 elements is refused by the library
-    odd = torch.zeros(5, 2 * 64 + 4, dtype=torch.bfloat16, device="cuda")[:, :128].unflatten(1, (2, 64))
+    odd = torch.zeros(5, 2 * 64 + 4, dtype=torch.bfloat16, device="cuda")
+    odd = odd[:, :128].unflatten(1, (2, 64))
     with pytest.raises(pa.PAError) as e:
         call(k=odd)
     assert e.value.status == 1

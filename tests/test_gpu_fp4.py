@@ -469,21 +469,25 @@ def test_argument_checks(cuda_device):
         a.update(kw)
         return pa.pa_decode_fp4(**a)
     call()
-    for kw, exc in ((dict(q=d["q"].float()), TypeError), (dict(q=d["q"][..., :64].contiguous()), ValueError),
-                    (dict(k_cache=d["k"][..., :64].contiguous(), v_cache=d["v"][..., :64].contiguous()), ValueError),
+    half_k, half_v = (d[p][..., :64].contiguous() for p in "kv")
+    for kw, exc in ((dict(q=d["q"].float()), TypeError),
+                    (dict(q=d["q"][..., :64].contiguous()), ValueError),
+                    (dict(k_cache=half_k, v_cache=half_v), ValueError),
                     (dict(seq_lens=d["lens"].long()), TypeError),
-                    (dict(block_tables=d["bt"][:1].contiguous()), ValueError), (dict(out=d["q"][:1]), ValueError),
-                    (dict(q=d["q"].cpu()), ValueError)):
+                    (dict(block_tables=d["bt"][:1].contiguous()), ValueError),
+                    (dict(out=d["q"][:1]), ValueError), (dict(q=d["q"].cpu()), ValueError),
+                    (dict(k_cache=d["k"].transpose(0, 1)), ValueError)):
         with pytest.raises(exc):
             call(**kw)
-    for kw, status in ((dict(window=-1), 1), (dict(k_scale=0.0), 1), (dict(flags=pa.PA_DECODE_SIMT), 2),
-                       (dict(workspace=torch.zeros(64, dtype=torch.uint8, device="cuda")), 3),
+    small = torch.zeros(64, dtype=torch.uint8, device="cuda")
+    for kw, status in ((dict(window=-1), 1), (dict(k_scale=0.0), 1),
+                       (dict(flags=pa.PA_DECODE_SIMT), 2), (dict(workspace=small), 3),
                        (dict(num_ctas=pa.PA_DECODE_MAX_CTAS + 1), 1)):
         with pytest.raises(pa.PAError) as e:
             call(**kw)
         assert e.value.status == status, kw
     with pytest.raises(ValueError):
-        pa.pa_cache_read_fp4(torch.zeros(2, dtype=torch.int64, device="cuda"), d["k"], d["v"], 1.0, 1.0,
-                             k_out=torch.zeros(2, 2, 128, dtype=torch.bfloat16, device="cuda"))
+        pa.pa_cache_read_fp4(torch.zeros(2, dtype=torch.int64, device="cuda"), d["k"], d["v"], 1.0,
+                             1.0, k_out=torch.zeros(2, 2, 128, dtype=torch.bfloat16, device="cuda"))
     # ulp_spacing is what the bounds count: one bfloat16 step above 1 is 2^-7
     assert ulp_spacing(W.to_bits(np.float32(1.0), W.BF16), W.BF16) == 2.0 ** -7
