@@ -2,7 +2,9 @@
 
 Every function takes CUDA tensors, checks dtypes and shapes, passes raw device
 pointers, sizes and the current CUDA stream to libpa.so, and raises PAError on
-a non-zero status.  Nothing is computed here.
+a non-zero status.  The append and the 4-bit cache's calls are marshalled by an
+extension module (csrc/pa_call.cpp), the others here through ctypes.  Nothing is
+computed here.
 """
 import ctypes
 
@@ -75,19 +77,6 @@ def pa_fp4_pool_shape(num_blocks, block_size, num_kv_heads, head_dim):
 _FP4_HEAD_DIM = {36: 64, 72: 128}
 
 
-def _fp4_pools(k_cache, v_cache):
-    """(num_blocks, B, H_kv, D) of a pair of 4-bit pools."""
-    shape = k_cache.shape
-    if len(shape) != 4 or v_cache.shape != shape or k_cache.dtype != v_cache.dtype:
-        raise ValueError("k_cache and v_cache must share one shape [num_blocks, H_kv, B, 9 D / 16]")
-    nb, H, B, row = shape
-    if k_cache.dtype != torch.uint8:
-        raise TypeError("4-bit pools must be uint8 tensors of codes and scales")
-    if row not in _FP4_HEAD_DIM:
-        raise ValueError("4-bit pools must be [num_blocks, H_kv, B, 9 D / 16], D 64 or 128")
-    return nb, B, H, _FP4_HEAD_DIM[row]
-
-
 _CODE = {torch.float16: PA_F16, torch.bfloat16: PA_BF16}
 
 
@@ -106,43 +95,27 @@ def _block_pools(k_cache, v_cache):
     return a, b, c, d, PA_FP8_E4M3
 
 
-def _raw_stream(dev):
-    """The current stream's handle: the lookup behind torch.cuda.current_stream
-    without the stream object, which costs more than a launch."""
-    return torch._C._cuda_getCurrentRawStream(dev)
+def _fp4_pools(k_cache, v_cache):
+    """(B, H_kv, D) of a pair of 4-bit pools."""
+    _, B, H, D, code = _block_pools(k_cache, v_cache)
+    if code != PA_FP4_E2M1:
+        raise ValueError("4-bit pools must be uint8 [num_blocks, H_kv, B, 9 D / 16], D 64 or 128")
+    return B, H, D
 
 
-def _here(dev, names, *tensors):
-    """The stream of the current device dev, after checking that every tensor
-    given (not None) is contiguous and on it.  names: theirs, space-separated."""
-    for t in tensors:
-        if t is not None and (t.get_device() != dev or not t.is_contiguous()):
-            for n, u in zip(names.split(), tensors):
-                if u is t:
-                    _cuda(u, n)
-                    raise ValueError("%s must be on the current device, cuda:%d" % (n, dev))
-    return _raw_stream(dev)
+_call = None
 
 
-def _tables(block_tables, token_seq, token_pos):
-    """The number of tokens, of slots given by table, sequence and position."""
-    i32 = torch.int32
-    if block_tables.dtype != i32 or token_seq.dtype != i32 or token_pos.dtype != i32:
-        raise TypeError("block_tables, token_seq and token_pos must be int32")
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables must be [num_seqs, stride]")
-    n_tok = token_seq.numel()
-    if token_pos.numel() != n_tok:
-        raise ValueError("token_seq and token_pos differ in length")
-    return n_tok
-
-
-def _outs(n_tok, slot_mapping, err):
-    if slot_mapping is not None and (slot_mapping.dtype != torch.int64
-                                     or slot_mapping.numel() != n_tok):
-        raise ValueError("slot_mapping must be int64 [num_tokens]")
-    if err is not None and (err.dtype != torch.int32 or err.numel() < 1):
-        raise ValueError("err must be an int32 CUDA tensor")
+def _calls():
+    """The extension module behind the append's and the 4-bit cache's calls.  It
+    checks types, shapes, layouts and devices, and raises TypeError or
+    ValueError; there is no fallback."""
+    global _call
+    if _call is None:
+        _lib.load()
+        from . import _pa_call
+        _call = _pa_call
+    return _call
 
 
 def pa_version():
@@ -419,21 +392,6 @@ def pa_decode_fp8(q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v
     return out
 
 
-def _token_rows(t, name, n_tok, heads, D, dtype, dev):
-    """A [num_tokens, heads, D] tensor whose rows are contiguous within a token;
-    tokens may lie any multiple of 8 elements apart.  Returns that distance."""
-    if t.get_device() != dev:
-        raise ValueError("%s must be on the current device, cuda:%d" % (name, dev))
-    if t.dtype != dtype:
-        raise TypeError("q, k and v must share a dtype")
-    if t.shape != (n_tok, heads, D):
-        raise ValueError("%s must be [num_tokens, heads, D] = %s" % (name, (n_tok, heads, D)))
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or (heads > 1 and s1 != D):
-        raise ValueError("the heads of a token must be contiguous in %s" % name)
-    return s0 if n_tok > 1 else heads * D
-
-
 def pa_append_rope(q, k, v, cos_sin, block_tables, token_seq, token_pos, k_cache, v_cache,
                    interleaved=False, q_norm=None, k_norm=None, eps=1e-6, k_scale=1.0,
                    v_scale=1.0, q_out=None, slot_mapping=None, err=None):
@@ -452,79 +410,24 @@ def pa_append_rope(q, k, v, cos_sin, block_tables, token_seq, token_pos, k_cache
     (pa_fp4_pool_shape); k_scale and v_scale apply to the last two.  Tokens of
     sequence -1 are padding: they write nothing, and their rows of q_out keep
     what they held (zeros when q_out is made here)."""
-    L = _lib.load()
-    nb, B, H, D, code = _block_pools(k_cache, v_cache)
-    n_tok = _tables(block_tables, token_seq, token_pos)
-    _outs(n_tok, slot_mapping, err)
-    dtype = k.dtype
-    if dtype not in _CODE or (code < PA_FP8_E4M3 and code != _CODE[dtype]):
-        raise TypeError("k must be float16 or bfloat16, and the pools of its dtype or uint8")
-    dev = torch.cuda.current_device()
-    ks = _token_rows(k, "k", n_tok, H, D, dtype, dev)
-    vs = _token_rows(v, "v", n_tok, H, D, dtype, dev)
-    Hq = qs = rot = max_pos = 0
-    if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be [num_tokens, Hq, D]")
-        Hq = q.shape[1]
-        qs = _token_rows(q, "q", n_tok, Hq, D, dtype, dev)
-        if q_out is None:
-            q_out = torch.zeros((n_tok, Hq, D), dtype=dtype, device=q.device)
-        elif q_out.shape != (n_tok, Hq, D) or q_out.dtype != dtype:
-            raise ValueError("q_out must be [num_tokens, Hq, D] of q's dtype")
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
-            raise TypeError("cos_sin must be float32 [max_pos, rotary_dim]")
-        max_pos, rot = cos_sin.shape
-    for g in (q_norm, k_norm):
-        if g is not None and (g.shape != (D,) or g.dtype != dtype):
-            raise ValueError("q_norm and k_norm must be [D] of k's dtype")
-    stream = _here(dev, "cos_sin q_norm k_norm block_tables token_seq token_pos k_cache v_cache "
-                   "q_out slot_mapping err", cos_sin, q_norm, k_norm, block_tables, token_seq,
-                   token_pos, k_cache, v_cache, q_out, slot_mapping, err)
-    stride = block_tables.shape
-    _check(L.pa_append_rope(
-        None if q is None else q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-        _CODE[dtype], None if cos_sin is None else cos_sin.data_ptr(), rot, max_pos,
-        1 if interleaved else 0, None if q_norm is None else q_norm.data_ptr(),
-        None if k_norm is None else k_norm.data_ptr(), eps, block_tables.data_ptr(), stride[1],
-        stride[0], token_seq.data_ptr(), token_pos.data_ptr(), n_tok,
-        None if q_out is None else q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), nb, B,
-        Hq, H, D, code, k_scale, v_scale,
-        None if slot_mapping is None else slot_mapping.data_ptr(),
-        None if err is None else err.data_ptr(), stream), "pa_append_rope")
+    if q_out is None and q is not None:
+        q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    status = (_call or _calls()).append_rope(
+        q, k, v, cos_sin, block_tables, token_seq, token_pos, k_cache, v_cache, interleaved, q_norm,
+        k_norm, eps, k_scale, v_scale, q_out, slot_mapping, err)
+    if status:
+        raise PAError(status, "pa_append_rope")
     return q_out
-
-
-def _kv_rows(k, v, n_tok, H, D):
-    if k.shape != (n_tok, H, D) or v.shape != (n_tok, H, D) or k.dtype != v.dtype:
-        raise ValueError("k, v must be [num_tokens, H_kv, D] of one dtype")
-
-
-def _slots_in(slot_mapping):
-    if slot_mapping.dtype != torch.int64:
-        raise TypeError("slot_mapping must be int64")
-    return slot_mapping.numel()
 
 
 def pa_cache_write_fp4(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, err=None):
     """Quantize k[n], v[n] ([n_tok, H_kv, D], float16 / bfloat16) to E2M1 codes
     with an E4M3 scale per 16 head_dim values (value = code * scale16 * scale)
     at pool slot slot_mapping[n] of the 4-bit pools (pa_fp4_pool_shape)."""
-    L = _lib.load()
-    nb, B, H, D = _fp4_pools(k_cache, v_cache)
-    n_tok = _slots_in(slot_mapping)
-    _kv_rows(k, v, n_tok, H, D)
-    _outs(n_tok, None, err)
-    stream = _here(torch.cuda.current_device(), "k v slot_mapping k_cache v_cache err", k, v,
-                   slot_mapping, k_cache, v_cache, err)
-    _check(L.pa_cache_write_fp4(k.data_ptr(), v.data_ptr(), _dtype_code(k),
-                                slot_mapping.data_ptr(), n_tok, k_cache.data_ptr(),
-                                v_cache.data_ptr(), nb, B, H, D, k_scale, v_scale,
-                                None if err is None else err.data_ptr(), stream),
-           "pa_cache_write_fp4")
+    status = (_call or _calls()).cache_write_fp4(k, v, slot_mapping, k_cache, v_cache, k_scale,
+                                                 v_scale, err)
+    if status:
+        raise PAError(status, "pa_cache_write_fp4")
 
 
 def pa_cache_write_fp4_mapped(k, v, block_tables, token_seq, token_pos, k_cache, v_cache,
@@ -532,20 +435,11 @@ def pa_cache_write_fp4_mapped(k, v, block_tables, token_seq, token_pos, k_cache,
     """Slot mapping and pa_cache_write_fp4 in one launch: new token n goes to
     slot block_tables[seq][pos // B] * B + pos % B; the int64 slots go to
     slot_mapping when given.  Tokens of sequence -1 are padding (slot -1)."""
-    L = _lib.load()
-    nb, B, H, D = _fp4_pools(k_cache, v_cache)
-    n_tok = _tables(block_tables, token_seq, token_pos)
-    _kv_rows(k, v, n_tok, H, D)
-    _outs(n_tok, slot_mapping, err)
-    stream = _here(torch.cuda.current_device(), "k v block_tables token_seq token_pos k_cache "
-                   "v_cache slot_mapping err", k, v, block_tables, token_seq, token_pos, k_cache,
-                   v_cache, slot_mapping, err)
-    stride = block_tables.shape
-    _check(L.pa_cache_write_fp4_mapped(
-        k.data_ptr(), v.data_ptr(), _dtype_code(k), block_tables.data_ptr(), stride[1], stride[0],
-        token_seq.data_ptr(), token_pos.data_ptr(), n_tok, k_cache.data_ptr(), v_cache.data_ptr(),
-        nb, B, H, D, k_scale, v_scale, None if slot_mapping is None else slot_mapping.data_ptr(),
-        None if err is None else err.data_ptr(), stream), "pa_cache_write_fp4_mapped")
+    status = (_call or _calls()).cache_write_fp4_mapped(k, v, block_tables, token_seq, token_pos,
+                                                        k_cache, v_cache, k_scale, v_scale,
+                                                        slot_mapping, err)
+    if status:
+        raise PAError(status, "pa_cache_write_fp4_mapped")
     return slot_mapping
 
 
@@ -554,24 +448,16 @@ def pa_cache_read_fp4(slot_mapping, k_cache, v_cache, k_scale, v_scale, dtype=to
     """The rows at pool slots slot_mapping[n] of 4-bit pools as 16-bit values
     (k, v), each [n, H_kv, D].  Rows of negative slots keep what the outputs
     held (zeros when the outputs are made here)."""
-    L = _lib.load()
-    nb, B, H, D = _fp4_pools(k_cache, v_cache)
-    n_tok = _slots_in(slot_mapping)
     if (k_out is None) != (v_out is None):
         raise ValueError("give both of k_out and v_out, or neither")
     if k_out is None:
-        k_out = torch.zeros((n_tok, H, D), dtype=dtype, device=k_cache.device)
+        _, H, D = _fp4_pools(k_cache, v_cache)
+        k_out = torch.zeros((slot_mapping.numel(), H, D), dtype=dtype, device=k_cache.device)
         v_out = torch.zeros_like(k_out)
-    if k_out.shape != (n_tok, H, D) or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
-        raise ValueError("k_out, v_out must be [n, H_kv, D] of one dtype")
-    _outs(n_tok, None, err)
-    stream = _here(torch.cuda.current_device(), "slot_mapping k_cache v_cache k_out v_out err",
-                   slot_mapping, k_cache, v_cache, k_out, v_out, err)
-    _check(L.pa_cache_read_fp4(slot_mapping.data_ptr(), n_tok, k_cache.data_ptr(),
-                               v_cache.data_ptr(), nb, B, H, D, k_scale, v_scale,
-                               k_out.data_ptr(), v_out.data_ptr(), _dtype_code(k_out),
-                               None if err is None else err.data_ptr(), stream),
-           "pa_cache_read_fp4")
+    status = (_call or _calls()).cache_read_fp4(slot_mapping, k_cache, v_cache, k_scale, v_scale,
+                                                k_out, v_out, err)
+    if status:
+        raise PAError(status, "pa_cache_read_fp4")
     return k_out, v_out
 
 
@@ -580,34 +466,18 @@ def pa_decode_fp4(q, k_cache, v_cache, block_tables, seq_lens, scale, k_scale, v
     """Paged decode over 4-bit pools (value = code * scale16 * scale): out
     [N, Hq, D] in q's dtype.  window >= 1: the query of position T - 1 attends
     to tokens [max(0, T - window), T); 0: to all of them."""
-    L = _lib.load()
-    nb, B, H, D = _fp4_pools(k_cache, v_cache)
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
-        raise TypeError("block_tables and seq_lens must be int32")
-    shape, table = q.shape, block_tables.shape
-    if len(shape) != 3 or shape[2] != D:
-        raise ValueError("q must be [N, Hq, D]")
-    N, Hq, _ = shape
-    if len(table) != 2 or table[0] != N or seq_lens.numel() != N:
-        raise ValueError("block_tables must be [N, stride] and seq_lens [N]")
-    code = _dtype_code(q)
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != shape or out.dtype != q.dtype:
-        raise ValueError("out must be [N, Hq, D] of q's dtype")
     if workspace is None:
-        nbytes = pa_decode_workspace_size(Hq, H, D, B, PA_FP4_E2M1, flags, num_ctas)
+        B, H, D = _fp4_pools(k_cache, v_cache)
+        nbytes = pa_decode_workspace_size(q.shape[1], H, D, B, PA_FP4_E2M1, flags, num_ctas)
         # zero-filled once; the decode leaves it ready for the next call
         workspace = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=q.device)
-    _outs(N, None, err)
-    stream = _here(torch.cuda.current_device(), "q k_cache v_cache block_tables seq_lens out "
-                   "workspace err", q, k_cache, v_cache, block_tables, seq_lens, out, workspace, err)
-    _check(L.pa_decode_fp4(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                           block_tables.data_ptr(), table[1], seq_lens.data_ptr(), N, Hq, H, D, B,
-                           nb, code, scale, k_scale, v_scale, window, out.data_ptr(),
-                           workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                           flags, num_ctas, None if err is None else err.data_ptr(), stream),
-           "pa_decode_fp4")
+    status = (_call or _calls()).decode_fp4(q, k_cache, v_cache, block_tables, seq_lens, scale,
+                                            k_scale, v_scale, window, out, workspace, flags,
+                                            num_ctas, err)
+    if status:
+        raise PAError(status, "pa_decode_fp4")
     return out
 
 
