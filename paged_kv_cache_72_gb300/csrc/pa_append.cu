@@ -116,7 +116,7 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 // smallest code.
 __device__ __forceinline__ F2 div_by(F2 x, float d, float r) {
   const F2 y = mul2(x, {r, r});
-  return fma2(fma2({-y.x, -y.y}, {d, d}, x), {r, r}, y);
+  return fma2(fma2(y, {-d, -d}, x), {r, r}, y);
 }
 __device__ __forceinline__ bool plain_quotient(float largest, float d) {
   return d > 0x1p-100f && d < 0x1p100f && largest <= 0x1p27f * d;
@@ -288,9 +288,8 @@ __device__ __forceinline__ void store_row(uint8_t* pool, const uint4& x, long lo
     const uint32_t s8 = f32x2_to_e4m3x2(s16, 0.f) & 0xffu;
     const float d = __fmul_rn(unpack2<false>(e4m3x2_to_f16x2(s8)).x, scale);
     quotients(z, m, d, __frcp_rn(d), y);
-    uint32_t code = 0u;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) code |= f32x2_to_e2m1x2(y[i].x, y[i].y) << (8 * i);
+    const uint32_t code = f32x8_to_e2m1x8(y[0].x, y[0].y, y[1].x, y[1].y, y[2].x, y[2].y, y[3].x,
+                                          y[3].y);
     if (in) {
       const int B = 1 << log2B, row = (int)(slot & (B - 1));
       uint8_t* plane = pool + fp4_plane(slot >> log2B, H, h, B * fp4_row_bytes(D));

@@ -38,13 +38,17 @@ __device__ __forceinline__ void e2m1x8_to_f16x2(uint32_t x, uint32_t (&r)[4]) {
       : "r"(x));
 }
 
-// Two fp32 values -> one byte of two E2M1 codes (`lo` in the low nibble),
-// round to nearest even, magnitudes beyond 6 saturate.
-__device__ __forceinline__ uint32_t f32x2_to_e2m1x2(float lo, float hi) {
+// Eight fp32 values -> eight E2M1 codes (the first in the lowest nibble), round
+// to nearest even, magnitudes beyond 6 saturate.
+__device__ __forceinline__ uint32_t f32x8_to_e2m1x8(float x0, float x1, float x2, float x3,
+                                                    float x4, float x5, float x6, float x7) {
   uint32_t r;
-  asm("{\n\t.reg .b8 t;\n\tcvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n\tcvt.u32.u8 %0, t;\n\t}"
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(x0), "f"(x1), "f"(x2), "f"(x3), "f"(x4), "f"(x5), "f"(x6), "f"(x7));
   return r;
 }
 
