@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
       if (live_warp) {
         const uint32_t so = (uint32_t)(st * kStage);
         const uint32_t bad = (odd_stages >> st) & 1u ? sh.bad[warp][st] : 0u;
-        const bool edge = t0 < first || t0 + kTile > w.T || bad != 0u;
+        const bool edge = t0 < first || w.T - t0 < kTile || bad != 0u;
         float s[2][NH][4];
         uint32_t pb[2][NH][2], pl[2][NH][2];
         const uint32_t kc[2] = {ok[0] + so, ok[1] + so}, ks[2] = {os[0] + so, os[1] + so};
@@ -770,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
         if (edge) {
           uint32_t live = kFull;
           if (t0 < first) live &= kFull << (first - t0);
-          if (t0 + kTile > w.T) live &= kFull >> (t0 + kTile - w.T);
+          if (w.T - t0 < kTile) live &= kFull >> (kTile - (w.T - t0));
           if (bad)
             for (int b = 0; b < kTile / bs; ++b)
               if ((bad >> b) & 1u) live &= ~((bs == 32 ? kFull : (1u << bs) - 1u) << (b * bs));

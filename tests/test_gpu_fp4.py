@@ -491,3 +491,111 @@ def test_argument_checks(cuda_device):
                              1.0, k_out=torch.zeros(2, 2, 128, dtype=torch.bfloat16, device="cuda"))
     # ulp_spacing is what the bounds count: one bfloat16 step above 1 is 2^-7
     assert ulp_spacing(W.to_bits(np.float32(1.0), W.BF16), W.BF16) == 2.0 ** -7
+
+
+# ---------------------------------------------------------------------------
+# the largest calls, and several calls at once
+# ---------------------------------------------------------------------------
+
+def _constant_pools(blocks, B, D, seed):
+    """One KV head; keys zero, every row's values the same vector of E2M1 values
+    with unit scales.  Every attended mean is that vector, and every product and
+    partial sum of the decode a multiple of 2^12 below 2^36: exact in fp32 up to
+    the joins of partial sums."""
+    rng = np.random.default_rng(seed)
+    row = np.array([0, .5, 1, 1.5, 2, 3, 4, 6])[rng.integers(0, 8, D)] * rng.choice([-1, 1], D)
+    code = oracle.e2m1_encode(row).astype(np.uint8)
+    v = np.zeros((blocks, 1, B * 9 * D // 16), np.uint8)
+    v[..., :B * D // 2] = np.tile(code[0::2] | (code[1::2] << 4), B)
+    v[..., B * D // 2:] = 0x38               # E4M3 one
+    k = np.zeros_like(v)
+    k[..., B * D // 2:] = 0x38
+    return row, k, v
+
+
+@pytest.mark.parametrize("window", [0, 40])
+def test_decode_longest_context(cuda_device, window):
+    # 2^31 - 1 tokens, the most an int32 length says; the row behind the last
+    # token has NaN scales
+    B, D, T = 256, 64, 2 ** 31 - 1
+    row, k, v = _constant_pools(2, B, D, 620)
+    for p in (k, v):
+        p[1, 0, B * D // 2:].reshape(B // 4, D // 16, 4)[-1, :, 3] = 0x7F
+    bt = torch.zeros((1, 2 ** 23), dtype=torch.int32, device="cuda")
+    bt[0, -1] = 1
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q = torch.randn(1, 4, D, device="cuda").bfloat16()
+    pools = [torch.from_numpy(p.reshape(2, 1, B, 9 * D // 16)).cuda() for p in (k, v)]
+    out = pa.pa_decode_fp4(q, *pools, bt, torch.tensor([T], dtype=torch.int32, device="cuda"), 1.0,
+                           1.0, 1.0, window=window, err=err)
+    assert pa.pa_get_error(err) == 0
+    # the joins leave relative errors below 2^-12, the values need 2 of 8 bits
+    assert np.array_equal(bits_to_f64(bits_of(out), W.BF16)[0], np.tile(row, (4, 1)))
+
+
+def test_decode_quarter_million_sequences(cuda_device):
+    n, B, D = 2 ** 18 + 1500, 4, 64
+    row, k, v = _constant_pools(64, B, D, 621)
+    sizes = np.arange(64) % 4                 # block b: its values times 2^(b % 4)
+    v[..., B * D // 2:] = (0x38 + 8 * sizes)[:, None, None]
+    rng = np.random.default_rng(622)
+    lens = rng.integers(0, 4, n).astype(np.int32)
+    bt = rng.integers(0, 64, (n, 1)).astype(np.int32)
+    pools = [torch.from_numpy(p.reshape(64, 1, B, 9 * D // 16)).cuda() for p in (k, v)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = pa.pa_decode_fp4(torch.randn(n, 1, D, device="cuda").bfloat16(), *pools,
+                           torch.from_numpy(bt).cuda(), torch.from_numpy(lens).cuda(), 1.0, 1.0,
+                           1.0, out=torch.full((n, 1, D), float("nan"), dtype=torch.bfloat16,
+                                               device="cuda"), err=err)
+    assert pa.pa_get_error(err) == 0
+    want = torch.from_numpy(row * (2.0 ** sizes[bt] * (lens[:, None] > 0))).cuda()
+    assert torch.equal(out[:, 0].double(), want)
+
+
+def test_decodes_of_three_caches_share_a_workspace(cuda_device):
+    st = State(623, W.BF16, 8, 2, 128, 16, [2000, 1, 300])
+    nb = len(st.k)
+    gen = torch.Generator(device="cuda").manual_seed(624)
+    k16, v16 = (torch.randn((nb, 16, 2, 128), device="cuda", generator=gen).bfloat16()
+                for _ in range(2))
+    k8, v8 = (torch.randint(0, 0x70, (nb, 16, 2, 128), dtype=torch.uint8, device="cuda",
+                            generator=gen) for _ in range(2))
+    d = st.dev
+    ws = torch.zeros(max(pa.pa_decode_workspace_size(8, 2, 128, 16, t)
+                         for t in (pa.PA_BF16, pa.PA_FP8_E4M3, pa.PA_FP4_E2M1)),
+                     dtype=torch.uint8, device="cuda")
+
+    def run16(w):
+        return pa.pa_decode(d["q"], k16, v16, d["bt"], d["lens"], st.scale, workspace=w)
+
+    def run8(w):
+        return pa.pa_decode_fp8(d["q"], k8, v8, d["bt"], d["lens"], st.scale, 0.1, 0.1, workspace=w)
+
+    runs = (run16, run8, lambda w: st.decode(workspace=w))
+    alone = [f(None) for f in runs]
+    ref = st.expected()
+    for order in ((0, 1, 2), (2, 0, 2, 1), (1, 2, 0)):
+        for i in order:
+            out = runs[i](ws)
+            assert torch.equal(out, alone[i]), i
+            if i == 2:
+                st.check(out, ref)
+
+
+def test_decodes_on_two_streams_at_once(cuda_device):
+    # a workspace each
+    states = [State(625, W.BF16, 32, 8, 128, 16, [4000, 900]), State(626, W.F16, 8, 2, 64, 8, [7000])]
+    alone = [st.decode() for st in states]
+    ws = [torch.zeros(pa.pa_decode_workspace_size(st.q.shape[1], st.H, st.D, st.B, pa.PA_FP4_E2M1),
+                      dtype=torch.uint8, device="cuda") for st in states]
+    streams = [torch.cuda.Stream() for _ in states]
+    kept = [[torch.zeros_like(st.dev["q"]) for _ in range(20)] for st in states]
+    torch.cuda.synchronize()
+    for n in range(20):
+        for st, s, w, out in zip(states, streams, ws, kept):
+            with torch.cuda.stream(s):
+                st.decode(workspace=w, out=out[n])
+    torch.cuda.synchronize()
+    for a, out, st in zip(alone, kept, states):
+        assert all(torch.equal(o, a) for o in out)
+        assert pa.pa_get_error(st.err) == 0
