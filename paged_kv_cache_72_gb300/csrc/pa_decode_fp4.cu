@@ -7,39 +7,50 @@
 // code * s16 has at most 6 significant bits and lies in [2^-10, 2688], so it is
 // exact in binary16, and every product is an f16 x f16 MMA with fp32 sums.
 //
-// Bound: bytes first (0.5625 bytes an element and nothing read twice), then the
-// conversions: one cvt, one multiply by the scale and (for V) half a byte merge
-// a pair of elements.  So the kernel keeps both small:
+// Bound: half bytes, half issue.  0.5625 bytes an element are read once and
+// nothing else is, but a tile of 32 tokens also costs a warp 34 MMAs, 128
+// conversions and 128 multiplies by scales (head_dim 128, up to 8 heads a KV
+// head).  32 contexts of 16 to 32 K tokens, 64 heads over 8 of 128 (883 MB):
+// 184 us, 4.8 TB/s; the copies alone take 144 us, the arithmetic alone 162.  256
+// contexts of 17 to 4,096 tokens, 32 over 8 heads (125 MB): 38.5 us, of which
+// the copies are 33.7.  So the arithmetic is kept lean and the copies are kept
+// going under it:
 //  * One warp is one pipeline.  A warp owns a (sequence, KV head) context or a
-//    contiguous range of one and reads its planes straight from global memory
-//    into MMA fragments: the layout of a plane lets every lane load its own
-//    fragment bytes as whole vectors, so there is no shared-memory staging, no
-//    producer and no barrier between warps until a block's end.
-//  * The next tile's K is loaded as soon as this tile's K is in the tensor
-//    cores, and the next V after this V: one set of registers each, with the
-//    other half of the tile's work to cover the latency.
+//    contiguous range of one.  Its tiles arrive by bulk copies in a ring of
+//    kStages tiles of its own, filled and waited for by the warp itself: no
+//    producer, and no barrier between warps until a block's end.  (Fragments
+//    loaded straight from global memory took 215 us where the ring took 205.)
 //  * Transposed products: S^T = K Q^T (16 tokens x 8 heads), O^T += V^T P^T
-//    (16 head_dim rows x 8 heads); groups of more than 8 query heads take two
-//    8-head tiles.
+//    (16 head_dim rows x 8 heads), so that K and V are the A operands and 8
+//    heads, not 16, fill a product; more than 8 heads a KV head take two tiles.
+//  * The softmax's base is lazy (below), the weights' sums are one more MMA row
+//    of ones, and tiles that need no mask run code without one (together 238 to
+//    215 us).
 //
 // Index maps (a contraction's order is free, an output row's place is undone
 // at the write):
 //  * a half tile is 16 tokens; MMA row r < 8 is token 4 (r / 2) + r % 2, row
 //    8 + r the token two further.  The K rows of lane (gid, tig) = (lane / 4,
 //    lane % 4) and its four V rows 4 tig .. 4 tig + 3 then each lie in one
-//    group of four tokens: one block-table entry, one scale word.
+//    group of four tokens: one scale word.
 //  * S^T, k-step s: k index 2 tig + e stands for d = (D/4) tig + 4 s + e, and
 //    2 tig + 8 + e for d + 2: the lane's K bytes are contiguous.
 //  * O^T, m-tile i: row gid is d = (D/8) gid + 2 i, row gid + 8 the next: the
 //    lane's V bytes are contiguous, and so is the slice of o it ends with.
 //
-// The split.  The tiles of 32 tokens of every (sequence, KV head), in that
-// order, are cut into equal contiguous ranges, one per block, and each block's
-// range into one per warp.  A warp that holds a whole context writes it out.
-// The parts of contexts cut between the warps of a block are merged in shared
-// memory; a context cut between blocks leaves one record (m, l, o) per block
-// in the workspace, and the block that completes the context's count merges
-// them.  No block waits for another.
+// The split.  Every (sequence, KV head) is kStart units and one for each of its
+// tiles; the units, in that order, are cut into equal contiguous ranges, one
+// per block, and each block's range into one per warp.  A warp that holds a
+// whole context writes it out.  The parts of contexts cut between the warps of
+// a block are merged in shared memory; a context cut between blocks leaves one
+// record (m, l, o) per block in the workspace, and the block that completes the
+// context's count merges them, always in the order of the tiles.  No block
+// waits for another.  Batches of short contexts take one warp each instead
+// (kWhole).
+//
+// Roundings below fp32: the weights to binary16 (a pair of them for binary16
+// outputs), a bfloat16 query's elements under 2^-14 of its row's largest, and
+// the output.
 #include <cmath>
 #include <mutex>
 
@@ -50,19 +61,28 @@ namespace pa {
 
 namespace {
 
+// Four warps a block and three blocks an SM: 12 warps leave a thread 168
+// registers, which o, the queries and a tile's work need (32 contexts of 16 to
+// 32 K tokens: 197 us where two blocks took 205 and 16 warps of fewer registers
+// 196 to 205).  Five to eight warps a block measured no better.
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kTile = 32;                 // tokens per tile
-constexpr int kStages = 2;                // tiles in shared memory per warp
+constexpr int kBlocksPerSm = 3;
+constexpr int kTile = 32;                 // tokens per tile (64: 190 us for 187)
+constexpr int kStages = 2;                // tiles in shared memory per warp (a third
+                                          // measured the same)
 // A context's share of the work is its tiles and kStart for its start and end
 // (queries to fragments, the write): without it a warp whose range holds many
-// short contexts finishes last (91.9 against 67.7 us for 64 contexts of 1 to
-// 2,048 tokens and 32 heads; 2 and 3 measured 69.2 and 70.7).
+// short contexts finishes last.  0 / 1 / 2 / 3 measured 91.9 / 67.7 / 69.2 /
+// 70.7 us for 64 contexts of 1 to 2,048 tokens and 32 KV heads, 41.7 / 38.5 /
+// 39.0 / 40.1 for the 256 contexts above.
 constexpr int kStart = 1;
 // Contexts of at most kWhole tiles go to one warp each when there are warps
-// enough: a warp takes 0.3 us a tile alone, joining parts costs 3 us.
+// enough, which saves joining parts: 6.4 us for 8.9 with 16 contexts of 1 to 64
+// tokens and 8 KV heads, 18.1 for 20.6 with 200 of 16 to 256; but 13.1 for 12.2
+// with 64 of 1 to 256, and a limit of 16 takes 21.4 for 15.4 with 64 of 128 to
+// 512.
 constexpr int kWhole = 8;
-constexpr int kBlocksPerSm = 3;
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kUnitBits = 44, kCounted = 1 << 18;   // of the scanned sums; sequences it counts
 // Weights are exp2(x - base) with base = a maximum less kShift, and a new base
@@ -145,7 +165,8 @@ struct Walk {
 // One warp's state over a range of one context's tiles.  kTwin (binary16
 // outputs, at most 4 query heads): the 8 head columns hold the heads twice, the
 // first copy's weights rounded to binary16, the second's what that rounding
-// left, so that the pair costs no second product; the two are added at the end.
+// left, so that the pair costs no second product; the two are added at the end
+// (44.2 us with the second product, 41.7 without, for the 256 contexts above).
 template <int D, bool kBF16, int NH, bool kTwin>
 struct Context {
   static constexpr int KS = D / 16;        // k-steps of S^T
