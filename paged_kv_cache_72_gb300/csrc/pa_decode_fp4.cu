@@ -140,6 +140,19 @@ __device__ __forceinline__ void ld_part(uint32_t addr, uint32_t* r) {
     asm volatile("ld.shared.b32 %0, [%1 + %2];" : "=r"(r[0]) : "r"(addr), "n"(kOff));
 }
 
+// 16 bytes from global to shared memory, past L1; the lane's copies since the
+// last commit are a group, and a wait leaves at most kPending groups in flight.
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
 // A place in the list of tiles: tile k of head h of sequence i, and that
 // sequence's length and tiles.
 struct Walk {
@@ -527,8 +540,6 @@ struct Shared {
   long long warp_tot[kWarps];
   int warp_longest[kWarps];
   Part part[2 * kWarps];
-  unsigned long long full[kWarps][kStages];   // a stage's copies have landed
-  uint32_t bad[kWarps][kStages];              // its blocks without a valid table entry
   int group_first[2 * kWarps + 1];
   int groups;
   int merges;                     // contexts this block owes the merge of
@@ -547,10 +558,6 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
   const int B = 1 << a.log2B;
   const size_t rf = rec_floats(a.G, D);
   float* const slots = reinterpret_cast<float*>(dyn);
-  if (lane == 0) {
-    for (int st = 0; st < kStages; ++st) mbar_init(smem_u32(&sh.full[warp][st]), 1);
-    fence_barrier_init();
-  }
 
   // The small inputs towards L2 while the previous kernel in the stream drains
   // (a prefetch returns no data: that kernel may still be writing them).
@@ -672,35 +679,39 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
     int ld_left = left;
 
     // ---- the copies: K and V of a tile into stage n % kStages --------------
-    // A block of up to 32 tokens is copied whole, plane by plane; of a larger
-    // one the tile's rows of codes and of scales.  Lanes 0..7 copy K's pieces,
-    // 8..15 V's.  In shared memory a tile is a plane of min(B, 32) tokens, or
-    // several.
+    // In shared memory a tile's K, and then its V, is a plane of bs = min(B, 32)
+    // tokens, or several: codes, then scales, in 16-byte vectors.  A lane copies
+    // vectors 32 i + lane, i < kWide, of both, and one of the last D / 8 of K
+    // (lanes 0 .. D/8 - 1) or of V (the next D / 8 lanes).
+    constexpr int kWide = D / 32;
     const uint32_t ring = smem_u32(dyn) + (uint32_t)(warp * kStages * kStage);
-    const uint32_t full = smem_u32(&sh.full[warp][0]);
     Walk ld = w;
-    const int piece = lane & 7;
-    const bool large = B > kTile;
-    const int bs = large ? kTile : B, per_tile = large ? 1 : kTile / bs;
-    const int pieces = large ? 2 : per_tile;
-    const bool mine = lane < 16 && piece < pieces;
-    const uint8_t* const pool = lane < 8 ? a.kc : a.vc;
-    const uint32_t bytes = !large ? bs * kRow : (piece == 0 ? kTile * (D / 2) : kTile * (D / 16));
-    const uint32_t dst0 = ring + (lane < 8 ? 0 : kPart) +
-                          (large ? piece * (kTile * (D / 2)) : piece * bytes);
-    const long long block_bytes = (long long)a.H * a.plane;
-    int l_first = 0, l_t0 = 0, l_last = 0;   // of the context being loaded
+    const int bs = min(B, kTile), per_tile = kTile / bs;
+    const uint32_t block_bytes = (uint32_t)a.H * (uint32_t)a.plane;
+    uint32_t at[kWide + 1];   // of each: its block in the tile << 16 | its offset in the plane
+#pragma unroll
+    for (int i = 0; i <= kWide; ++i) {
+      const int v = 32 * i + (i < kWide ? lane : lane & (D / 8 - 1)), vecs = bs * kRow / 16;
+      const int off = 16 * (v % vecs) + (i == kWide && B > kTile ? (B - kTile) * (D / 2) : 0);
+      at[i] = (uint32_t)(v / vecs) << 16 | (uint32_t)off;
+    }
+    const uint32_t dst = ring + 16 * lane;
+    const uint32_t dst_last = ring + 16 * (32 * kWide + (lane & (D / 8 - 1))) +
+                              (lane < D / 8 ? 0 : kPart);
+    const uint8_t* const pool_last = lane < D / 8 ? a.kc : a.vc;
+    int l_t0 = 0, l_last = 0, l_blk = 0;     // of the context being loaded
+    uint32_t l_head = 0;                     // its head's plane in a block
     int win = -1, ent = -1;                  // entries [32 win, 32 win + 32) of its table row
-    const uint8_t* l_src = nullptr;          // its head's plane in block 0
+    uint32_t win_bad = 0, bads = 0;          // those out of range; of the stages' blocks, 8 bits each
     auto load_context = [&]() {
-      l_first = first_token(ld.T, a);
-      l_t0 = (l_first / kTile + ld.k) * kTile;
+      const int first = first_token(ld.T, a);
+      l_blk = first >> a.log2B;
+      l_t0 = (first / kTile + ld.k) * kTile;
       l_last = (ld.T - 1) >> a.log2B;
-      l_src = pool + (size_t)ld.h * a.plane + (large && piece ? B * (D / 2) : 0);
+      l_head = (uint32_t)ld.h * (uint32_t)a.plane;
       win = -1;
     };
     load_context();
-    uint32_t odd_stages = 0;   // stages with a block that was not copied
     auto issue = [&](int st) {
       const int blk0 = l_t0 >> a.log2B;
       if ((blk0 >> 5) != win) {
@@ -708,32 +719,33 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
         const int idx = 32 * win + lane;
         ent = -2;   // no entry
         // entries of blocks that hold an attended token
-        if (idx >= (l_first >> a.log2B) && idx <= l_last) {
+        if (idx >= l_blk && idx <= l_last) {
           ent = __ldg(a.bt + (size_t)ld.i * a.stride + idx);
           if (ent < 0 || (long long)ent >= a.num_blocks) {
             set_error(a.err, PA_DEVERR_BLOCK_ID);
             ent = -1;
           }
         }
+        win_bad = __ballot_sync(kFull, ent == -1);
       }
-      const int e = __shfl_sync(kFull, ent, (blk0 + (large ? 0 : piece)) & 31);
-      const bool copy = mine && e >= 0;
-      uint32_t total = kStage;
-      odd_stages &= ~(1u << st);
-      if (__any_sync(kFull, mine && e < 0)) {
-        total = __popc(__ballot_sync(kFull, copy)) * bytes;
-        if (large) total = 0;   // one block: all pieces or none
-        const uint32_t bad = __ballot_sync(kFull, mine && e == -1) & 0xffu;
-        if (lane == 0) sh.bad[warp][st] = bad;
-        odd_stages |= 1u << st;
+      const uint32_t bad = (win_bad >> (blk0 & 31)) & ((1u << per_tile) - 1u);
+      bads = (bads & ~(0xffu << (8 * st))) | (bad << (8 * st));
+      const uint32_t tok = (uint32_t)l_t0 & (uint32_t)(B - 1);
+      const uint32_t so = (uint32_t)(st * kStage);
+#pragma unroll
+      for (int i = 0; i < kWide; ++i) {
+        const int e = __shfl_sync(kFull, ent, blk0 + (int)(at[i] >> 16));
+        const uint64_t off = (uint64_t)(uint32_t)e * block_bytes +
+                             (l_head + (at[i] & 0xffffu) + tok * (D / 2));
+        if (e >= 0) {
+          copy16(dst + so + 512 * i, a.kc + off);
+          copy16(dst + so + 512 * i + kPart, a.vc + off);
+        }
       }
-      if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, total);
-      __syncwarp();
-      if (copy) {
-        const uint8_t* src = l_src + e * block_bytes;
-        if (large) src += (l_t0 & (B - 1)) * (piece == 0 ? D / 2 : D / 16);
-        bulk_load(dst0 + st * kStage, src, bytes, full + 8 * st);
-      }
+      const int e = __shfl_sync(kFull, ent, blk0 + (int)(at[kWide] >> 16));
+      if (e >= 0 && lane < D / 4)
+        copy16(dst_last + so, pool_last + ((uint64_t)(uint32_t)e * block_bytes +
+                                           (l_head + (at[kWide] & 0xffffu) + tok * (D / 16))));
       l_t0 += kTile;
       --ld_left;
       if (++ld.k == ld.nt) {
@@ -761,12 +773,13 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
     }
 
     Context<D, kBF16, NH, kTwin> cx;
-    for (int n = 0; n < kStages; ++n)
+    for (int n = 0; n < kStages; ++n) {
       if (ld_left > 0) issue(n);
+      copies_commit();   // of every tile, issued or not: one group each
+    }
     int st = 0, seg_k0 = w.k, segments = 0;
     int first = 0, t0 = 0;   // of the tile's context and tile
-    uint32_t ph = 0;
-    bool live_warp = true, fresh = true;
+    bool fresh = true;
     while (left > 0) {
       if (fresh) {
         fresh = false;
@@ -775,35 +788,32 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
         t0 = (first / kTile + w.k) * kTile;
         cx.begin(a.q + ((size_t)w.i * a.Hq + (size_t)w.h * a.G) * D, a.G, a.scale_log2);
       }
-      if (live_warp && __any_sync(kFull, !mbar_wait_bounded(full + 8 * st, ph, nullptr))) {
-        if (lane == 0) set_error(a.err, PA_DEVERR_TIMEOUT);
-        live_warp = false;   // copies may be in flight: nothing more is issued or read
+      copies_wait<kStages - 1>();
+      __syncwarp();   // every lane's copies of this tile have landed
+      const uint32_t so = (uint32_t)(st * kStage);
+      const uint32_t bad = (bads >> (8 * st)) & 0xffu;
+      const bool edge = t0 < first || w.T - t0 < kTile || bad != 0u;
+      float s[2][NH][4];
+      uint32_t pb[2][NH][2], pl[2][NH][2];
+      const uint32_t kc[2] = {ok[0] + so, ok[1] + so}, ks[2] = {os[0] + so, os[1] + so};
+      const uint32_t vc[2] = {ov[0] + so, ov[1] + so}, vs[2] = {ow[0] + so, ow[1] + so};
+      cx.scores(s, kc, ks);
+      if (edge) {
+        uint32_t live = kFull;
+        if (t0 < first) live &= kFull << (first - t0);
+        if (w.T - t0 < kTile) live &= kFull >> (kTile - (w.T - t0));
+        if (bad)
+          for (int b = 0; b < kTile / bs; ++b)
+            if ((bad >> b) & 1u) live &= ~((bs == 32 ? kFull : (1u << bs) - 1u) << (b * bs));
+        cx.template weights<true>(s, live, pb, pl);
+        cx.template values<true>(pb, pl, live, vc, vs);
+      } else {
+        cx.template weights<false>(s, kFull, pb, pl);
+        cx.template values<false>(pb, pl, kFull, vc, vs);
       }
-      if (live_warp) {
-        const uint32_t so = (uint32_t)(st * kStage);
-        const uint32_t bad = (odd_stages >> st) & 1u ? sh.bad[warp][st] : 0u;
-        const bool edge = t0 < first || w.T - t0 < kTile || bad != 0u;
-        float s[2][NH][4];
-        uint32_t pb[2][NH][2], pl[2][NH][2];
-        const uint32_t kc[2] = {ok[0] + so, ok[1] + so}, ks[2] = {os[0] + so, os[1] + so};
-        const uint32_t vc[2] = {ov[0] + so, ov[1] + so}, vs[2] = {ow[0] + so, ow[1] + so};
-        cx.scores(s, kc, ks);
-        if (edge) {
-          uint32_t live = kFull;
-          if (t0 < first) live &= kFull << (first - t0);
-          if (w.T - t0 < kTile) live &= kFull >> (kTile - (w.T - t0));
-          if (bad)
-            for (int b = 0; b < kTile / bs; ++b)
-              if ((bad >> b) & 1u) live &= ~((bs == 32 ? kFull : (1u << bs) - 1u) << (b * bs));
-          cx.template weights<true>(s, live, pb, pl);
-          cx.template values<true>(pb, pl, live, vc, vs);
-        } else {
-          cx.template weights<false>(s, kFull, pb, pl);
-          cx.template values<false>(pb, pl, kFull, vc, vs);
-        }
-        __syncwarp();   // every lane has read the stage
-        if (ld_left > 0) issue(st);
-      }
+      __syncwarp();   // every lane has read the stage
+      if (ld_left > 0) issue(st);
+      copies_commit();
       const bool ends = w.k == w.nt - 1;
       if (ends || left == 1) {
         // the end of the context, or of this warp's part of it.  The warp's last
@@ -815,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
           const int rec = left <= (ends ? 1 + kStart : 1)
                               ? warp * (kStages * kStage / 4)
                               : kWarps * (kStages * kStage / 4) + warp * (int)rf;
-          if (live_warp) cx.store(slots + rec, a.G);
+          cx.store(slots + rec, a.G);
           if (lane == 0) {
             Part& p = sh.part[2 * warp + (segments > 0 ? 1 : 0)];
             p.pair = (long long)w.i * a.H + w.h;
@@ -828,10 +838,7 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
         }
         ++segments;
       }
-      if (++st == kStages) {
-        st = 0;
-        ph ^= 1u;
-      }
+      if (++st == kStages) st = 0;
       t0 += kTile;
       --left;
       ++g;
@@ -844,9 +851,6 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
         ++w.k;
       }
     }
-    if (!live_warp)   // leave with no copy in flight
-      for (int k = 0; k < kStages; ++k)
-        mbar_wait_bounded(full + 8 * k, k < st ? ph ^ 1u : ph, nullptr);
   }
   __syncthreads();
 
@@ -965,6 +969,8 @@ int make_plan(int Hq, int H, int D, int B, int q_dtype, int flags, int num_ctas,
   if (Hq % H != 0) return PA_ERR_INVALID_ARG;
   const int G = Hq / H;
   if (G > 16) return PA_ERR_UNSUPPORTED;
+  // a block's bytes are counted in 31 bits
+  if ((long long)H * B * fp4_row_bytes(D) > 0x7fffffffLL) return PA_ERR_UNSUPPORTED;
   flags &= ~PA_DECODE_TABLES_READY;
   if (flags == PA_DECODE_SIMT) return PA_ERR_UNSUPPORTED;
   if (flags != PA_DECODE_AUTO && flags != PA_DECODE_MMA) return PA_ERR_INVALID_ARG;
