@@ -65,9 +65,8 @@ namespace {
 // registers, which o, the queries and a tile's work need (32 contexts of 16 to
 // 32 K tokens: 197 us where two blocks took 205 and 16 warps of fewer registers
 // 196 to 205).  Five to eight warps a block measured no better.
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kBlocksPerSm = 3;
+__host__ __device__ constexpr int warps_of(int NH) { return NH == 1 ? 12 : 8; }
+constexpr int kLeast = 4;
 constexpr int kTile = 32;                 // tokens per tile (64: 190 us for 187)
 constexpr int kStages = 2;                // tiles in shared memory per warp (a third
                                           // measured the same)
@@ -147,6 +146,15 @@ __device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
 }
 __device__ __forceinline__ void copies_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// a lane's part of the codes of kBs tokens of K and V (one tile's apart at dst)
+template <int D, int kBs>
+__device__ __forceinline__ void copy_codes(uint32_t dst, const uint8_t* k, const uint8_t* v) {
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    copy16(dst + 16 * kBs * i, k + 16 * kBs * i);
+    copy16(dst + 16 * kBs * i + kTile * fp4_row_bytes(D), v + 16 * kBs * i);
+  }
 }
 template <int kPending>
 __device__ __forceinline__ void copies_wait() {
@@ -535,8 +543,9 @@ struct Part {
   int rec;            // its record, in floats from the start of shared memory
 };
 
+template <int kWarps>
 struct Shared {
-  long long run_pref[kThreads];   // tiles (of one head) before each thread's run of sequences
+  long long run_pref[kWarps * 32];   // tiles (of one head) before each thread's run of sequences
   long long warp_tot[kWarps];
   int warp_longest[kWarps];
   Part part[2 * kWarps];
@@ -547,11 +556,12 @@ struct Shared {
 };
 
 template <int D, bool kBF16, int NH, bool kTwin>
-__global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
+__global__ void __launch_bounds__(warps_of(NH) * 32, 1)
     decode_fp4_kernel(const Args a) {
   // per warp kStages tiles of K and V; after the last tile: [2 * kWarps] records
   extern __shared__ __align__(128) uint8_t dyn[];
-  __shared__ Shared sh;
+  constexpr int kWarps = warps_of(NH), kThreads = 32 * kWarps;
+  __shared__ Shared<kWarps> sh;
   constexpr int kRow = fp4_row_bytes(D), kPart = kTile * kRow, kStage = 2 * kPart;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int gid = lane >> 2, tig = lane & 3;
@@ -634,20 +644,24 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
   // at least kWarps units a block, so that small batches do not split contexts
   // between blocks for nothing
   const long long U = whole ? contexts : (total & low) * a.H;
-  const long long nb = min((long long)gridDim.x, (U + kWarps - 1) / kWarps);
+  const int least = whole ? 1 : kLeast;
+  const long long nb = min((long long)gridDim.x, (U + least - 1) / least);
   if ((long long)blockIdx.x >= nb) return;
   const long long c0 = U * blockIdx.x / nb, c1 = U * (blockIdx.x + 1) / nb;
   const long long n_cta = c1 - c0;
-  long long g = c0 + n_cta * warp / kWarps;
-  const long long g_end = c0 + n_cta * (warp + 1) / kWarps;
+  // a warp's place in the block's range: neighbours on one scheduler (warp % 4),
+  // so that few units fall on all four
+  const int place = (warp & 3) * (kWarps / 4) + (warp >> 2);
+  long long g = c0 + n_cta * place / kWarps;
+  const long long g_end = c0 + n_cta * (place + 1) / kWarps;
 
   if (g < g_end) {
     // the sequence of unit g: the last run that starts at or before it, then
     // along the run
     int r = 0;
 #pragma unroll
-    for (int b = kThreads / 2; b > 0; b >>= 1)
-      if (sh.run_pref[r + b] * a.H <= g) r += b;
+    for (int b = 256; b > 0; b >>= 1)
+      if (r + b < kThreads && sh.run_pref[r + b] * a.H <= g) r += b;
     Walk w;   // the tile being computed
     w.i = r * per;
     w.load_seq(a);
@@ -680,25 +694,21 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
 
     // ---- the copies: K and V of a tile into stage n % kStages --------------
     // In shared memory a tile's K, and then its V, is a plane of bs = min(B, 32)
-    // tokens, or several: codes, then scales, in 16-byte vectors.  A lane copies
-    // vectors 32 i + lane, i < kWide, of both, and one of the last D / 8 of K
-    // (lanes 0 .. D/8 - 1) or of V (the next D / 8 lanes).
-    constexpr int kWide = D / 32;
+    // tokens, or several: codes, then scales.  Each of these is copied by its
+    // own kLanes = bs lanes, 16 bytes a lane and copy: D / 32 copies of K and of
+    // V, then the last bytes (the scales) of K by the first and of V by the next
+    // D / 256 of the lanes.
     const uint32_t ring = smem_u32(dyn) + (uint32_t)(warp * kStages * kStage);
     Walk ld = w;
     const int bs = min(B, kTile), per_tile = kTile / bs;
+    const int piece = lane / bs, u = lane & (bs - 1), last = bs * D / 256;
     const uint32_t block_bytes = (uint32_t)a.H * (uint32_t)a.plane;
-    uint32_t at[kWide + 1];   // of each: its block in the tile << 16 | its offset in the plane
-#pragma unroll
-    for (int i = 0; i <= kWide; ++i) {
-      const int v = 32 * i + (i < kWide ? lane : lane & (D / 8 - 1)), vecs = bs * kRow / 16;
-      const int off = 16 * (v % vecs) + (i == kWide && B > kTile ? (B - kTile) * (D / 2) : 0);
-      at[i] = (uint32_t)(v / vecs) << 16 | (uint32_t)off;
-    }
-    const uint32_t dst = ring + 16 * lane;
-    const uint32_t dst_last = ring + 16 * (32 * kWide + (lane & (D / 8 - 1))) +
-                              (lane < D / 8 ? 0 : kPart);
-    const uint8_t* const pool_last = lane < D / 8 ? a.kc : a.vc;
+    const bool last_k = u < last, last_v = !last_k && u < 2 * last;
+    const uint32_t dst = ring + piece * (bs * kRow) + 16 * u;
+    const uint32_t dst_last = ring + piece * (bs * kRow) + bs * (D / 2) +
+                              (last_k ? 16 * u : 16 * (u - last) + kPart);
+    const uint8_t* const pool_last =
+        (last_k ? a.kc : a.vc) + (B * (D / 2) + 16 * (last_k ? u : u - last));
     int l_t0 = 0, l_last = 0, l_blk = 0;     // of the context being loaded
     uint32_t l_head = 0;                     // its head's plane in a block
     int win = -1, ent = -1;                  // entries [32 win, 32 win + 32) of its table row
@@ -730,22 +740,19 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
       }
       const uint32_t bad = (win_bad >> (blk0 & 31)) & ((1u << per_tile) - 1u);
       bads = (bads & ~(0xffu << (8 * st))) | (bad << (8 * st));
-      const uint32_t tok = (uint32_t)l_t0 & (uint32_t)(B - 1);
+      const uint32_t tok = (uint32_t)l_t0 & (uint32_t)(B - 1);   // 0 but in larger blocks
       const uint32_t so = (uint32_t)(st * kStage);
-#pragma unroll
-      for (int i = 0; i < kWide; ++i) {
-        const int e = __shfl_sync(kFull, ent, blk0 + (int)(at[i] >> 16));
-        const uint64_t off = (uint64_t)(uint32_t)e * block_bytes +
-                             (l_head + (at[i] & 0xffffu) + tok * (D / 2));
-        if (e >= 0) {
-          copy16(dst + so + 512 * i, a.kc + off);
-          copy16(dst + so + 512 * i + kPart, a.vc + off);
-        }
+      const int e = __shfl_sync(kFull, ent, blk0 + piece);
+      if (e >= 0) {
+        const uint64_t at = (uint64_t)(uint32_t)e * block_bytes + l_head;
+        const uint64_t codes = at + (tok * (D / 2) + 16 * u);
+        const uint8_t *k = a.kc + codes, *v = a.vc + codes;
+        if (bs == 32) copy_codes<D, 32>(dst + so, k, v);
+        else if (bs == 16) copy_codes<D, 16>(dst + so, k, v);
+        else if (bs == 8) copy_codes<D, 8>(dst + so, k, v);
+        else copy_codes<D, 4>(dst + so, k, v);
+        if (last_k || last_v) copy16(dst_last + so, pool_last + (at + tok * (D / 16)));
       }
-      const int e = __shfl_sync(kFull, ent, blk0 + (int)(at[kWide] >> 16));
-      if (e >= 0 && lane < D / 4)
-        copy16(dst_last + so, pool_last + ((uint64_t)(uint32_t)e * block_bytes +
-                                           (l_head + (at[kWide] & 0xffffu) + tok * (D / 16))));
       l_t0 += kTile;
       --ld_left;
       if (++ld.k == ld.nt) {
@@ -777,79 +784,71 @@ __global__ void __launch_bounds__(kThreads, NH == 1 ? kBlocksPerSm : 2)
       if (ld_left > 0) issue(n);
       copies_commit();   // of every tile, issued or not: one group each
     }
-    int st = 0, seg_k0 = w.k, segments = 0;
-    int first = 0, t0 = 0;   // of the tile's context and tile
-    bool fresh = true;
+    int st = 0, segments = 0;
     while (left > 0) {
-      if (fresh) {
-        fresh = false;
-        seg_k0 = w.k;
-        first = first_token(w.T, a);
-        t0 = (first / kTile + w.k) * kTile;
-        cx.begin(a.q + ((size_t)w.i * a.Hq + (size_t)w.h * a.G) * D, a.G, a.scale_log2);
-      }
-      copies_wait<kStages - 1>();
-      __syncwarp();   // every lane's copies of this tile have landed
-      const uint32_t so = (uint32_t)(st * kStage);
-      const uint32_t bad = (bads >> (8 * st)) & 0xffu;
-      const bool edge = t0 < first || w.T - t0 < kTile || bad != 0u;
-      float s[2][NH][4];
-      uint32_t pb[2][NH][2], pl[2][NH][2];
-      const uint32_t kc[2] = {ok[0] + so, ok[1] + so}, ks[2] = {os[0] + so, os[1] + so};
-      const uint32_t vc[2] = {ov[0] + so, ov[1] + so}, vs[2] = {ow[0] + so, ow[1] + so};
-      cx.scores(s, kc, ks);
-      if (edge) {
-        uint32_t live = kFull;
-        if (t0 < first) live &= kFull << (first - t0);
-        if (w.T - t0 < kTile) live &= kFull >> (kTile - (w.T - t0));
-        if (bad)
-          for (int b = 0; b < kTile / bs; ++b)
-            if ((bad >> b) & 1u) live &= ~((bs == 32 ? kFull : (1u << bs) - 1u) << (b * bs));
-        cx.template weights<true>(s, live, pb, pl);
-        cx.template values<true>(pb, pl, live, vc, vs);
-      } else {
-        cx.template weights<false>(s, kFull, pb, pl);
-        cx.template values<false>(pb, pl, kFull, vc, vs);
-      }
-      __syncwarp();   // every lane has read the stage
-      if (ld_left > 0) issue(st);
-      copies_commit();
-      const bool ends = w.k == w.nt - 1;
-      if (ends || left == 1) {
-        // the end of the context, or of this warp's part of it.  The warp's last
-        // part goes where its tiles were, an earlier one to the warp's slot.
-        cx.finish();
-        if (seg_k0 == 0 && ends) {
-          cx.write(a.out + ((size_t)w.i * a.Hq + (size_t)w.h * a.G) * D, a.G, a.v_scale);
+      // a context, or this warp's part of one: its tiles w.k .. w.k + run - 1
+      const int run = min(w.nt - w.k, left), first = first_token(w.T, a);
+      const bool ends = w.k + run == w.nt;
+      g -= w.k;   // the unit of its first tile
+      cx.begin(a.q + ((size_t)w.i * a.Hq + (size_t)w.h * a.G) * D, a.G, a.scale_log2);
+      int t0 = (first / kTile + w.k) * kTile;
+      for (int n = run; n > 0; --n) {
+        copies_wait<kStages - 1>();
+        __syncwarp();   // every lane's copies of this tile have landed
+        const uint32_t so = (uint32_t)(st * kStage);
+        const uint32_t bad = (bads >> (8 * st)) & 0xffu;
+        const bool edge = t0 < first || w.T - t0 < kTile || bad != 0u;
+        float s[2][NH][4];
+        uint32_t pb[2][NH][2], pl[2][NH][2];
+        const uint32_t kc[2] = {ok[0] + so, ok[1] + so}, ks[2] = {os[0] + so, os[1] + so};
+        const uint32_t vc[2] = {ov[0] + so, ov[1] + so}, vs[2] = {ow[0] + so, ow[1] + so};
+        cx.scores(s, kc, ks);
+        if (edge) {
+          uint32_t live = kFull;
+          if (t0 < first) live &= kFull << (first - t0);
+          if (w.T - t0 < kTile) live &= kFull >> (kTile - (w.T - t0));
+          if (bad)
+            for (int b = 0; b < kTile / bs; ++b)
+              if ((bad >> b) & 1u) live &= ~((bs == 32 ? kFull : (1u << bs) - 1u) << (b * bs));
+          cx.template weights<true>(s, live, pb, pl);
+          cx.template values<true>(pb, pl, live, vc, vs);
         } else {
-          const int rec = left <= (ends ? 1 + kStart : 1)
-                              ? warp * (kStages * kStage / 4)
-                              : kWarps * (kStages * kStage / 4) + warp * (int)rf;
-          cx.store(slots + rec, a.G);
-          if (lane == 0) {
-            Part& p = sh.part[2 * warp + (segments > 0 ? 1 : 0)];
-            p.pair = (long long)w.i * a.H + w.h;
-            p.g0 = g - w.k;
-            p.nt = w.nt;
-            p.begins = seg_k0 == 0;
-            p.ends = ends;
-            p.rec = rec;
-          }
+          cx.template weights<false>(s, kFull, pb, pl);
+          cx.template values<false>(pb, pl, kFull, vc, vs);
         }
-        ++segments;
+        __syncwarp();   // every lane has read the stage
+        if (ld_left > 0) issue(st);
+        copies_commit();
+        if (++st == kStages) st = 0;
+        t0 += kTile;
       }
-      if (++st == kStages) st = 0;
-      t0 += kTile;
-      --left;
-      ++g;
-      if (ends) {
-        w.advance(a);
-        left -= kStart;
-        g += kStart;
-        fresh = true;
+      left -= run;
+      // the end of the context, or of this warp's part of it.  The warp's last
+      // part goes where its tiles were, an earlier one to the warp's slot.
+      cx.finish();
+      if (w.k == 0 && ends) {
+        cx.write(a.out + ((size_t)w.i * a.Hq + (size_t)w.h * a.G) * D, a.G, a.v_scale);
       } else {
-        ++w.k;
+        const int rec = left <= (ends ? kStart : 0)
+                            ? warp * (kStages * kStage / 4)
+                            : kWarps * (kStages * kStage / 4) + warp * (int)rf;
+        cx.store(slots + rec, a.G);
+        if (lane == 0) {
+          Part& p = sh.part[2 * place + (segments > 0 ? 1 : 0)];
+          p.pair = (long long)w.i * a.H + w.h;
+          p.g0 = g;
+          p.nt = w.nt;
+          p.begins = w.k == 0;
+          p.ends = ends;
+          p.rec = rec;
+        }
       }
+      ++segments;
+      // the next context of the range, if there is one
+      g += w.nt + kStart;
+      left -= kStart;
+      w.k = w.nt - 1;
+      if (left > 0) w.advance(a);
     }
   }
   __syncthreads();
@@ -941,8 +940,8 @@ Kernel pick_d(bool bf16, int G) {
 // the ring of every warp (which its last part's record shares) and a slot each
 // for an earlier part
 size_t smem_bytes(int D, int G) {
-  return (size_t)kWarps * kStages * 2 * kTile * fp4_row_bytes(D) +
-         kWarps * rec_floats(G, D) * sizeof(float);
+  return (size_t)warps_of(G > 8 ? 2 : 1) *
+         (kStages * 2 * kTile * fp4_row_bytes(D) + rec_floats(G, D) * sizeof(float));
 }
 static_assert(rec_floats(16, 128) * 4 <= kStages * 2 * kTile * fp4_row_bytes(128) &&
                   rec_floats(16, 64) * 4 <= kStages * 2 * kTile * fp4_row_bytes(64),
@@ -950,14 +949,13 @@ static_assert(rec_floats(16, 128) * 4 <= kStages * 2 * kTile * fp4_row_bytes(128
 
 struct Plan {
   Kernel kern;
-  int grid;
+  int grid, threads;
   size_t smem, count_bytes, rec_bytes;
 };
 
-// Blocks per SM depend on the kernel, the group size and the device: looked up
-// once each, with the kernel's opt-in to its shared memory.
+// The kernels' opt-in to their shared memory, once a device.
 constexpr int kMaxDevices = 64;
-int g_per_sm[kMaxDevices][2][2][17];   // [device][D == 128][bf16][G], 0 = not yet
+bool g_ready[kMaxDevices][2][2][3];   // [device][D == 128][bf16][heads <= 4, <= 8, <= 16]
 std::mutex g_mu;
 
 int make_plan(int Hq, int H, int D, int B, int q_dtype, int flags, int num_ctas, Plan* p) {
@@ -979,24 +977,19 @@ int make_plan(int Hq, int H, int D, int B, int q_dtype, int flags, int num_ctas,
   p->smem = smem_bytes(D, G);
   DeviceInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  int per_sm;
   {
     std::lock_guard<std::mutex> lk(g_mu);
-    int& c = g_per_sm[di.device][D == 128][bf16][G];
-    if (c == 0) {
-      const size_t most = smem_bytes(D, G > 8 ? 16 : 8);
-      int n = 0;
-      cudaError_t e = cudaFuncSetAttribute(p->kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)most);
+    bool& ready = g_ready[di.device][D == 128][bf16][G > 8 ? 2 : (G > 4 ? 1 : 0)];
+    if (!ready) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(p->kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (int)smem_bytes(D, G > 8 ? 16 : 8));
       if (e) return launch_status(e, "cudaFuncSetAttribute (4-bit decode)");
-      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, p->kern, kThreads, p->smem);
-      if (e) return launch_status(e, "occupancy (4-bit decode)");
-      if (n < 1) return PA_ERR_UNSUPPORTED;
-      c = n;
+      ready = true;
     }
-    per_sm = c;
   }
-  p->grid = num_ctas > 0 ? num_ctas : di.sm_count * per_sm;
+  p->threads = 32 * warps_of(G > 8 ? 2 : 1);
+  p->grid = num_ctas > 0 ? num_ctas : di.sm_count;
   if (p->grid > PA_DECODE_MAX_CTAS) return PA_ERR_INVALID_ARG;
   p->count_bytes = (size_t)PA_DECODE_MAX_CTAS * sizeof(uint32_t);
   p->rec_bytes = (size_t)p->grid * 2 * rec_floats(G, D) * sizeof(float);
@@ -1064,7 +1057,7 @@ extern "C" int pa_decode_fp4(const void* q, const void* k_cache, const void* v_c
   a.window = window;
   a.early_tables = (flags & PA_DECODE_TABLES_READY) ? 1 : 0;
   clear_stale_error();
-  return launch_status(launch_pdl(p.kern, dim3((unsigned)p.grid), dim3(kThreads), p.smem,
+  return launch_status(launch_pdl(p.kern, dim3((unsigned)p.grid), dim3((unsigned)p.threads), p.smem,
                                   static_cast<cudaStream_t>(stream), a),
                        "4-bit decode launch");
 }
