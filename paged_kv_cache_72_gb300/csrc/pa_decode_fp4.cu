@@ -82,6 +82,7 @@ constexpr int kStart = 1;
 // with 64 of 1 to 256, and a limit of 16 takes 21.4 for 15.4 with 64 of 128 to
 // 512.
 constexpr int kWhole = 8;
+constexpr int kRecords = 4;               // of a split context, loaded at a time
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kUnitBits = 44, kCounted = 1 << 18;   // of the scanned sums; sequences it counts
 // Weights are exp2(x - base) with base = a maximum less kShift, and a new base
@@ -503,6 +504,17 @@ struct Context {
   }
 };
 
+// Elements 4 c .. 4 c + 3 of row r of a record.
+struct Vec {
+  float4 o;
+  float m, l;
+  __device__ __forceinline__ void load(const float* rec, int G, int D, int r, int c) {
+    o = *reinterpret_cast<const float4*>(rec + r * D + 4 * c);
+    m = rec[G * D + r];
+    l = rec[G * D + G + r];
+  }
+};
+
 // Four elements of one row of a context, merged over parts: acc = sum_p
 // 2^(m_p - m) o_p, l likewise, m the largest m_p.
 struct Merged {
@@ -520,10 +532,17 @@ struct Merged {
     acc.w = acc.w * wa + v.w * wb;
   }
 
-  // row r, elements 4 c .. 4 c + 3 of a record
   __device__ __forceinline__ void fold_record(const float* rec, int G, int D, int r, int c) {
-    fold(rec[(size_t)G * D + r], rec[(size_t)G * D + G + r],
-         *reinterpret_cast<const float4*>(rec + (size_t)r * D + 4 * c));
+    Vec v;
+    v.load(rec, G, D, r, c);
+    fold(v.m, v.l, v.o);
+  }
+  __device__ __forceinline__ void store_record(float* rec, int G, int D, int r, int c) const {
+    *reinterpret_cast<float4*>(rec + r * D + 4 * c) = acc;
+    if (c == 0) {
+      rec[G * D + r] = m;
+      rec[G * D + G + r] = l;
+    }
   }
 
   template <bool kBF16>
@@ -543,6 +562,12 @@ struct Part {
   int rec;            // its record, in floats from the start of shared memory
 };
 
+// A context whose records, those of blocks first .. first + count - 1, are joined here.
+struct Merge {
+  long long pair;
+  int first, count;
+};
+
 template <int kWarps>
 struct Shared {
   long long run_pref[kWarps * 32];   // tiles (of one head) before each thread's run of sequences
@@ -552,7 +577,7 @@ struct Shared {
   int group_first[2 * kWarps + 1];
   int groups;
   int merges;                     // contexts this block owes the merge of
-  Part merge[2];
+  Merge merge[2];
 };
 
 template <int D, bool kBF16, int NH, bool kTwin>
@@ -882,8 +907,7 @@ __global__ void __launch_bounds__(warps_of(NH) * 32, 1)
     }
     const long long pair = sh.part[k0].pair;
     if (sh.part[k0].begins && sh.part[k_last].ends) {
-      const long long i = pair / a.H, h = pair % a.H;
-      x.write<kBF16>(a.out + ((size_t)i * a.Hq + (size_t)h * a.G + r) * D + 4 * c, a.v_scale);
+      x.write<kBF16>(a.out + ((size_t)pair * a.G + r) * D + 4 * c, a.v_scale);
     } else {
       // record 0: the context began in an earlier block; 1: it begins here
       float* rec = a.ws_rec + ((size_t)blockIdx.x * 2 + (sh.part[k0].begins ? 1 : 0)) * rf;
@@ -905,24 +929,51 @@ __global__ void __launch_bounds__(warps_of(NH) * 32, 1)
       // those counted before it
       if (atom_add_acq_rel_gpu(cnt, 1u) + 1u == (uint32_t)(e - f + 1)) {
         *cnt = 0u;   // ready for the next call
-        sh.merge[atomicAdd(&sh.merges, 1)] = p;
+        Merge& m = sh.merge[atomicAdd(&sh.merges, 1)];
+        m.pair = p.pair;
+        m.first = (int)f;
+        m.count = (int)(e - f + 1);
       }
     }
   }
   __syncthreads();
+  // ---- the contexts whose last record this block counted -------------------
+  // their records, record 1 of the first block and record 0 of the others, in
+  // equal runs over the threads that a context's vectors leave free
   for (int k = 0; k < sh.merges; ++k) {
-    const Part p = sh.merge[k];
-    const long long f = ((p.g0 + 1) * nb - 1) / U, e = ((p.g0 + p.nt) * nb - 1) / U;
-    const long long i = p.pair / a.H, h = p.pair % a.H;
-    for (int t = tid; t < per_group; t += kThreads) {
+    const Merge m = sh.merge[k];
+    const float* const recs = a.ws_rec + (size_t)m.first * 2 * rf;
+    uint16_t* const out = a.out + (size_t)m.pair * a.G * D;
+    const int rows = per_group, runs = m.count <= kRecords ? 1 : max(1, kThreads / rows);
+    const int run = runs == 1 ? 0 : tid / rows;
+    for (int t = tid - run * rows; t < rows && run < runs; t += kThreads) {
       const int r = t / cols, c = t % cols;
-      // record 1 of block f, then record 0 of blocks f + 1 .. e
+      const int n1 = m.count * (run + 1) / runs;
       Merged x;
-      x.fold_record(a.ws_rec + ((size_t)f * 2 + 1) * rf, a.G, D, r, c);
-#pragma unroll 4
-      for (long long b = f + 1; b <= e; ++b)
-        x.fold_record(a.ws_rec + (size_t)b * 2 * rf, a.G, D, r, c);
-      x.write<kBF16>(a.out + ((size_t)i * a.Hq + (size_t)h * a.G + r) * D + 4 * c, a.v_scale);
+      for (int n = m.count * run / runs; n < n1; n += kRecords) {
+        Vec v[kRecords];
+#pragma unroll
+        for (int b = 0; b < kRecords; ++b) {
+          const int i = min(n + b, n1 - 1);
+          v[b].load(recs + (size_t)(2 * i + (i == 0 ? 1 : 0)) * rf, a.G, D, r, c);
+        }
+#pragma unroll
+        for (int b = 0; b < kRecords; ++b)
+          if (n + b < n1) x.fold(v[b].m, v[b].l, v[b].o);
+      }
+      if (runs == 1)
+        x.write<kBF16>(out + (size_t)4 * t, a.v_scale);
+      else
+        x.store_record(slots + run * rf, a.G, D, r, c);
+    }
+    if (runs > 1) {
+      __syncthreads();
+      if (tid < rows) {
+        Merged x;
+        for (int b = 0; b < runs; ++b) x.fold_record(slots + b * rf, a.G, D, tid / cols, tid % cols);
+        x.write<kBF16>(out + (size_t)4 * tid, a.v_scale);
+      }
+      __syncthreads();
     }
   }
 }
