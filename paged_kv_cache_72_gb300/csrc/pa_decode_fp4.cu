@@ -7,25 +7,31 @@
 // code * s16 has at most 6 significant bits and lies in [2^-10, 2688], so it is
 // exact in binary16, and every product is an f16 x f16 MMA with fp32 sums.
 //
-// Bound: half bytes, half issue.  0.5625 bytes an element are read once and
-// nothing else is, but a tile of 32 tokens also costs a warp 34 MMAs, 128
-// conversions and 128 multiplies by scales (head_dim 128, up to 8 heads a KV
-// head).  32 contexts of 16 to 32 K tokens, 64 heads over 8 of 128 (883 MB):
-// 184 us, 4.8 TB/s; the copies alone take 144 us, the arithmetic alone 162.  256
-// contexts of 17 to 4,096 tokens, 32 over 8 heads (125 MB): 38.5 us, of which
-// the copies are 33.7.  So the arithmetic is kept lean and the copies are kept
-// going under it:
+// Bound: bytes, and close behind them issue slots.  0.5625 bytes an element are
+// read once and nothing else is, but a tile of 32 tokens also costs a warp 610
+// instructions, 34 of them MMAs, 128 conversions and 128 multiplies by scales
+// (head_dim 128, up to 8 heads a KV head).  32 contexts of 16 to 32 K tokens,
+// 64 heads over 8 of 128 (883 MB): 162 us, 5.46 TB/s, 80% of a copy's rate;
+// copies without arithmetic take 144 us.  256 contexts of 17 to 4,096 tokens, 32
+// over 8 heads (125 MB): 35.1 us, of which 21 are tiles, 7 the start up to the
+// first tile and 7 the joining of split contexts.  So:
 //  * One warp is one pipeline.  A warp owns a (sequence, KV head) context or a
-//    contiguous range of one.  Its tiles arrive by bulk copies in a ring of
-//    kStages tiles of its own, filled and waited for by the warp itself: no
-//    producer, and no barrier between warps until a block's end.  (Fragments
-//    loaded straight from global memory took 215 us where the ring took 205.)
+//    contiguous range of one.  Its tiles arrive in a ring of kStages tiles of
+//    its own that it fills itself with 16-byte asynchronous copies, nine a lane
+//    and tile: no producer, no barrier object, and no barrier between warps
+//    until a block's end.  (One bulk copy a plane, with a barrier object a
+//    stage, cost a warp 630 cycles a tile to issue against 480; loads straight
+//    into fragments were slower than either.)
+//  * Twelve warps, one block an SM.  Its warps get equal ranges and equal turns.
+//    With three blocks of four warps the scheduler serves the oldest block
+//    first, and the other two finish 7 and 15% later on a half-empty SM (180 us
+//    for 162).
 //  * Transposed products: S^T = K Q^T (16 tokens x 8 heads), O^T += V^T P^T
 //    (16 head_dim rows x 8 heads), so that K and V are the A operands and 8
 //    heads, not 16, fill a product; more than 8 heads a KV head take two tiles.
 //  * The softmax's base is lazy (below), the weights' sums are one more MMA row
-//    of ones, and tiles that need no mask run code without one (together 238 to
-//    215 us).
+//    of ones, and tiles that need no mask run code without one (238 to 215 us
+//    when they came in, together).
 //
 // Index maps (a contraction's order is free, an output row's place is undone
 // at the write):
@@ -61,26 +67,24 @@ namespace pa {
 
 namespace {
 
-// Four warps a block and three blocks an SM: 12 warps leave a thread 168
-// registers, which o, the queries and a tile's work need (32 contexts of 16 to
-// 32 K tokens: 197 us where two blocks took 205 and 16 warps of fewer registers
-// 196 to 205).  Five to eight warps a block measured no better.
+// Twelve warps leave a thread 168 registers, which o, the queries and a tile's
+// work need; 16 warps of 128 spill and measured the same on long contexts and 3
+// to 10% more on short ones.  Two head tiles a KV head take 8 warps of 255.
 __host__ __device__ constexpr int warps_of(int NH) { return NH == 1 ? 12 : 8; }
+constexpr int kTile = 32;                 // tokens per tile
+constexpr int kStages = 2;                // tiles in shared memory per warp (3 measured the same)
+// A block takes at least kLeast units, one a scheduler; 2 and 8 measured the same.
 constexpr int kLeast = 4;
-constexpr int kTile = 32;                 // tokens per tile (64: 190 us for 187)
-constexpr int kStages = 2;                // tiles in shared memory per warp (a third
-                                          // measured the same)
 // A context's share of the work is its tiles and kStart for its start and end
 // (queries to fragments, the write): without it a warp whose range holds many
-// short contexts finishes last.  0 / 1 / 2 / 3 measured 91.9 / 67.7 / 69.2 /
-// 70.7 us for 64 contexts of 1 to 2,048 tokens and 32 KV heads, 41.7 / 38.5 /
-// 39.0 / 40.1 for the 256 contexts above.
+// short contexts finishes last.  0 / 1 / 2 measured 85.6 / 62.2 / 62.9 us for
+// 64 contexts of 1 to 2,048 tokens and 32 KV heads, 38.8 / 35.6 / 36.3 for the
+// 256 contexts above.
 constexpr int kStart = 1;
 // Contexts of at most kWhole tiles go to one warp each when there are warps
-// enough, which saves joining parts: 6.4 us for 8.9 with 16 contexts of 1 to 64
-// tokens and 8 KV heads, 18.1 for 20.6 with 200 of 16 to 256; but 13.1 for 12.2
-// with 64 of 1 to 256, and a limit of 16 takes 21.4 for 15.4 with 64 of 128 to
-// 512.
+// enough, which saves joining parts: 7.1 us for 9.1 with 16 contexts of 1 to 64
+// tokens and 8 KV heads, 18.0 for 20.4 with 200 of 16 to 256 (12.0 for 11.1 with
+// 32 of 16 to 250).
 constexpr int kWhole = 8;
 constexpr int kRecords = 4;               // of a split context, loaded at a time
 constexpr uint32_t kFull = 0xffffffffu;
@@ -666,8 +670,8 @@ __global__ void __launch_bounds__(warps_of(NH) * 32, 1)
     }
 
   // ---- this block's and this warp's range of units -------------------------
-  // at least kWarps units a block, so that small batches do not split contexts
-  // between blocks for nothing
+  // at least kLeast units a block, so that small batches do not split contexts
+  // between blocks for nothing; whole, a context a warp
   const long long U = whole ? contexts : (total & low) * a.H;
   const int least = whole ? 1 : kLeast;
   const long long nb = min((long long)gridDim.x, (U + least - 1) / least);
