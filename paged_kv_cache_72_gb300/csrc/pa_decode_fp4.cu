@@ -527,7 +527,7 @@ struct Merged {
 
   __device__ __forceinline__ void fold(float mk, float lk, const float4& v) {
     const float mn = fmaxf(m, mk), base = mn == -INFINITY ? 0.f : mn;
-    const float wa = exp2f(m - base), wb = exp2f(mk - base);
+    const float wa = ex2_approx(m - base), wb = ex2_approx(mk - base);
     m = mn;
     l = l * wa + lk * wb;
     acc.x = acc.x * wa + v.x * wb;
@@ -536,6 +536,13 @@ struct Merged {
     acc.w = acc.w * wa + v.w * wb;
   }
 
+  __device__ __forceinline__ void take_record(const float* rec, int G, int D, int r, int c) {
+    Vec v;
+    v.load(rec, G, D, r, c);
+    acc = v.o;
+    m = v.m;
+    l = v.l;
+  }
   __device__ __forceinline__ void fold_record(const float* rec, int G, int D, int r, int c) {
     Vec v;
     v.load(rec, G, D, r, c);
@@ -898,28 +905,31 @@ __global__ void __launch_bounds__(warps_of(NH) * 32, 1)
     }
   }
   __syncthreads();
-  const int cols = D / 4, per_group = a.G * cols;
-  for (int e = tid; e < sh.groups * per_group; e += kThreads) {
-    const int gr = e / per_group, r = (e % per_group) / cols, c = e % cols;
+  constexpr int cols = D / 4;
+  const int per_group = a.G * cols;
+  const int step_gr = kThreads / per_group, step_t = kThreads % per_group;
+  for (int gr = tid / per_group, t = tid % per_group; gr < sh.groups;) {
+    const int r = t / cols, c = t % cols;
     const int k0 = sh.group_first[gr], k1 = sh.group_first[gr + 1];
+    const long long pair = sh.part[k0].pair;
+    const int begins = sh.part[k0].begins;
+    int ends = sh.part[k0].ends;
     Merged x;
-    int k_last = k0;
-    for (int k = k0; k < k1; ++k) {
+    x.take_record(slots + sh.part[k0].rec, a.G, D, r, c);
+    for (int k = k0 + 1; k < k1; ++k) {
       if (sh.part[k].pair < 0) continue;
-      k_last = k;
+      ends = sh.part[k].ends;
       x.fold_record(slots + sh.part[k].rec, a.G, D, r, c);
     }
-    const long long pair = sh.part[k0].pair;
-    if (sh.part[k0].begins && sh.part[k_last].ends) {
+    if (begins && ends)
       x.write<kBF16>(a.out + ((size_t)pair * a.G + r) * D + 4 * c, a.v_scale);
-    } else {
-      // record 0: the context began in an earlier block; 1: it begins here
-      float* rec = a.ws_rec + ((size_t)blockIdx.x * 2 + (sh.part[k0].begins ? 1 : 0)) * rf;
-      *reinterpret_cast<float4*>(rec + (size_t)r * D + 4 * c) = x.acc;
-      if (c == 0) {
-        rec[(size_t)a.G * D + r] = x.m;
-        rec[(size_t)a.G * D + a.G + r] = x.l;
-      }
+    else   // record 0: the context began in an earlier block; 1: it begins here
+      x.store_record(a.ws_rec + ((size_t)blockIdx.x * 2 + begins) * rf, a.G, D, r, c);
+    gr += step_gr;
+    t += step_t;
+    if (t >= per_group) {
+      t -= per_group;
+      ++gr;
     }
   }
   __syncthreads();
