@@ -13,8 +13,8 @@
 // (head_dim 128, up to 8 heads a KV head).  32 contexts of 16 to 32 K tokens,
 // 64 heads over 8 of 128 (883 MB): 162 us, 5.46 TB/s, 80% of a copy's rate;
 // copies without arithmetic take 144 us.  256 contexts of 17 to 4,096 tokens, 32
-// over 8 heads (125 MB): 35.1 us, of which 21 are tiles, 7 the start up to the
-// first tile and 7 the joining of split contexts.  So:
+// over 8 heads (125 MB): 34.0 us, of which 21 are tiles, 7 the start up to the
+// first tile and 6 the joining of split contexts.  So:
 //  * One warp is one pipeline.  A warp owns a (sequence, KV head) context or a
 //    contiguous range of one.  Its tiles arrive in a ring of kStages tiles of
 //    its own that it fills itself with 16-byte asynchronous copies, nine a lane

@@ -599,3 +599,29 @@ def test_decodes_on_two_streams_at_once(cuda_device):
     for a, out, st in zip(alone, kept, states):
         assert all(torch.equal(o, a) for o in out)
         assert pa.pa_get_error(st.err) == 0
+
+
+@pytest.mark.parametrize("B", [4, 8, 32, 128])
+@pytest.mark.parametrize("window", [0, 150])
+def test_decode_leaves_out_bad_blocks_of_every_size(cuda_device, B, window):
+    # of 300 tokens, whole blocks drop out at both ends and inside a tile; the rest is
+    # attended to as if their weights were zero
+    st = State(630 + B, W.F16, 4, 2, 64, B, [300, 300, 5], window=window)
+    lost = [299 // B] if B > 32 else sorted({180 // B, 180 // B + 2, 299 // B})
+    bt = st.bt.copy()
+    bt[0, lost] = [len(st.k), -7, 1 << 30][:len(lost)]
+    st.dev["bt"] = torch.from_numpy(bt).cuda()
+    out = st.decode()
+    assert pa.pa_get_error(st.err) == pa.PA_DEVERR_BLOCK_ID
+    q = bits_to_f64(st.q, W.F16)
+    k, v = oracle.fp4_dequant(st.k, 64) * st.k_scale, oracle.fp4_dequant(st.v, 64) * st.v_scale
+    rows = [t for t in range(max(0, 300 - window) if window else 0, 300) if t // B not in lost]
+    blk, off = st.bt[0, np.array(rows) // B], np.array(rows) % B
+    o, spread = st.expected()
+    for h in range(4):
+        kk, vv = k[blk, off, h // 2], v[blk, off, h // 2]
+        w = np.exp(st.scale * (kk @ q[0, h]) - (st.scale * (kk @ q[0, h])).max())
+        w /= w.sum()
+        o[0, h] = w @ vv
+        spread[0, h] = w @ np.abs(vv - o[0, h])
+    rounding_report(bits_of(out), o, spread, W.F16, _u_p(W.F16), "B=%d" % B)
