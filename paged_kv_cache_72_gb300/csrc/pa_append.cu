@@ -307,6 +307,9 @@ __device__ __forceinline__ void store_row(uint8_t* pool, const uint4& x, long lo
 // Rows a thread group loads before it works on the first (8: 58 us for 50 in the
 // append of 8,192 tokens; 2 measured no better).
 constexpr int kBatch = 4;
+constexpr int kMostShares = 16;
+constexpr int kPasses = 10;
+constexpr int kBlocks = 7;
 
 // One block per token (blockIdx.x) and share of its rows (blockIdx.y): query
 // rows, then key rows, then value rows, each D / 8 lanes wide.  The angles are
@@ -316,14 +319,19 @@ constexpr int kBatch = 4;
 // slot is known.  Six blocks an SM: enough rows in flight without the spills of
 // eight (50 us; five 52, eight 88 with 8,192 tokens).
 template <int D, bool kBF16, int kPool, bool kNorm>
-__global__ void __launch_bounds__(kThreads, 6) append_kernel(const AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const AppendArgs a, int log2_shares,
+                                                             long long n) {
   constexpr int LPR = D / 8;               // lanes per row
-  constexpr int RPP = kThreads / LPR;      // rows per pass of the block
+  constexpr int RPP = 32 / LPR;            // rows per pass of a warp
   grid_dep_wait();
   grid_dep_launch();
-  const long long tok = blockIdx.x;
-  const int d0 = 8 * (threadIdx.x % LPR);
-  const int r0 = blockIdx.y * RPP + threadIdx.x / LPR, step = gridDim.y * RPP;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long unit = (long long)blockIdx.x * (kThreads / 32) + warp;
+  const long long tok = unit >> log2_shares;
+  const int shares = 1 << log2_shares, share = (int)unit & (shares - 1);
+  if (tok >= n) return;
+  const int d0 = 8 * (lane % LPR);
+  const int r0 = share * RPP + lane / LPR, step = shares * RPP;
   const uint16_t* const qr = a.q + tok * a.q_stride + d0;
   const uint16_t* const kr = a.k + tok * a.k_stride + d0;
   const uint16_t* const vr = a.v + tok * a.v_stride + d0;
@@ -339,17 +347,17 @@ __global__ void __launch_bounds__(kThreads, 6) append_kernel(const AppendArgs a)
     xv = *reinterpret_cast<const uint4*>(vr + r0 * D);
   }
   int pos;
-  const bool lead = threadIdx.x == 0 && blockIdx.y == 0;
+  const bool lead = lane == 0 && share == 0;
   const long long slot = append_slot(a, tok, lead, pos);
   if (a.slots && lead) a.slots[tok] = slot;
-  if (slot < 0) return;                    // the whole block: every thread found the same slot
+  if (slot < 0) return;                    // the whole warp: every lane found the same slot
   Turn t;
   t.load(a, pos, d0);
-  // rows in lockstep over the block (the shuffles need every lane)
+  // rows in lockstep over the warp (the shuffles need every lane)
   if (kNorm && a.q_norm) t.join<kBF16>(a.q_norm, a.rot > 0, d0);
   uint16_t* const qo = a.q_out + (size_t)tok * a.Hq * D + d0;
-  for (int first = blockIdx.y * RPP; first < a.Hq; first += kBatch * step) {
-    const int hb = first + threadIdx.x / LPR;
+  for (int first = share * RPP; first < a.Hq; first += kBatch * step) {
+    const int hb = first + lane / LPR;
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       if (first + b * step >= a.Hq) break;
@@ -364,8 +372,8 @@ __global__ void __launch_bounds__(kThreads, 6) append_kernel(const AppendArgs a)
     if (a.q_norm) t.load(a, pos, d0);
     if (a.k_norm) t.join<kBF16>(a.k_norm, a.rot > 0, d0);
   }
-  for (int first = blockIdx.y * RPP; first < a.H; first += step) {
-    const int h = first + threadIdx.x / LPR;
+  for (int first = share * RPP; first < a.H; first += step) {
+    const int h = first + lane / LPR;
     const bool in = h < a.H;
     const uint4 k = xk, v = xv;
     if (h + step < a.H) {
@@ -522,16 +530,20 @@ int tokens_per_block(int D, int rows, long long n, int sm_count) {
 
 template <int D, bool kBF16, int kPool, bool kNorm>
 cudaError_t launch_append_n(const AppendArgs& a, long long n, int sm_count, cudaStream_t s) {
-  // few tokens: a token's rows spread over several blocks, until two blocks an
-  // SM; many tokens fill the GPU by themselves (32 tokens of 64 and 8 heads into
-  // a 4-bit pool: append and read-back 4.6 us, 5.4 with one block a token)
-  const int per_pass = kThreads / (D / 8), most = a.Hq > a.H ? a.Hq : a.H;
+  const int per_pass = 32 / (D / 8), most = a.Hq > a.H ? a.Hq : a.H;
   const int passes = (most + per_pass - 1) / per_pass;
-  long long y = (2LL * sm_count + n - 1) / n;
-  if (y > passes) y = passes;
-  if (y < 1) y = 1;
-  return launch_pdl(append_kernel<D, kBF16, kPool, kNorm>, dim3((unsigned)n, (unsigned)y),
-                    dim3(kThreads), 0, s, a);
+  int log2_shares = 0;
+  const int passes_all = (a.Hq + a.H + per_pass - 1) / per_pass;
+  while ((1 << log2_shares) < passes && (1 << log2_shares) < kMostShares) {
+    const long long warps = n << log2_shares;
+    if (warps >= 32LL * sm_count) break;
+    if (warps >= 6LL * sm_count && (passes_all >> log2_shares) <= kPasses) break;
+    ++log2_shares;
+  }
+  constexpr int kWarps = kThreads / 32;
+  return launch_pdl(append_kernel<D, kBF16, kPool, kNorm>,
+                    dim3((unsigned)(((n << log2_shares) + kWarps - 1) / kWarps)), dim3(kThreads), 0, s,
+                    a, log2_shares, n);
 }
 
 template <int D, bool kBF16>
