@@ -13,11 +13,10 @@
 //
 // Bound: bytes.  A token of 32 query and 8 KV heads of 128 moves 24.6 KB
 // between q, k, v, the pools and the rotated queries, and computes 3 operations
-// an element.  8,192 of them (204 MB, half read, half written), with norms: 50
-// us, 4.1 TB/s; with the arithmetic left out 41.5 us, the rate of mixed reads
-// and writes here (a plain device copy of 100 MB takes 65 us).  Into an E4M3
-// pool, 1,939 tokens of 32 and 32 heads (80 MB): 19.6 us.  A step of 256 tokens
-// takes 4.3 us, one of four 2.1.
+// an element.  8,192 of them (204 MB, half read, half written), with norms: 37.3
+// us, 5.5 TB/s (a copy kernel of that size takes 34).  Into an E4M3 pool, 1,939
+// tokens of 32 and 32 heads (80 MB): 16.8 us.  A step of 256 tokens takes 4.1 us,
+// one of four 2.1.
 //
 // A row (one head of one token) is held by D / 8 lanes of 16 bytes each, so
 // loads and stores are whole 16-byte vectors and the rotation's partner element
@@ -58,7 +57,7 @@ struct AppendArgs {
   int32_t* err;
 };
 
-constexpr int kThreads = 128;   // of a block of every kernel here (256 in the append: 76 us for 50)
+constexpr int kThreads = 128;   // of a block of every kernel here (64 measured no better)
 
 // The slot of token `tok`, or -1 for a token that writes nothing: a padding
 // token (sequence -1, or a negative given slot), or a bad one, which sets an
@@ -304,23 +303,24 @@ __device__ __forceinline__ void store_row(uint8_t* pool, const uint4& x, long lo
   }
 }
 
-// Rows a thread group loads before it works on the first (8: 58 us for 50 in the
-// append of 8,192 tokens; 2 measured no better).
+// Rows a thread group loads before it works on the first, and blocks of the
+// append an SM (72 registers, a few of them spilled): 37.2 us for the append of
+// 8,192 tokens; 3, 5 and 6 rows take 38.5, 38.8 and 43.8, five, six and eight
+// blocks 40.6, 42.0 and 40.3.
 constexpr int kBatch = 4;
-constexpr int kMostShares = 16;
-constexpr int kPasses = 10;
 constexpr int kBlocks = 7;
 
-// One block per token (blockIdx.x) and share of its rows (blockIdx.y): query
-// rows, then key rows, then value rows, each D / 8 lanes wide.  The angles are
-// loaded once per thread and used for all of the token's rows; a norm's weights
-// are multiplied into them, so that a normed row costs one multiplication more
-// than a plain one.  The first rows of each kind are loaded before the token's
-// slot is known.  Six blocks an SM: enough rows in flight without the spills of
-// eight (50 us; five 52, eight 88 with 8,192 tokens).
+// One warp per token and share of its rows: query rows, then key rows with their
+// value rows, each D / 8 lanes wide.  The angles are loaded once per lane and
+// used for all of the share's rows; a norm's weights are multiplied into them, so
+// that a normed row costs one multiplication more than a plain one.  The first
+// rows of each kind are loaded before the token's slot is known.  A warp, not a
+// block, per token: slot, angles and weights cost a warp some 400 instructions
+// and three dependent loads, once for 24 passes of rows instead of four times
+// (50 us with a block per token, 42 with a warp at the same six blocks an SM).
 template <int D, bool kBF16, int kPool, bool kNorm>
-__global__ void __launch_bounds__(kThreads, kBlocks) append_kernel(const AppendArgs a, int log2_shares,
-                                                             long long n) {
+__global__ void __launch_bounds__(kThreads, kBlocks)
+    append_kernel(const AppendArgs a, int log2_shares, long long n) {
   constexpr int LPR = D / 8;               // lanes per row
   constexpr int RPP = 32 / LPR;            // rows per pass of a warp
   grid_dep_wait();
@@ -530,14 +530,18 @@ int tokens_per_block(int D, int rows, long long n, int sm_count) {
 
 template <int D, bool kBF16, int kPool, bool kNorm>
 cudaError_t launch_append_n(const AppendArgs& a, long long n, int sm_count, cudaStream_t s) {
+  // shares of a token's rows, a power of two: until six warps an SM (4.0 us for
+  // 256 tokens, 4.4 with twice as many shares), and on to 32 warps an SM as long
+  // as a warp has more than 20 passes of rows (16.8 us for the 1,939 tokens above
+  // with two shares, 17.5 with four).  Up to 16: 4.6 us for 32 tokens of 64 and 8
+  // heads into a 4-bit pool and back, 4.8 with 8, 5.5 with 4.
   const int per_pass = 32 / (D / 8), most = a.Hq > a.H ? a.Hq : a.H;
-  const int passes = (most + per_pass - 1) / per_pass;
+  const int passes = (a.Hq + a.H + per_pass - 1) / per_pass;
   int log2_shares = 0;
-  const int passes_all = (a.Hq + a.H + per_pass - 1) / per_pass;
-  while ((1 << log2_shares) < passes && (1 << log2_shares) < kMostShares) {
+  while (log2_shares < 4 && (per_pass << log2_shares) < most) {
     const long long warps = n << log2_shares;
     if (warps >= 32LL * sm_count) break;
-    if (warps >= 6LL * sm_count && (passes_all >> log2_shares) <= kPasses) break;
+    if (warps >= 6LL * sm_count && (passes >> log2_shares) <= 20) break;
     ++log2_shares;
   }
   constexpr int kWarps = kThreads / 32;
