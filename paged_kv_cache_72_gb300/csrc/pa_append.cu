@@ -403,8 +403,8 @@ struct Items {
   }
 };
 
-// The 4-bit write of rows that are rotated already, bound by bytes (2 read and
-// 0.5625 written for an element): H key rows, then H value
+// The 4-bit write of rows that are rotated already, for tokens of few rows; bound
+// by bytes (2 read and 0.5625 written for an element): H key rows, then H value
 // rows of each of a block's per_block tokens.  kBatch rows a thread are in
 // flight: their data and slots are loaded before the first is quantized.
 template <int D, bool kBF16>
@@ -519,8 +519,7 @@ __global__ void __launch_bounds__(kThreads) read_fp4_kernel(const ReadArgs a, in
 
 // Tokens a block takes when a token has `rows` rows of D: as many as fill
 // kBatch rows a thread, as long as two blocks an SM remain (write and read-back
-// of 8,192 tokens of 8 heads of 128: 16.7 us, 18.9 with one token a block; of
-// 1,800 of 2 heads of 64: 4.9 and 6.4).
+// of 1,800 tokens of 2 heads of 64: 4.9 us, 6.4 with one token a block).
 int tokens_per_block(int D, int rows, long long n, int sm_count) {
   long long t = (long long)kBatch * (kThreads / (D / 8)) / rows;
   const long long most = n / (2LL * sm_count);
@@ -619,6 +618,12 @@ int write_fp4(const void* k, const void* v, int32_t src_dtype, AppendArgs a, int
   a.v_scale = v_scale;
   a.err = err_word;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // tokens of eight passes of a warp's rows or more: the append without queries
+  // (write and read-back of 8,192 tokens of 8 heads of 128: 14.9 us, 16.7 with
+  // the kernel below); of fewer, several tokens to a block (8,192 tokens of 2
+  // heads of 64: 3.8 us, 7.3 with a warp or more a token)
+  if (2 * num_kv_heads * (head_dim / 8) >= 8 * 32)
+    return launch_append(a, head_dim, src_dtype == PA_BF16, kPoolE2M1, num_tokens, s, what);
   DeviceInfo di;
   if (int rc = current_device_info(&di)) return rc;
   const int per = tokens_per_block(head_dim, 2 * num_kv_heads, num_tokens, di.sm_count);
