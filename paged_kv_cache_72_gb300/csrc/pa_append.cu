@@ -462,12 +462,13 @@ struct ReadArgs {
 };
 
 // Rows at given slots of 4-bit pools as 16-bit values, code * scale16 (exact in
-// fp32) * tensor scale, rounded to fp32 and then to 16 bits.  A block takes
-// per_block tokens, D / 8 lanes a row as in the write, kBatch rows a thread:
-// their slots, then their codes, then their values.
+// binary16) * tensor scale, rounded to fp32 and then to 16 bits.  Bound by bytes
+// and close behind them by issue slots, so a lane takes 16 values of a row, 8 in
+// each half (whole sectors a store): D / 16 lanes a row.  A block takes per_block
+// tokens, kBatch rows a thread: their slots, then their codes, then their values.
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(kThreads) read_fp4_kernel(const ReadArgs a, int per_block) {
-  constexpr int LPR = D / 8, RPP = kThreads / LPR;
+  constexpr int LPR = D / 16, RPP = kThreads / LPR;
   grid_dep_wait();
   grid_dep_launch();
   const int B = 1 << a.log2B, rows = 2 * a.H, j = threadIdx.x % LPR;
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kThreads) read_fp4_kernel(const ReadArgs a, in
   const int tokens = (int)min((long long)per_block, a.n - tok0), count = tokens * rows;
   Items it(threadIdx.x / LPR, RPP, rows);
   for (int i0 = 0; i0 < count; i0 += kBatch * RPP) {
-    uint32_t code[kBatch], s8[kBatch];
+    uint32_t code[kBatch][2], s8[kBatch][2];
     uint16_t* dst[kBatch];
     bool v[kBatch];
 #pragma unroll
@@ -484,7 +485,6 @@ __global__ void __launch_bounds__(kThreads) read_fp4_kernel(const ReadArgs a, in
       v[b] = it.r >= a.H;
       const int h = v[b] ? it.r - a.H : it.r;
       dst[b] = nullptr;
-      code[b] = s8[b] = 0u;
       if (it.t < tokens) {
         const long long slot = __ldg(a.slots + tok);
         if (slot >= (a.num_blocks << a.log2B)) {
@@ -493,8 +493,12 @@ __global__ void __launch_bounds__(kThreads) read_fp4_kernel(const ReadArgs a, in
           const uint8_t* plane = (v[b] ? a.vc : a.kc) +
                                  fp4_plane(slot >> a.log2B, a.H, h, B * fp4_row_bytes(D));
           const int row = (int)(slot & (B - 1));
-          code[b] = __ldg(reinterpret_cast<const uint32_t*>(plane + row * (D / 2) + 4 * j));
-          s8[b] = __ldg(plane + fp4_scale_off<D>(B, row, j >> 1));
+          const uint8_t* codes = plane + row * (D / 2) + 4 * j;
+          const uint8_t* scales = plane + fp4_scale_off<D>(B, row, j >> 1);
+          code[b][0] = __ldg(reinterpret_cast<const uint32_t*>(codes));
+          code[b][1] = __ldg(reinterpret_cast<const uint32_t*>(codes + D / 4));
+          s8[b][0] = __ldg(scales);
+          s8[b][1] = __ldg(scales + 4 * (D / 32));
           dst[b] = (v[b] ? a.v_out : a.k_out) + ((size_t)tok * a.H + h) * D + 8 * j;
         }
       }
@@ -503,25 +507,29 @@ __global__ void __launch_bounds__(kThreads) read_fp4_kernel(const ReadArgs a, in
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
       if (!dst[b]) continue;
-      const float s16 = unpack2<false>(e4m3x2_to_f16x2(s8[b])).x;
       const float scale = v[b] ? a.v_scale : a.k_scale;
-      uint32_t f[4], o[4];
-      e2m1x8_to_f16x2(code[b], f);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 g = unpack2<false>(f[k]);
-        o[k] = pack2<kBF16>(g.x * s16 * scale, g.y * s16 * scale);
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t s16 = e4m3x2_to_f16x2(s8[b][half]);
+        uint32_t f[4], o[4];
+        e2m1x8_to_f16x2(code[b][half], f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 g = unpack2<false>(hmul2_lo(f[k], s16));
+          const F2 y = mul2({g.x, g.y}, {scale, scale});
+          o[k] = pack2<kBF16>(y.x, y.y);
+        }
+        *reinterpret_cast<uint4*>(dst[b] + half * (D / 2)) = make_uint4(o[0], o[1], o[2], o[3]);
       }
-      *reinterpret_cast<uint4*>(dst[b]) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
 
-// Tokens a block takes when a token has `rows` rows of D: as many as fill
+// Tokens a block takes when a token has `rows` rows of `lanes`: as many as fill
 // kBatch rows a thread, as long as two blocks an SM remain (write and read-back
 // of 1,800 tokens of 2 heads of 64: 4.9 us, 6.4 with one token a block).
-int tokens_per_block(int D, int rows, long long n, int sm_count) {
-  long long t = (long long)kBatch * (kThreads / (D / 8)) / rows;
+int tokens_per_block(int lanes, int rows, long long n, int sm_count) {
+  long long t = (long long)kBatch * (kThreads / lanes) / rows;
   const long long most = n / (2LL * sm_count);
   if (t > most) t = most;
   return t < 1 ? 1 : (int)t;
@@ -626,7 +634,7 @@ int write_fp4(const void* k, const void* v, int32_t src_dtype, AppendArgs a, int
     return launch_append(a, head_dim, src_dtype == PA_BF16, kPoolE2M1, num_tokens, s, what);
   DeviceInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  const int per = tokens_per_block(head_dim, 2 * num_kv_heads, num_tokens, di.sm_count);
+  const int per = tokens_per_block(head_dim / 8, 2 * num_kv_heads, num_tokens, di.sm_count);
   const long long n = num_tokens;
   const dim3 grid((unsigned)((n + per - 1) / per)), block(kThreads);
   const bool bf16 = src_dtype == PA_BF16;
@@ -778,7 +786,7 @@ int pa_cache_read_fp4(const int64_t* slot_mapping, int64_t num_tokens, const voi
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   DeviceInfo di;
   if (int rc = current_device_info(&di)) return rc;
-  const int per = tokens_per_block(head_dim, 2 * num_kv_heads, num_tokens, di.sm_count);
+  const int per = tokens_per_block(head_dim / 16, 2 * num_kv_heads, num_tokens, di.sm_count);
   const dim3 grid((unsigned)((num_tokens + per - 1) / per)), block(kThreads);
   const bool bf16 = out_dtype == PA_BF16;
   clear_stale_error();
