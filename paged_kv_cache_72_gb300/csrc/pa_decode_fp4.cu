@@ -69,7 +69,8 @@ namespace {
 
 // Twelve warps leave a thread 168 registers, which o, the queries and a tile's
 // work need; 16 warps of 128 spill and measured the same on long contexts and 3
-// to 10% more on short ones.  Two head tiles a KV head take 8 warps of 255.
+// to 10% more on short ones (head_dim 64, without spills: 8% more).  Two head
+// tiles a KV head take 8 warps of 255 (12: 2% less to 15% more).
 __host__ __device__ constexpr int warps_of(int NH) { return NH == 1 ? 12 : 8; }
 constexpr int kTile = 32;                 // tokens per tile
 constexpr int kStages = 2;                // tiles in shared memory per warp (3 measured the same)
