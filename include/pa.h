@@ -520,11 +520,10 @@ int pa_cache_read_fp4(const int64_t* slot_mapping, int64_t num_tokens, const voi
  *                 PA_DECODE_TABLES_READY
  * The tensor scales are applied outside the products (k_scale joins `scale`,
  * v_scale multiplies the output); code * s16 and the queries (a bfloat16 row
- * after a power-of-two scaling) are binary16, every sum is fp32.  For binary16
- * outputs the softmax weights are a pair of binary16 values, for bfloat16
- * outputs one.  Tokens of a block whose table entry is out of range
- * (PA_DEVERR_BLOCK_ID) are left out of the softmax.  Every other argument,
- * the errors and the workspace rules are those of pa_decode.
+ * after a power-of-two scaling) are binary16, the softmax weights a pair of
+ * binary16 values (2^-21), every sum is fp32.  Tokens of a block whose table
+ * entry is out of range (PA_DEVERR_BLOCK_ID) are left out of the softmax.  Every
+ * other argument, the errors and the workspace rules are those of pa_decode.
  */
 int pa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
                   const int32_t* block_tables, int32_t table_stride, const int32_t* seq_lens,

@@ -11,10 +11,10 @@
 // read once and nothing else is, but a tile of 32 tokens also costs a warp 610
 // instructions, 34 of them MMAs, 128 conversions and 128 multiplies by scales
 // (head_dim 128, up to 8 heads a KV head).  32 contexts of 16 to 32 K tokens,
-// 64 heads over 8 of 128 (883 MB): 162 us, 5.46 TB/s, 80% of a copy's rate;
-// copies without arithmetic take 144 us.  256 contexts of 17 to 4,096 tokens, 32
-// over 8 heads (125 MB): 34.0 us, of which 21 are tiles, 7 the start up to the
-// first tile and 6 the joining of split contexts.  So:
+// 64 heads over 8 of 128 (883 MB): 181 us, 4.87 TB/s, 72% of a copy's rate (32
+// heads over 8: 167); copies without arithmetic take 144 us.  256 contexts of 17
+// to 4,096 tokens, 32 over 8 heads (125 MB): 35.4 us, of which 22 are tiles, 7 the
+// start up to the first tile and 6 the joining of split contexts.  So:
 //  * One warp is one pipeline.  A warp owns a (sequence, KV head) context or a
 //    contiguous range of one.  Its tiles arrive in a ring of kStages tiles of
 //    its own that it fills itself with 16-byte asynchronous copies, nine a lane
@@ -54,9 +54,8 @@
 // waits for another.  Batches of short contexts take one warp each instead
 // (kWhole).
 //
-// Roundings below fp32: the weights to binary16 (a pair of them for binary16
-// outputs), a bfloat16 query's elements under 2^-14 of its row's largest, and
-// the output.
+// Roundings below fp32: the weights to a pair of binary16 values (2^-21), a
+// bfloat16 query's elements under 2^-14 of its row's largest, and the output.
 #include <cmath>
 #include <mutex>
 
@@ -189,18 +188,22 @@ struct Walk {
   }
 };
 
-// One warp's state over a range of one context's tiles.  kTwin (binary16
-// outputs, at most 4 query heads): the 8 head columns hold the heads twice, the
-// first copy's weights rounded to binary16, the second's what that rounding
-// left, so that the pair costs no second product; the two are added at the end
-// (44.2 us with the second product, 41.7 without, for the 256 contexts above).
+// One warp's state over a range of one context's tiles.  The weights enter the
+// products as a pair of binary16 values, their rounding and what it left: one
+// value (2^-11) shows in outputs of either type (bfloat16 ones 8.5e-4 off a 32-bit
+// computation's in norm, with the pair 3e-5 to 1.2e-4).  kTwin (at most 4 query
+// heads): the 8 head columns hold the heads twice, the first copy's weights
+// rounded, the second's the rest, so that the pair costs no second product; the
+// two are added at the end.  With bfloat16 outputs and 32 contexts of 16 to 32 K
+// tokens, 8 KV heads of 128, the pair takes 166.6 us for the 159.7 of one value
+// with 4 query heads each, 181 for 160 with 8.
 template <int D, bool kBF16, int NH, bool kTwin>
 struct Context {
   static constexpr int KS = D / 16;        // k-steps of S^T
   static constexpr int MT = D / 16;        // m-tiles of O^T
   static constexpr int KW = D / 32;        // words of K codes per lane and row
   static constexpr int VW = D / 64;        // words of V codes per lane and row
-  static constexpr bool kPair = !kBF16 && !kTwin;   // weights as a pair, two products
+  static constexpr bool kPair = !kTwin;    // the pair takes two products
   uint32_t qb[NH][KS][2];
   float sl[NH][2];                         // score factor of heads 8 nh + 2 tig + e (log2)
   float o[NH][MT][4];
@@ -303,7 +306,7 @@ struct Context {
   }
 
   // Weights of the tile's scores, exp2(s - base) as B fragments pb (pl: what
-  // their rounding to binary16 left, for binary16 outputs), and their sums.
+  // their rounding to binary16 left), and their sums.
   // The base is the largest score less kShift when it is set and stays until a
   // weight would pass exp2(kShift + kLag), so most tiles need neither the
   // maximum over lanes nor a rescale of o: one vote says so.
@@ -380,9 +383,9 @@ struct Context {
           const float p0 = ex2_approx(s[hf][nh][2 * r]), p1 = ex2_approx(s[hf][nh][2 * r + 1]);
           uint32_t pk = pack2<false>(p0, p1);
           if constexpr (kTwin) {
-            const float2 f = unpack2<false>(pk);
-            const bool rest = (threadIdx.x & 2) != 0;   // the heads' second copy
-            pk = pack2<false>(p0 - (rest ? f.x : 0.f), p1 - (rest ? f.y : 0.f));
+            // the heads' second copy is left with the rest
+            const float2 f = unpack2<false>((threadIdx.x & 2) != 0 ? pk : 0u);
+            pk = pack2<false>(p0 - f.x, p1 - f.y);
           }
           if constexpr (kPair) {
             const float2 f = unpack2<false>(pk);
@@ -997,10 +1000,9 @@ typedef void (*Kernel)(const Args);
 
 template <int D>
 Kernel pick_d(bool bf16, int G) {
-  if (bf16)
-    return G > 8 ? decode_fp4_kernel<D, true, 2, false> : decode_fp4_kernel<D, true, 1, false>;
-  if (G > 8) return decode_fp4_kernel<D, false, 2, false>;
-  return G > 4 ? decode_fp4_kernel<D, false, 1, false> : decode_fp4_kernel<D, false, 1, true>;
+  if (G > 8) return bf16 ? decode_fp4_kernel<D, true, 2, false> : decode_fp4_kernel<D, false, 2, false>;
+  if (G > 4) return bf16 ? decode_fp4_kernel<D, true, 1, false> : decode_fp4_kernel<D, false, 1, false>;
+  return bf16 ? decode_fp4_kernel<D, true, 1, true> : decode_fp4_kernel<D, false, 1, true>;
 }
 
 // the ring of every warp (which its last part's record shares) and a slot each
