@@ -112,15 +112,16 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return r;
 }
-// x / d rounded to nearest, from r = 1 / d rounded to nearest: one residual
-// step on x r gives the correctly rounded quotient (P. Markstein, "Computation
+// -x / d rounded to nearest, from r = 1 / d rounded to nearest: one residual
+// step on -x r gives the correctly rounded quotient (P. Markstein, "Computation
 // of elementary functions on the IBM RISC System/6000 processor", 1990) where
 // nothing under- or overflows: d within 2^+-100 and |x| at most 2^27 d
 // (plain_quotient); an x so small that its residual is lost is far below the
-// smallest code.
-__device__ __forceinline__ F2 div_by(F2 x, float d, float r) {
-  const F2 y = mul2(x, {r, r});
-  return fma2(fma2(y, {-d, -d}, x), {r, r}, y);
+// smallest code.  The negative quotient, because a residual of zero is +0: added
+// to x r it would turn a quotient of -0 into +0; here it is multiplied by -r.
+__device__ __forceinline__ F2 minus_div_by(F2 x, float d, float r) {
+  const F2 y = mul2(x, {-r, -r});
+  return fma2(fma2(y, {d, d}, x), {-r, -r}, y);
 }
 __device__ __forceinline__ bool plain_quotient(float largest, float d) {
   return d > 0x1p-100f && d < 0x1p100f && largest <= 0x1p27f * d;
@@ -128,15 +129,15 @@ __device__ __forceinline__ bool plain_quotient(float largest, float d) {
 // x / d for the others, off the common path (0 for d = 0)
 __device__ __noinline__ float div_any(float x, float d) { return d > 0.f ? __fdiv_rn(x, d) : 0.f; }
 
-// z / d, four pairs of magnitudes up to `largest`; r is 1 / d rounded to nearest
-__device__ __forceinline__ void quotients(const F2 (&z)[4], float largest, float d, float r,
-                                          F2 (&y)[4]) {
+// -z / d, four pairs of magnitudes up to `largest`; r is 1 / d rounded to nearest
+__device__ __forceinline__ void minus_quotients(const F2 (&z)[4], float largest, float d, float r,
+                                                F2 (&y)[4]) {
   if (plain_quotient(largest, d)) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = div_by(z[i], d, r);
+    for (int i = 0; i < 4; ++i) y[i] = minus_div_by(z[i], d, r);
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = {div_any(z[i].x, d), div_any(z[i].y, d)};
+    for (int i = 0; i < 4; ++i) y[i] = {-div_any(z[i].x, d), -div_any(z[i].y, d)};
   }
 }
 
@@ -275,25 +276,26 @@ __device__ __forceinline__ void store_row(uint8_t* pool, const uint4& x, long lo
   float m = fmaxf(fabsf(z[0].x), fabsf(z[0].y));
 #pragma unroll
   for (int i = 1; i < 4; ++i) m = max3f(m, fabsf(z[i].x), fabsf(z[i].y));
-  // the scale's own reciprocals are the call's: the compiler hoists them
+  // the scale's own reciprocals are the call's: the compiler hoists them; the
+  // codes of the negative quotients get their sign bits flipped
   if constexpr (kPool == kPoolE4M3) {
-    quotients(z, m, scale, __frcp_rn(scale), y);
+    minus_quotients(z, m, scale, __frcp_rn(scale), y);
     uint32_t e[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) e[i] = f32x2_to_e4m3x2(y[i].x, y[i].y);
     if (in)
       *reinterpret_cast<uint2*>(pool + ((size_t)slot * H + h) * D + d0) =
-          make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+          make_uint2((e[0] | (e[1] << 16)) ^ 0x80808080u, (e[2] | (e[3] << 16)) ^ 0x80808080u);
   } else if constexpr (kPool == kPoolE2M1) {
     m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
     const float six = __fmul_rn(6.f, scale);
     const float s16 =
-        plain_quotient(m, six) ? div_by({m, m}, six, __frcp_rn(six)).x : div_any(m, six);
+        plain_quotient(m, six) ? -minus_div_by({m, m}, six, __frcp_rn(six)).x : div_any(m, six);
     const uint32_t s8 = f32x2_to_e4m3x2(s16, 0.f) & 0xffu;
     const float d = __fmul_rn(unpack2<false>(e4m3x2_to_f16x2(s8)).x, scale);
-    quotients(z, m, d, __frcp_rn(d), y);
-    const uint32_t code = f32x8_to_e2m1x8(y[0].x, y[0].y, y[1].x, y[1].y, y[2].x, y[2].y, y[3].x,
-                                          y[3].y);
+    minus_quotients(z, m, d, __frcp_rn(d), y);
+    const uint32_t code = 0x88888888u ^ f32x8_to_e2m1x8(y[0].x, y[0].y, y[1].x, y[1].y, y[2].x,
+                                                        y[2].y, y[3].x, y[3].y);
     if (in) {
       const int B = 1 << log2B, row = (int)(slot & (B - 1));
       uint8_t* plane = pool + fp4_plane(slot >> log2B, H, h, B * fp4_row_bytes(D));
