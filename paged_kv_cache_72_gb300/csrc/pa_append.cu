@@ -588,7 +588,10 @@ int launch_append(const AppendArgs& a, int D, bool bf16, int pool, long long n, 
   return launch_status(e, what);
 }
 
-bool scale_ok(float s) { return s > 0.f && std::isfinite(s) && std::isfinite(6.f * s); }
+// a tensor scale; a 4-bit group's scale is a quotient by 6 s
+bool scale_ok(float s, bool four_bit) {
+  return s > 0.f && std::isfinite(s) && (!four_bit || std::isfinite(6.f * s));
+}
 
 int append_shape(int32_t block_size, int32_t num_kv_heads, int32_t head_dim, int32_t src_dtype,
                  int32_t cache_dtype) {
@@ -609,7 +612,7 @@ int write_fp4(const void* k, const void* v, int32_t src_dtype, AppendArgs a, int
               int32_t* err_word, pa_stream stream, const char* what) {
   if (num_tokens < 0 || num_blocks < 0) return PA_ERR_INVALID_ARG;
   if (int rc = append_shape(block_size, num_kv_heads, head_dim, src_dtype, PA_FP4_E2M1)) return rc;
-  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return PA_ERR_INVALID_ARG;
+  if (!scale_ok(k_scale, true) || !scale_ok(v_scale, true)) return PA_ERR_INVALID_ARG;
   if (num_tokens == 0) return PA_OK;
   if (num_tokens > 0x7fffffffLL) return PA_ERR_INVALID_ARG;
   if (!k || !v || !k_cache || !v_cache) return PA_ERR_INVALID_ARG;
@@ -675,7 +678,8 @@ int pa_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_str
   if (num_q_heads > 65536 || rotary_dim > head_dim || rotary_dim % 16 != 0)
     return PA_ERR_UNSUPPORTED;
   if ((q_norm || k_norm) && !(eps >= 0.f && std::isfinite(eps))) return PA_ERR_INVALID_ARG;
-  if (cache_dtype != src_dtype && (!scale_ok(k_scale) || !scale_ok(v_scale)))
+  const bool four = cache_dtype == PA_FP4_E2M1;
+  if (cache_dtype != src_dtype && (!scale_ok(k_scale, four) || !scale_ok(v_scale, four)))
     return PA_ERR_INVALID_ARG;
   if (num_tokens == 0) return PA_OK;
   if (num_tokens > 0x7fffffffLL) return PA_ERR_INVALID_ARG;
@@ -721,8 +725,7 @@ int pa_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_str
   a.v_scale = v_scale;
   a.slots = slot_mapping;
   a.err = err_word;
-  const int pool = cache_dtype == PA_FP4_E2M1 ? kPoolE2M1
-                                              : (cache_dtype == PA_FP8_E4M3 ? kPoolE4M3 : kPool16);
+  const int pool = four ? kPoolE2M1 : (cache_dtype == PA_FP8_E4M3 ? kPoolE4M3 : kPool16);
   return launch_append(a, head_dim, src_dtype == PA_BF16, pool, num_tokens,
                        static_cast<cudaStream_t>(stream), "append launch");
 }
@@ -766,7 +769,7 @@ int pa_cache_read_fp4(const int64_t* slot_mapping, int64_t num_tokens, const voi
                       pa_stream stream) {
   if (num_tokens < 0 || num_blocks < 0) return PA_ERR_INVALID_ARG;
   if (int rc = append_shape(block_size, num_kv_heads, head_dim, out_dtype, PA_FP4_E2M1)) return rc;
-  if (!scale_ok(k_scale) || !scale_ok(v_scale)) return PA_ERR_INVALID_ARG;
+  if (!scale_ok(k_scale, true) || !scale_ok(v_scale, true)) return PA_ERR_INVALID_ARG;
   if (num_tokens == 0) return PA_OK;
   if (num_tokens > 0x7fffffffLL) return PA_ERR_INVALID_ARG;
   if (!slot_mapping || !k_cache || !v_cache || !k_out || !v_out) return PA_ERR_INVALID_ARG;
