@@ -407,8 +407,10 @@ struct Items {
 
 // The 4-bit write of rows that are rotated already, for tokens of few rows; bound
 // by bytes (2 read and 0.5625 written for an element): H key rows, then H value
-// rows of each of a block's per_block tokens.  kBatch rows a thread are in
-// flight: their data and slots are loaded before the first is quantized.
+// rows of each of a block's per_block tokens.  All rows of a thread are in flight,
+// at most kBatch of them (a token of few rows has no more, and tokens_per_block
+// gives a block no more): their data and slots are loaded before the first is
+// quantized.
 template <int D, bool kBF16>
 __global__ void __launch_bounds__(kThreads) write_fp4_kernel(const AppendArgs a, int per_block,
                                                              long long n) {
@@ -419,35 +421,33 @@ __global__ void __launch_bounds__(kThreads) write_fp4_kernel(const AppendArgs a,
   const long long tok0 = (long long)blockIdx.x * per_block;
   const int tokens = (int)min((long long)per_block, n - tok0), count = tokens * rows;
   Items it(threadIdx.x / LPR, RPP, rows);
-  for (int i0 = 0; i0 < count; i0 += kBatch * RPP) {
-    uint4 x[kBatch];
-    long long slot[kBatch];
-    int h[kBatch];
-    bool v[kBatch];
+  uint4 x[kBatch];
+  long long slot[kBatch];
+  int h[kBatch];
+  bool v[kBatch];
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const bool in = it.t < tokens;
-      const long long tok = tok0 + it.t;
-      v[b] = it.r >= a.H;
-      h[b] = v[b] ? it.r - a.H : it.r;
-      x[b] = make_uint4(0u, 0u, 0u, 0u);
-      slot[b] = -1;
-      if (in) {
-        x[b] = *reinterpret_cast<const uint4*>((v[b] ? a.v : a.k) + tok * a.k_stride + h[b] * D +
-                                               8 * j);
-        const bool lead = j == 0 && it.r == 0;   // one thread a token
-        int pos;
-        slot[b] = append_slot(a, tok, lead, pos);
-        if (a.slots && lead) a.slots[tok] = slot[b];
-      }
-      it.next();
+  for (int b = 0; b < kBatch; ++b) {
+    const bool in = it.t < tokens;
+    const long long tok = tok0 + it.t;
+    v[b] = it.r >= a.H;
+    h[b] = v[b] ? it.r - a.H : it.r;
+    x[b] = make_uint4(0u, 0u, 0u, 0u);
+    slot[b] = -1;
+    if (in) {
+      x[b] = *reinterpret_cast<const uint4*>((v[b] ? a.v : a.k) + tok * a.k_stride + h[b] * D +
+                                             8 * j);
+      const bool lead = j == 0 && it.r == 0;   // one thread a token
+      int pos;
+      slot[b] = append_slot(a, tok, lead, pos);
+      if (a.slots && lead) a.slots[tok] = slot[b];
     }
+    it.next();
+  }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      if (i0 + b * RPP >= count) break;
-      store_row<D, kBF16, kPoolE2M1>(v[b] ? a.vc : a.kc, x[b], slot[b], a.H, a.log2B, h[b],
-                                     v[b] ? a.v_scale : a.k_scale, slot[b] >= 0);
-    }
+  for (int b = 0; b < kBatch; ++b) {
+    if (b * RPP >= count) break;
+    store_row<D, kBF16, kPoolE2M1>(v[b] ? a.vc : a.kc, x[b], slot[b], a.H, a.log2B, h[b],
+                                   v[b] ? a.v_scale : a.k_scale, slot[b] >= 0);
   }
 }
 
@@ -635,7 +635,9 @@ int write_fp4(const void* k, const void* v, int32_t src_dtype, AppendArgs a, int
   // (write and read-back of 8,192 tokens of 8 heads of 128: 14.9 us, 16.7 with
   // the kernel below); of fewer, several tokens to a block (8,192 tokens of 2
   // heads of 64: 3.8 us, 7.3 with a warp or more a token)
-  if (2 * num_kv_heads * (head_dim / 8) >= 8 * 32)
+  constexpr int kFewLanes = 8 * 32;
+  static_assert(kFewLanes <= kBatch * kThreads, "a token of few rows fits a block's registers");
+  if (2 * num_kv_heads * (head_dim / 8) >= kFewLanes)
     return launch_append(a, head_dim, src_dtype == PA_BF16, kPoolE2M1, num_tokens, s, what);
   DeviceInfo di;
   if (int rc = current_device_info(&di)) return rc;
