@@ -713,7 +713,8 @@ __global__ void __launch_bounds__(warps_of(NH) * 32, 1)
       w.load_seq(a);
     }
     const bool sound = w.i < a.num_seqs && rem >= 0;
-    // only if seq_lens changes during the call: never walk blind
+    // only if seq_lens changes during the call (an error of the caller's): never
+    // walk blind, here, at the next contexts or in the count of cut ones
     if (!sound) set_error(a.err, PA_DEVERR_SEQ_LEN);
     int left = 0;   // units to go, the tile's among them
     w.h = w.k = 0;
@@ -800,6 +801,7 @@ __global__ void __launch_bounds__(warps_of(NH) * 32, 1)
         ld.advance(a);
         ld_left -= kStart;
         if (ld.nt > 0) load_context();
+        else ld_left = 0;   // past the last sequence
       }
     };
     // this lane's bytes of a tile.  K: rows (gid & 1) and (gid & 1) + 2 of token
@@ -889,7 +891,12 @@ __global__ void __launch_bounds__(warps_of(NH) * 32, 1)
       left -= kStart;
       w.k = w.nt - 1;
       if (left > 0) w.advance(a);
+      if (left > 0 && w.nt == 0) {   // past the last sequence: not blind either
+        set_error(a.err, PA_DEVERR_SEQ_LEN);
+        left = 0;
+      }
     }
+    copies_wait<0>();   // none, unless the loads' walk met other lengths
   }
   __syncthreads();
 
@@ -943,9 +950,14 @@ __global__ void __launch_bounds__(warps_of(NH) * 32, 1)
     if (p.g0 < c0 || p.g0 + p.nt > c1) {   // else inside this block's range: already written
       const long long f = ((p.g0 + 1) * nb - 1) / U, e = ((p.g0 + p.nt) * nb - 1) / U;
       uint32_t* cnt = a.ws_count + e;
+      // a block's first and last context alone may be cut, and it lies among the
+      // blocks that hold them, unless seq_lens changed during the call
+      const bool cut = (tid == 0 || tid == sh.groups - 1) && f >= 0 && f <= blockIdx.x &&
+                       e >= blockIdx.x && e < nb;
+      if (!cut) set_error(a.err, PA_DEVERR_SEQ_LEN);
       // releases the block's record (ordered before by the barrier), acquires
       // those counted before it
-      if (atom_add_acq_rel_gpu(cnt, 1u) + 1u == (uint32_t)(e - f + 1)) {
+      if (cut && atom_add_acq_rel_gpu(cnt, 1u) + 1u == (uint32_t)(e - f + 1)) {
         *cnt = 0u;   // ready for the next call
         Merge& m = sh.merge[atomicAdd(&sh.merges, 1)];
         m.pair = p.pair;
