@@ -77,9 +77,10 @@ extern "C" {
 #define PA_DECODE_AUTO 0
 #define PA_DECODE_SIMT 1  /* CUDA-core kernel (group size 1 only) */
 #define PA_DECODE_MMA 2   /* tensor-core kernel (any supported group size) */
-/* OR-ed into the flags of pa_decode, pa_decode_window and pa_decode_fp8: the
- * caller promises that seq_lens and block_tables are complete before the
- * preceding kernel in the stream starts (as a serving step's metadata is).
+/* OR-ed into the flags of pa_decode, pa_decode_window, pa_decode_fp8 and
+ * pa_decode_fp4: the caller promises that seq_lens and block_tables are
+ * complete before the preceding kernel in the stream starts (as a serving
+ * step's metadata is).
  * The decode then reads them while that kernel drains, under programmatic
  * dependent launch; q, the pools, out and the workspace are still touched
  * only after it completes. */
@@ -495,8 +496,9 @@ int pa_cache_write_fp4_mapped(const void* k, const void* v, int32_t src_dtype,
 /*
  * pa_cache_read_fp4 -- the rows at given slots of a 4-bit cache as 16-bit
  * values, the inverse of pa_cache_write_fp4: code * s16 * scale, rounded to
- * out_dtype.  Rows read into a 16-bit pool's blocks serve pa_prefill, which
- * reads 16-bit pools ([P1] "How does it support prompts of arbitrary length?").
+ * out_dtype.  Output rows are consecutive: read into consecutive blocks of a
+ * 16-bit pool they serve pa_prefill, which reads 16-bit pools ([P1] "How does it
+ * support prompts of arbitrary length?"); pa_cache_write takes them to others.
  *   slot_mapping  int64 [num_tokens]; slot < 0: the output row is left as it
  *                 is; slot >= num_blocks * block_size: the same, and
  *                 PA_DEVERR_SLOT
@@ -521,9 +523,10 @@ int pa_cache_read_fp4(const int64_t* slot_mapping, int64_t num_tokens, const voi
  * The tensor scales are applied outside the products (k_scale joins `scale`,
  * v_scale multiplies the output); code * s16 and the queries (a bfloat16 row
  * after a power-of-two scaling) are binary16, the softmax weights a pair of
- * binary16 values (2^-21), every sum is fp32.  Tokens of a block whose table
- * entry is out of range (PA_DEVERR_BLOCK_ID) are left out of the softmax.  Every
- * other argument, the errors and the workspace rules are those of pa_decode.
+ * binary16 values (2^-21) of an exponential within 2^-22, every sum is fp32.
+ * Tokens of a block whose table entry is out of range (PA_DEVERR_BLOCK_ID) are
+ * left out of the softmax.  Every other argument, the errors and the workspace
+ * rules are those of pa_decode.
  */
 int pa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
                   const int32_t* block_tables, int32_t table_stride, const int32_t* seq_lens,

@@ -13,10 +13,11 @@
 //
 // Bound: bytes.  A token of 32 query and 8 KV heads of 128 moves 24.6 KB
 // between q, k, v, the pools and the rotated queries, and computes 3 operations
-// an element.  8,192 of them (204 MB, half read, half written), with norms: 37.3
+// an element.  8,192 of them (204 MB, half read, half written), with norms: 37.0
 // us, 5.5 TB/s (a copy kernel of that size takes 34).  Into an E4M3 pool, 1,939
-// tokens of 32 and 32 heads (80 MB): 16.8 us.  A step of 256 tokens takes 4.1 us,
-// one of four 2.1.
+// tokens of 32 and 32 heads (80 MB): 16.6 us.  A step of 256 tokens takes 3.9 us,
+// one of four 2.1.  A norm costs 8,192 tokens' stores into quantized pools 3 to 4
+// us (E4M3 36.9 for 34.0, 4-bit 40.5 for 36.6).
 //
 // A row (one head of one token) is held by D / 8 lanes of 16 bytes each, so
 // loads and stores are whole 16-byte vectors and the rotation's partner element
@@ -465,7 +466,8 @@ struct ReadArgs {
 
 // Rows at given slots of 4-bit pools as 16-bit values, code * scale16 (exact in
 // binary16) * tensor scale, rounded to fp32 and then to 16 bits.  Bound by bytes
-// and close behind them by issue slots, so a lane takes 16 values of a row, 8 in
+// and close behind them by issue slots (8,192 tokens of 8 heads of 128 out of memory,
+// 43 MB: 9.9 us; 32,768: 30.2 us, 5.7 TB/s), so a lane takes 16 values of a row, 8 in
 // each half (whole sectors a store): D / 16 lanes a row.  A block takes per_block
 // tokens, kBatch rows a thread: their slots, then their codes, then their values.
 template <int D, bool kBF16>
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kThreads) read_fp4_kernel(const ReadArgs a, in
 
 // Tokens a block takes when a token has `rows` rows of `lanes`: as many as fill
 // kBatch rows a thread, as long as two blocks an SM remain (write and read-back
-// of 1,800 tokens of 2 heads of 64: 4.9 us, 6.4 with one token a block).
+// of 1,800 tokens of 2 heads of 64: 4.6 us, 6.4 with one token a block).
 int tokens_per_block(int lanes, int rows, long long n, int sm_count) {
   long long t = (long long)kBatch * (kThreads / lanes) / rows;
   const long long most = n / (2LL * sm_count);
@@ -539,11 +541,15 @@ int tokens_per_block(int lanes, int rows, long long n, int sm_count) {
 
 template <int D, bool kBF16, int kPool, bool kNorm>
 cudaError_t launch_append_n(const AppendArgs& a, long long n, int sm_count, cudaStream_t s) {
-  // shares of a token's rows, a power of two: until six warps an SM (4.0 us for
-  // 256 tokens, 4.4 with twice as many shares), and on to 32 warps an SM as long
-  // as a warp has more than 20 passes of rows (16.8 us for the 1,939 tokens above
-  // with two shares, 17.5 with four).  Up to 16: 4.6 us for 32 tokens of 64 and 8
-  // heads into a 4-bit pool and back, 4.8 with 8, 5.5 with 4.
+  // shares of a token's rows, a power of two: until six warps an SM, and on to 32
+  // warps an SM as long as a warp has more than 20 passes of rows (the 1,939 tokens
+  // above: 16.8 us with two shares, 17.5 with four).  Up to 16: 4.6 us for 32
+  // tokens of 64 and 8 heads into a 4-bit pool and back, 4.8 with 8, 5.5 with 4.
+  // 32 and 8 heads of 128, norms, us with the rule's shares and with twice as many:
+  // 256 tokens 4.0 (four) 4.0, 512 7.3 (two) 5.9, 1,024 12.2 (one) 9.3, 2,048 14.5
+  // (one) 12.3, 4,096 20.2 (one) 21.8; 64 and 8 heads: 256 tokens 5.8 (four) 5.0,
+  // 1,024 13.0 (two) 10.9, 2,048 17.6 (two) 19.3.  Between 512 and 2,048 tokens it
+  // splits too little; a rule by passes and warps together is not built yet.
   const int per_pass = 32 / (D / 8), most = a.Hq > a.H ? a.Hq : a.H;
   const int passes = (a.Hq + a.H + per_pass - 1) / per_pass;
   int log2_shares = 0;
@@ -632,9 +638,12 @@ int write_fp4(const void* k, const void* v, int32_t src_dtype, AppendArgs a, int
   a.err = err_word;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   // tokens of eight passes of a warp's rows or more: the append without queries
-  // (write and read-back of 8,192 tokens of 8 heads of 128: 14.9 us, 16.7 with
-  // the kernel below); of fewer, several tokens to a block (8,192 tokens of 2
-  // heads of 64: 3.8 us, 7.3 with a warp or more a token)
+  // (4,096 tokens of 8 heads of 128: 8.9 us, 11.4 with the kernel below; 256
+  // tokens 2.4 for 2.8, but 1,024 4.8 for 4.4); of fewer, several tokens to a block
+  // (8,192 tokens of 2 heads of 64: 4.6 us, 7.8 with a warp or more a token; 256
+  // tokens 2.0 for 3.0).  With two to seven passes a token, this is right up to
+  // some 1,000 tokens (4 heads of 128, 256 tokens: 2.1 us for 2.2), the append
+  // would be from there on (1,024: 3.1 for 3.7, 8,192: 10.0 for 11.5).
   constexpr int kFewLanes = 8 * 32;
   static_assert(kFewLanes <= kBatch * kThreads, "a token of few rows fits a block's registers");
   if (2 * num_kv_heads * (head_dim / 8) >= kFewLanes)

@@ -8,13 +8,14 @@
 // exact in binary16, and every product is an f16 x f16 MMA with fp32 sums.
 //
 // Bound: bytes, and close behind them issue slots.  0.5625 bytes an element are
-// read once and nothing else is, but a tile of 32 tokens also costs a warp 610
+// read once and nothing else is, but a tile of 32 tokens also costs a warp 625
 // instructions, 34 of them MMAs, 128 conversions and 128 multiplies by scales
-// (head_dim 128, up to 8 heads a KV head).  32 contexts of 16 to 32 K tokens,
-// 64 heads over 8 of 128 (883 MB): 181 us, 4.87 TB/s, 72% of a copy's rate (32
-// heads over 8: 167); copies without arithmetic take 144 us.  256 contexts of 17
-// to 4,096 tokens, 32 over 8 heads (125 MB): 35.4 us, of which 22 are tiles, 7 the
-// start up to the first tile and 6 the joining of split contexts.  So:
+// (head_dim 128, up to 4 heads a KV head; 5 to 8: 661, 52 of them MMAs).  32
+// contexts of 16 to 32 K tokens, 8 KV heads of 128 (883 MB): 163 us with 32 query
+// heads, 5.4 TB/s, 80% of a copy's rate, 181 us with 64; copies without arithmetic
+// take 144 us.  256 contexts of 17 to 4,096 tokens, 32 over 8 heads (125 MB): 34.9
+// us, of which 22 are tiles, 7 the start up to the first tile and 6 the joining of
+// split contexts.  So:
 //  * One warp is one pipeline.  A warp owns a (sequence, KV head) context or a
 //    contiguous range of one.  Its tiles arrive in a ring of kStages tiles of
 //    its own that it fills itself with 16-byte asynchronous copies, nine a lane
@@ -24,8 +25,8 @@
 //    into fragments were slower than either.)
 //  * Twelve warps, one block an SM.  Its warps get equal ranges and equal turns.
 //    With three blocks of four warps the scheduler serves the oldest block
-//    first, and the other two finish 7 and 15% later on a half-empty SM (180 us
-//    for 162).
+//    first, and the other two finish 7 and 15% later on a half-empty SM (11%
+//    more time).
 //  * Transposed products: S^T = K Q^T (16 tokens x 8 heads), O^T += V^T P^T
 //    (16 head_dim rows x 8 heads), so that K and V are the A operands and 8
 //    heads, not 16, fill a product; more than 8 heads a KV head take two tiles.
@@ -56,6 +57,7 @@
 //
 // Roundings below fp32: the weights to a pair of binary16 values (2^-21), a
 // bfloat16 query's elements under 2^-14 of its row's largest, and the output.
+// Weights and the factors that join parts are ex2.approx (2^-22).
 #include <cmath>
 #include <mutex>
 
@@ -67,32 +69,34 @@ namespace pa {
 namespace {
 
 // Twelve warps leave a thread 168 registers, which o, the queries and a tile's
-// work need; 16 warps of 128 spill and measured the same on long contexts and 3
-// to 10% more on short ones (head_dim 64, without spills: 8% more).  Two head
-// tiles a KV head take 8 warps of 255 (12: 2% less to 15% more).
+// work need; 16 warps of 128 spill and measured 1 to 2% more on long contexts and
+// 2 to 8% on short ones (head_dim 64: 10%).  Two head tiles a KV head take 8 warps
+// of 255 (12: 16 to 29% more).
 __host__ __device__ constexpr int warps_of(int NH) { return NH == 1 ? 12 : 8; }
 constexpr int kTile = 32;                 // tokens per tile
-constexpr int kStages = 2;                // tiles in shared memory per warp (3 measured the same)
-// A block takes at least kLeast units, one a scheduler; 2 and 8 measured the same.
+constexpr int kStages = 2;                // tiles in shared memory per warp (3: 0 to 4% more)
+// Small batches take units / kLeast blocks, rounded up, so that each has about
+// kLeast, one a scheduler: 8.4 us for one context of 300 tokens and one KV head, 8.9
+// with 2 and with 8.
 constexpr int kLeast = 4;
 // A context's share of the work is its tiles and kStart for its start and end
 // (queries to fragments, the write): without it a warp whose range holds many
-// short contexts finishes last.  0 / 1 / 2 measured 85.6 / 62.2 / 62.9 us for
-// 64 contexts of 1 to 2,048 tokens and 32 KV heads, 38.8 / 35.6 / 36.3 for the
+// short contexts finishes last.  0 / 1 / 2 measured 86.2 / 60.9 / 61.8 us for
+// 64 contexts of 1 to 2,048 tokens and 32 KV heads, 39.8 / 34.9 / 35.7 for the
 // 256 contexts above.
 constexpr int kStart = 1;
 // Contexts of at most kWhole tiles go to one warp each when there are warps
-// enough, which saves joining parts: 7.1 us for 9.1 with 16 contexts of 1 to 64
-// tokens and 8 KV heads, 18.0 for 20.4 with 200 of 16 to 256 (12.0 for 11.1 with
-// 32 of 16 to 250).
+// enough, which saves joining parts: 7.4 us for 8.6 with 16 contexts of 1 to 64
+// tokens, 32 heads over 8, and 18.8 for 19.7 with 200 of 16 to 256 (12.5 for 10.5
+// with 32 of 16 to 250, which leave most warps without one).
 constexpr int kWhole = 8;
 constexpr int kRecords = 4;               // of a split context, loaded at a time
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kUnitBits = 44, kCounted = 1 << 18;   // of the scanned sums; sequences it counts
 // Weights are exp2(x - base) with base = a maximum less kShift, and a new base
-// once they pass exp2(kShift + kLag) = 2^15, inside binary16's range.  binary16
-// keeps its full precision down to 2^-14, so the shift moves the loss of small
-// weights from 2^-14 to 2^-22 of that maximum.  It cancels in o / l.
+// once they pass exp2(kShift + kLag) = 2^15, inside binary16's range.  A pair of
+// binary16 values leaves 2^-25 of a small weight, whose second value is subnormal:
+// the shift makes that 2^-33 of that maximum.  It cancels in o / l.
 constexpr float kShift = 8.f, kLag = 7.f;
 
 struct Args {
@@ -194,9 +198,9 @@ struct Walk {
 // computation's in norm, with the pair 3e-5 to 1.2e-4).  kTwin (at most 4 query
 // heads): the 8 head columns hold the heads twice, the first copy's weights
 // rounded, the second's the rest, so that the pair costs no second product; the
-// two are added at the end.  With bfloat16 outputs and 32 contexts of 16 to 32 K
-// tokens, 8 KV heads of 128, the pair takes 166.6 us for the 159.7 of one value
-// with 4 query heads each, 181 for 160 with 8.
+// two are added at the end.  With 32 contexts of 16 to 32 K tokens and 8 KV heads
+// of 128, the pair takes 163 us for the 160 of one value with 4 query heads each,
+// 181 for 161 with 8, and 137 for 118 with 16 heads to each of 4 KV heads.
 template <int D, bool kBF16, int NH, bool kTwin>
 struct Context {
   static constexpr int KS = D / 16;        // k-steps of S^T
@@ -524,7 +528,8 @@ struct Vec {
 };
 
 // Four elements of one row of a context, merged over parts: acc = sum_p
-// 2^(m_p - m) o_p, l likewise, m the largest m_p.
+// 2^(m_p - m) o_p, l likewise, m the largest m_p.  The factors are ex2.approx: off
+// by 2^-22, the same in o and l, below the weights' own rounding.
 struct Merged {
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float m = -INFINITY, l = 0.f;
@@ -681,8 +686,8 @@ __global__ void __launch_bounds__(warps_of(NH) * 32, 1)
     }
 
   // ---- this block's and this warp's range of units -------------------------
-  // at least kLeast units a block, so that small batches do not split contexts
-  // between blocks for nothing; whole, a context a warp
+  // about kLeast units a block in small batches, which then split contexts
+  // between few blocks; whole, a context a warp
   const long long U = whole ? contexts : (total & low) * a.H;
   const int least = whole ? 1 : kLeast;
   const long long nb = min((long long)gridDim.x, (U + least - 1) / least);
@@ -1012,9 +1017,11 @@ typedef void (*Kernel)(const Args);
 
 template <int D>
 Kernel pick_d(bool bf16, int G) {
-  if (G > 8) return bf16 ? decode_fp4_kernel<D, true, 2, false> : decode_fp4_kernel<D, false, 2, false>;
-  if (G > 4) return bf16 ? decode_fp4_kernel<D, true, 1, false> : decode_fp4_kernel<D, false, 1, false>;
-  return bf16 ? decode_fp4_kernel<D, true, 1, true> : decode_fp4_kernel<D, false, 1, true>;
+  if (bf16)
+    return G > 8 ? decode_fp4_kernel<D, true, 2, false>
+                 : (G > 4 ? decode_fp4_kernel<D, true, 1, false> : decode_fp4_kernel<D, true, 1, true>);
+  return G > 8 ? decode_fp4_kernel<D, false, 2, false>
+               : (G > 4 ? decode_fp4_kernel<D, false, 1, false> : decode_fp4_kernel<D, false, 1, true>);
 }
 
 // the ring of every warp (which its last part's record shares) and a slot each

@@ -195,7 +195,8 @@ def pa_cache_write_mapped(k, v, block_tables, token_seq, token_pos, k_cache, v_c
 def pa_copy_blocks(pairs, k_cache, v_cache, err=None):
     """Copy pool block src -> dst (K and V) for each row (src, dst) of pairs.
 
-    Pools of float16 / bfloat16 elements, uint8 E4M3 codes, or 4-bit pools."""
+    Pools of float16 / bfloat16 elements, uint8 E4M3 codes, or 4-bit pools: uint8
+    with a last dimension of 36 or 72, which no E4M3 pool has."""
     L = _lib.load()
     _pool_shape(k_cache, v_cache)
     nb, B, H, D, code = _block_pools(k_cache, v_cache)
