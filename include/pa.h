@@ -447,6 +447,37 @@ int pa_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_str
                    int64_t* slot_mapping, int32_t* err_word, pa_stream stream);
 
 /*
+ * pa_append_rope_axes -- pa_append_rope for tokens whose position has several
+ * axes (time, height and width of image and video patches, say): the angle of
+ * frequency i < rotary_dim / 2 comes from the token's position on axis
+ * axis_of[i]; the other arguments and the results are those of pa_append_rope
+ * ([P1] "How is vLLM's KV cache paged?", bullet "Writing", for the store).
+ *   rotary_dim    as there, > 0
+ *   cos_sin       its row p holds the angles of position p on any axis
+ *   axis_of       uint8 [rotary_dim / 2], device memory: runs of frequencies
+ *                 per axis, axes dealt out in turn, or any other map
+ *   rot_pos       int32 [num_axes][num_tokens]: the positions that select
+ *                 angles; token_pos places the token in the cache alone and may
+ *                 pass max_pos
+ *   num_axes      1 to 4
+ * A token with a rot_pos outside [0, max_pos) on any axis, and every token when
+ * an axis_of is not below num_axes, gets slot -1, writes nothing and sets
+ * PA_DEVERR_POSITION.  With rot_pos = token_pos on every axis the results are
+ * pa_append_rope's bit for bit.
+ */
+int pa_append_rope_axes(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, int32_t src_dtype, const float* cos_sin,
+                        int32_t rotary_dim, int32_t max_pos, const uint8_t* axis_of,
+                        const int32_t* rot_pos, int32_t num_axes, int32_t interleaved,
+                        const void* q_norm, const void* k_norm, float eps,
+                        const int32_t* block_tables, int32_t table_stride, int32_t num_seqs,
+                        const int32_t* token_seq, const int32_t* token_pos, int64_t num_tokens,
+                        void* q_out, void* k_cache, void* v_cache, int64_t num_blocks,
+                        int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                        int32_t head_dim, int32_t cache_dtype, float k_scale, float v_scale,
+                        int64_t* slot_mapping, int32_t* err_word, pa_stream stream);
+
+/*
  * pa_cache_write_fp4 -- pa_cache_write into a 4-bit KV cache: a quarter of the
  * 16-bit pool's bytes in codes plus a scale byte for every 16 of them (0.5625
  * bytes an element).  The pages stop at kv_cache_dtype="fp8" ([P1] "How can one
@@ -535,6 +566,64 @@ int pa_decode_fp4(const void* q, const void* k_cache, const void* v_cache,
                   float k_scale, float v_scale, int32_t window, void* out, void* workspace,
                   size_t workspace_bytes, int32_t flags, int32_t num_ctas, int32_t* err_word,
                   pa_stream stream);
+
+/*
+ * pa_prefill_fp8, pa_prefill_fp4 -- pa_prefill over quantized pools: chunks of
+ * new tokens (one, several that are verified together, a part of a prompt)
+ * attend to an E4M3 or a 4-bit cache as it lies in the pool, with sliding-window
+ * attention as in pa_decode_window.  [P1] "How does it support prompts of
+ * arbitrary length?" (the chunks); [P1] "How can one customize the tokenizer,
+ * cache strategy, or scheduler strategy?" (the quantized cache).  Sequence i
+ * brings L_i = query_start[i + 1] - query_start[i] new tokens whose K/V are
+ * already in the cache (pa_append_rope, pa_append_rope_axes or the pool's own
+ * write) as its last L_i of seq_lens[i] tokens; new token j, at position
+ * p = seq_lens[i] - L_i + j, attends to tokens [max(0, p - window + 1), p]:
+ *   out = v_scale * softmax(scale * k_scale * q . K^T) . V
+ * with K, V what the codes stand for before the tensor's scale.
+ *   q, out        [total_q][num_q_heads][head_dim] in q_dtype (PA_F16 or
+ *                 PA_BF16); out must not alias q; rows of no sequence are left
+ *                 as they are
+ *   k_cache, v_cache  pools of pa_cache_write_fp8 / pa_cache_write_fp4,
+ *                 block_size a power of two in [4, 256]
+ *   query_start   int32 [num_seqs + 1], non-decreasing, in [0, total_q]
+ *   scale         finite; k_scale, v_scale finite and > 0
+ *   window        >= 1, or 0: no window.  Table entries of blocks wholly before
+ *                 token max(0, seq_lens[i] - L_i - window + 1) are never read
+ *   workspace     pa_prefill_quant_workspace_size() bytes, the first
+ *                 PA_PREFILL_QUANT_COUNTERS of them zero-filled before its first
+ *                 use; every call that runs to its end leaves them zero (one
+ *                 that reported PA_DEVERR_TIMEOUT, or whose lengths changed while
+ *                 it ran, may not: zero-fill them again).  Calls that share a
+ *                 workspace must not overlap on the GPU
+ * Any num_seqs.  The result depends on neither the blocks' places nor the order
+ * in which thread blocks finish.  Code values are exact in binary16, queries are
+ * binary16 (a bfloat16 row after a power-of-two scaling), the softmax weights
+ * are rounded to binary16 (2^-11) and summed as rounded, every sum is fp32.
+ * A sequence with L_i > seq_lens[i], a length outside its table row or a
+ * query_start outside [0, total_q] sets PA_DEVERR_SEQ_LEN; its rows, those in
+ * [0, total_q], get zeros.  Tokens of a block whose table entry is out of range
+ * (PA_DEVERR_BLOCK_ID) are left out of the softmax; a row left with none gets
+ * zeros.  A NaN among the codes or scales of an attended token's value row
+ * makes the whole output row NaN; tokens that a row does not attend to never
+ * reach it, whatever they hold.
+ */
+#define PA_PREFILL_QUANT_COUNTERS 16384
+int pa_prefill_quant_workspace_size(int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                    size_t* bytes);
+int pa_prefill_fp8(const void* q, const void* k_cache, const void* v_cache,
+                   const int32_t* block_tables, int32_t table_stride, const int32_t* seq_lens,
+                   const int32_t* query_start, int32_t num_seqs, int64_t total_q,
+                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                   int32_t block_size, int64_t num_blocks, int32_t q_dtype, float scale,
+                   float k_scale, float v_scale, int32_t window, void* out, void* workspace,
+                   size_t workspace_bytes, int32_t* err_word, pa_stream stream);
+int pa_prefill_fp4(const void* q, const void* k_cache, const void* v_cache,
+                   const int32_t* block_tables, int32_t table_stride, const int32_t* seq_lens,
+                   const int32_t* query_start, int32_t num_seqs, int64_t total_q,
+                   int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                   int32_t block_size, int64_t num_blocks, int32_t q_dtype, float scale,
+                   float k_scale, float v_scale, int32_t window, void* out, void* workspace,
+                   size_t workspace_bytes, int32_t* err_word, pa_stream stream);
 
 /*
  * pa_gather_kv -- (test support) gather every sequence's K and V rows into

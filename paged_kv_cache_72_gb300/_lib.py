@@ -32,6 +32,7 @@ PA_DECODE_MMA = 2
 PA_DECODE_TABLES_READY = 0x100
 PA_NOALLOC_SCRATCH_BYTES = 16 << 20
 PA_DECODE_MAX_CTAS = 16384
+PA_PREFILL_QUANT_COUNTERS = 16384
 PA_PREFILL_WARP_MMA = 0
 PA_PREFILL_TENSOR_CORE = 1
 
@@ -77,6 +78,11 @@ SIGNATURES = {
                                       _vp, _vp, ctypes.c_float, _vp, _i32, _i32, _vp, _vp, _i64,
                                       _vp, _vp, _vp, _i64, _i32, _i32, _i32, _i32, _i32,
                                       ctypes.c_float, ctypes.c_float, _vp, _vp, _vp]),
+    "pa_append_rope_axes": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i32, _i32,
+                                           _vp, _vp, _i32, _i32, _vp, _vp, ctypes.c_float, _vp,
+                                           _i32, _i32, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _i32,
+                                           _i32, _i32, _i32, _i32, ctypes.c_float, ctypes.c_float,
+                                           _vp, _vp, _vp]),
     "pa_cache_write_fp4": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i64, _vp, _vp, _i64, _i32, _i32,
                                           _i32, ctypes.c_float, ctypes.c_float, _vp, _vp]),
     "pa_cache_write_fp4_mapped": (ctypes.c_int, [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _vp, _i64,
@@ -88,6 +94,15 @@ SIGNATURES = {
     "pa_decode_fp4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _i32,
                                      _i64, _i32, ctypes.c_float, ctypes.c_float, ctypes.c_float,
                                      _i32, _vp, _vp, _sz, _i32, _i32, _vp, _vp]),
+    "pa_prefill_quant_workspace_size": (ctypes.c_int, [_i32, _i32, _i32, ctypes.POINTER(_sz)]),
+    "pa_prefill_fp8": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i32,
+                                      _i32, _i32, _i32, _i64, _i32, ctypes.c_float,
+                                      ctypes.c_float, ctypes.c_float, _i32, _vp, _vp, _sz, _vp,
+                                      _vp]),
+    "pa_prefill_fp4": (ctypes.c_int, [_vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _i64, _i32,
+                                      _i32, _i32, _i32, _i64, _i32, ctypes.c_float,
+                                      ctypes.c_float, ctypes.c_float, _i32, _vp, _vp, _sz, _vp,
+                                      _vp]),
     "pa_gather_kv": (ctypes.c_int, [_vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, _i32, _i32, _i64,
                                     _i32, _i32, _vp, _vp, _vp, _vp]),
     "pa_get_error": (ctypes.c_int, [_vp, _vp, ctypes.POINTER(_i32)]),

@@ -6,7 +6,8 @@
 //   norm      y_d = x_d * r * w_d,  r = 1 / sqrt(mean_d(x_d^2) + eps)
 //   rotation  a' = a c - b s,  b' = b c + a s  for the pairs (a, b) =
 //             (y_i, y_{i + rot/2}), or (y_{2i}, y_{2i+1}) when interleaved,
-//             i < rot / 2, with c, s the position's row of the angle table
+//             i < rot / 2, with c, s the position's row of the angle table; with
+//             axes, frequency i's c, s from the row of its axis's position
 //   store     round to 16 bits; an E4M3 or E2M1 pool quantizes that 16-bit value
 // Without a norm the products of the rotation are rounded before they are added
 // (no fused multiply-add): bit for bit what separate products and a sum give.
@@ -40,6 +41,9 @@ struct AppendArgs {
   long long q_stride, k_stride, v_stride;   // elements between tokens
   const float* cos_sin;                     // [max_pos][rot]: rot / 2 cosines, then sines
   int rot, max_pos, interleaved;
+  const uint8_t* axis_of;                   // [rot / 2]: the axis of every frequency
+  const int32_t* rot_pos;                   // [axes][tokens]: positions that select angles
+  int axes;
   const uint16_t* q_norm;
   const uint16_t* k_norm;
   float eps;
@@ -58,11 +62,14 @@ struct AppendArgs {
   int32_t* err;
 };
 
+constexpr int kMaxAxes = 4;
 constexpr int kThreads = 128;   // of a block of every kernel here (64 measured no better)
 
 // The slot of token `tok`, or -1 for a token that writes nothing: a padding
 // token (sequence -1, or a negative given slot), or a bad one, which sets an
 // error bit (when `report`).  pos receives its position.
+// kAxes: the position selects no angles.
+template <bool kAxes = false>
 __device__ __forceinline__ long long append_slot(const AppendArgs& a, long long tok, bool report,
                                                  int& pos) {
   if (a.slots_in) {
@@ -78,7 +85,8 @@ __device__ __forceinline__ long long append_slot(const AppendArgs& a, long long 
   pos = __ldg(a.tok_pos + tok);
   if (i == -1) return -1;
   if (i < 0 || i >= a.num_seqs || pos < 0 ||
-      (long long)pos >= ((long long)a.stride << a.log2B) || (a.rot > 0 && pos >= a.max_pos)) {
+      (long long)pos >= ((long long)a.stride << a.log2B) ||
+      (!kAxes && a.rot > 0 && pos >= a.max_pos)) {
     if (report) set_error(a.err, PA_DEVERR_POSITION);
     return -1;
   }
@@ -191,6 +199,56 @@ struct Turn {
       c[2 * u + 1] = {c4.z, c4.w};
       s[2 * u] = {s4.x, s4.y};
       s[2 * u + 1] = {s4.z, s4.w};
+    }
+  }
+
+  // load with a position per axis, at[x] on axis x: runs of four frequencies of
+  // one axis as above, others one by one (they come from L1 or L2 like the rows)
+  __device__ __forceinline__ void load_axes(const AppendArgs& a, const int (&at)[kMaxAxes],
+                                            int d0) {
+    const int half = a.rot >> 1, lane = threadIdx.x & 31;
+    on = d0 < a.rot;
+    swap = a.interleaved != 0;
+    from = lane;
+    if (!on) return;
+    const bool first = d0 < half;
+    const int i0 = swap ? d0 / 2 : (first ? d0 : d0 - half);
+    if (!swap) from = first ? lane + (half >> 3) : lane - (half >> 3);
+    float4 c4[2], s4[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (u == 1 && swap) break;
+      const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(a.axis_of + i0 + 4 * u));
+      const float* cs[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t x = (w >> (8 * e)) & 3u;
+        const int pos = x == 0 ? at[0] : (x == 1 ? at[1] : (x == 2 ? at[2] : at[3]));
+        cs[e] = a.cos_sin + (size_t)pos * a.rot + i0 + 4 * u + e;
+      }
+      if (w == (w & 0xffu) * 0x01010101u) {
+        c4[u] = __ldg(reinterpret_cast<const float4*>(cs[0]));
+        s4[u] = __ldg(reinterpret_cast<const float4*>(cs[0] + half));
+      } else {
+        c4[u] = make_float4(__ldg(cs[0]), __ldg(cs[1]), __ldg(cs[2]), __ldg(cs[3]));
+        s4[u] = make_float4(__ldg(cs[0] + half), __ldg(cs[1] + half), __ldg(cs[2] + half),
+                            __ldg(cs[3] + half));
+      }
+    }
+    if (swap) {
+      c[0] = {c4[0].x, c4[0].x}; c[1] = {c4[0].y, c4[0].y};
+      c[2] = {c4[0].z, c4[0].z}; c[3] = {c4[0].w, c4[0].w};
+      s[0] = {-s4[0].x, s4[0].x}; s[1] = {-s4[0].y, s4[0].y};
+      s[2] = {-s4[0].z, s4[0].z}; s[3] = {-s4[0].w, s4[0].w};
+      return;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (first) s4[u] = make_float4(-s4[u].x, -s4[u].y, -s4[u].z, -s4[u].w);
+      c[2 * u] = {c4[u].x, c4[u].y};
+      c[2 * u + 1] = {c4[u].z, c4[u].w};
+      s[2 * u] = {s4[u].x, s4[u].y};
+      s[2 * u + 1] = {s4[u].z, s4[u].w};
     }
   }
 
@@ -321,7 +379,27 @@ constexpr int kBlocks = 7;
 // block, per token: slot, angles and weights cost a warp some 400 instructions
 // and three dependent loads, once for 24 passes of rows instead of four times
 // (50 us with a block per token, 42 with a warp at the same six blocks an SM).
-template <int D, bool kBF16, int kPool, bool kNorm>
+// Whether token `tok` can be rotated with axes: its positions, which `at` receives,
+// lie in the table, and every frequency's axis is one of them (every lane of the
+// warp takes part; a row's lanes read all of axis_of between them).
+__device__ __forceinline__ bool axes_ok(const AppendArgs& a, long long tok, long long n, int d0,
+                                        int (&at)[kMaxAxes]) {
+  bool ok = true;
+#pragma unroll
+  for (int x = 0; x < kMaxAxes; ++x) {
+    at[x] = x < a.axes ? __ldg(a.rot_pos + x * n + tok) : 0;
+    ok = ok && at[x] >= 0 && (x >= a.axes || at[x] < a.max_pos);
+  }
+  if (2 * d0 < a.rot) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2*>(a.axis_of + d0));
+    const uint32_t most = (uint32_t)(a.axes - 1) * 0x01010101u;
+    ok = ok && (__vcmpgtu4(w.x, most) | __vcmpgtu4(w.y, most)) == 0u;
+  }
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
+// kAxes: the angles of each frequency from the position on its axis.
+template <int D, bool kBF16, int kPool, bool kNorm, bool kAxes>
 __global__ void __launch_bounds__(kThreads, kBlocks)
     append_kernel(const AppendArgs a, int log2_shares, long long n) {
   constexpr int LPR = D / 8;               // lanes per row
@@ -349,13 +427,21 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     xk = *reinterpret_cast<const uint4*>(kr + r0 * D);
     xv = *reinterpret_cast<const uint4*>(vr + r0 * D);
   }
-  int pos;
+  int pos, at[kMaxAxes];
   const bool lead = lane == 0 && share == 0;
-  const long long slot = append_slot(a, tok, lead, pos);
+  long long slot = append_slot<kAxes>(a, tok, lead, pos);
+  if constexpr (kAxes) {
+    const bool ok = axes_ok(a, tok, n, d0, at);
+    if (slot >= 0 && !ok) {
+      if (lead) set_error(a.err, PA_DEVERR_POSITION);
+      slot = -1;
+    }
+  }
   if (a.slots && lead) a.slots[tok] = slot;
   if (slot < 0) return;                    // the whole warp: every lane found the same slot
   Turn t;
-  t.load(a, pos, d0);
+  if constexpr (kAxes) t.load_axes(a, at, d0);
+  else t.load(a, pos, d0);
   // rows in lockstep over the warp (the shuffles need every lane)
   if (kNorm && a.q_norm) t.join<kBF16>(a.q_norm, a.rot > 0, d0);
   uint16_t* const qo = a.q_out + (size_t)tok * a.Hq * D + d0;
@@ -372,7 +458,10 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     }
   }
   if constexpr (kNorm) {   // the keys' weights: the angles are read again (from L1)
-    if (a.q_norm) t.load(a, pos, d0);
+    if (a.q_norm) {
+      if constexpr (kAxes) t.load_axes(a, at, d0);
+      else t.load(a, pos, d0);
+    }
     if (a.k_norm) t.join<kBF16>(a.k_norm, a.rot > 0, d0);
   }
   for (int first = share * RPP; first < a.H; first += step) {
@@ -539,7 +628,7 @@ int tokens_per_block(int lanes, int rows, long long n, int sm_count) {
   return t < 1 ? 1 : (int)t;
 }
 
-template <int D, bool kBF16, int kPool, bool kNorm>
+template <int D, bool kBF16, int kPool, bool kNorm, bool kAxes>
 cudaError_t launch_append_n(const AppendArgs& a, long long n, int sm_count, cudaStream_t s) {
   // shares of a token's rows, a power of two: until six warps an SM, and on to 32
   // warps an SM as long as a warp has more than 20 passes of rows (the 1,939 tokens
@@ -560,25 +649,26 @@ cudaError_t launch_append_n(const AppendArgs& a, long long n, int sm_count, cuda
     ++log2_shares;
   }
   constexpr int kWarps = kThreads / 32;
-  return launch_pdl(append_kernel<D, kBF16, kPool, kNorm>,
+  return launch_pdl(append_kernel<D, kBF16, kPool, kNorm, kAxes>,
                     dim3((unsigned)(((n << log2_shares) + kWarps - 1) / kWarps)), dim3(kThreads), 0, s,
                     a, log2_shares, n);
 }
 
-template <int D, bool kBF16>
+template <int D, bool kBF16, bool kAxes>
 cudaError_t launch_append_p(const AppendArgs& a, int pool, long long n, int sm_count,
                             cudaStream_t s) {
   const bool norm = a.q_norm || a.k_norm;
   if (pool == kPoolE2M1)
-    return norm ? launch_append_n<D, kBF16, kPoolE2M1, true>(a, n, sm_count, s)
-                : launch_append_n<D, kBF16, kPoolE2M1, false>(a, n, sm_count, s);
+    return norm ? launch_append_n<D, kBF16, kPoolE2M1, true, kAxes>(a, n, sm_count, s)
+                : launch_append_n<D, kBF16, kPoolE2M1, false, kAxes>(a, n, sm_count, s);
   if (pool == kPoolE4M3)
-    return norm ? launch_append_n<D, kBF16, kPoolE4M3, true>(a, n, sm_count, s)
-                : launch_append_n<D, kBF16, kPoolE4M3, false>(a, n, sm_count, s);
-  return norm ? launch_append_n<D, kBF16, kPool16, true>(a, n, sm_count, s)
-              : launch_append_n<D, kBF16, kPool16, false>(a, n, sm_count, s);
+    return norm ? launch_append_n<D, kBF16, kPoolE4M3, true, kAxes>(a, n, sm_count, s)
+                : launch_append_n<D, kBF16, kPoolE4M3, false, kAxes>(a, n, sm_count, s);
+  return norm ? launch_append_n<D, kBF16, kPool16, true, kAxes>(a, n, sm_count, s)
+              : launch_append_n<D, kBF16, kPool16, false, kAxes>(a, n, sm_count, s);
 }
 
+template <bool kAxes>
 int launch_append(const AppendArgs& a, int D, bool bf16, int pool, long long n, cudaStream_t s,
                   const char* what) {
   DeviceInfo di;
@@ -586,11 +676,11 @@ int launch_append(const AppendArgs& a, int D, bool bf16, int pool, long long n, 
   clear_stale_error();
   cudaError_t e;
   if (D == 64)
-    e = bf16 ? launch_append_p<64, true>(a, pool, n, di.sm_count, s)
-             : launch_append_p<64, false>(a, pool, n, di.sm_count, s);
+    e = bf16 ? launch_append_p<64, true, kAxes>(a, pool, n, di.sm_count, s)
+             : launch_append_p<64, false, kAxes>(a, pool, n, di.sm_count, s);
   else
-    e = bf16 ? launch_append_p<128, true>(a, pool, n, di.sm_count, s)
-             : launch_append_p<128, false>(a, pool, n, di.sm_count, s);
+    e = bf16 ? launch_append_p<128, true, kAxes>(a, pool, n, di.sm_count, s)
+             : launch_append_p<128, false, kAxes>(a, pool, n, di.sm_count, s);
   return launch_status(e, what);
 }
 
@@ -647,7 +737,7 @@ int write_fp4(const void* k, const void* v, int32_t src_dtype, AppendArgs a, int
   constexpr int kFewLanes = 8 * 32;
   static_assert(kFewLanes <= kBatch * kThreads, "a token of few rows fits a block's registers");
   if (2 * num_kv_heads * (head_dim / 8) >= kFewLanes)
-    return launch_append(a, head_dim, src_dtype == PA_BF16, kPoolE2M1, num_tokens, s, what);
+    return launch_append<false>(a, head_dim, src_dtype == PA_BF16, kPoolE2M1, num_tokens, s, what);
   DeviceInfo di;
   if (int rc = current_device_info(&di)) return rc;
   const int per = tokens_per_block(head_dim / 8, 2 * num_kv_heads, num_tokens, di.sm_count);
@@ -665,23 +755,16 @@ int write_fp4(const void* k, const void* v, int32_t src_dtype, AppendArgs a, int
   return launch_status(e, what);
 }
 
-}  // namespace
-
-}  // namespace pa
-
-using namespace pa;
-
-extern "C" {
-
-int pa_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
-                   int64_t v_stride, int32_t src_dtype, const float* cos_sin, int32_t rotary_dim,
-                   int32_t max_pos, int32_t interleaved, const void* q_norm, const void* k_norm,
-                   float eps, const int32_t* block_tables, int32_t table_stride, int32_t num_seqs,
-                   const int32_t* token_seq, const int32_t* token_pos, int64_t num_tokens,
-                   void* q_out, void* k_cache, void* v_cache, int64_t num_blocks,
-                   int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
-                   int32_t head_dim, int32_t cache_dtype, float k_scale, float v_scale,
-                   int64_t* slot_mapping, int32_t* err_word, pa_stream stream) {
+// The append behind its two entry points; num_axes 0: one position a token.
+int append(const uint8_t* axis_of, const int32_t* rot_pos, int32_t num_axes, const void* q,
+           int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+           int32_t src_dtype, const float* cos_sin, int32_t rotary_dim, int32_t max_pos,
+           int32_t interleaved, const void* q_norm, const void* k_norm, float eps,
+           const int32_t* block_tables, int32_t table_stride, int32_t num_seqs,
+           const int32_t* token_seq, const int32_t* token_pos, int64_t num_tokens, void* q_out,
+           void* k_cache, void* v_cache, int64_t num_blocks, int32_t block_size,
+           int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim, int32_t cache_dtype,
+           float k_scale, float v_scale, int64_t* slot_mapping, int32_t* err_word, pa_stream stream) {
   if (num_tokens < 0 || num_seqs < 0 || table_stride < 0 || num_blocks < 0 || num_q_heads < 0 ||
       rotary_dim < 0 || max_pos < 0)
     return PA_ERR_INVALID_ARG;
@@ -698,6 +781,7 @@ int pa_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_str
     return PA_ERR_INVALID_ARG;
   if (num_q_heads > 0 && (!q || !q_out)) return PA_ERR_INVALID_ARG;
   if (rotary_dim > 0 && !cos_sin) return PA_ERR_INVALID_ARG;
+  if (num_axes && (!axis_of || !rot_pos || !aligned16(axis_of))) return PA_ERR_INVALID_ARG;
   const int64_t kv_row = (int64_t)num_kv_heads * head_dim;
   if (k_stride < kv_row || v_stride < kv_row || k_stride % 8 || v_stride % 8)
     return PA_ERR_INVALID_ARG;
@@ -717,6 +801,9 @@ int pa_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_str
   a.rot = rotary_dim;
   a.max_pos = max_pos;
   a.interleaved = interleaved ? 1 : 0;
+  a.axis_of = axis_of;
+  a.rot_pos = rot_pos;
+  a.axes = num_axes;
   a.q_norm = static_cast<const uint16_t*>(q_norm);
   a.k_norm = static_cast<const uint16_t*>(k_norm);
   a.eps = eps;
@@ -737,8 +824,55 @@ int pa_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_str
   a.slots = slot_mapping;
   a.err = err_word;
   const int pool = four ? kPoolE2M1 : (cache_dtype == PA_FP8_E4M3 ? kPoolE4M3 : kPool16);
-  return launch_append(a, head_dim, src_dtype == PA_BF16, pool, num_tokens,
-                       static_cast<cudaStream_t>(stream), "append launch");
+  const bool bf16 = src_dtype == PA_BF16;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return num_axes ? launch_append<true>(a, head_dim, bf16, pool, num_tokens, s,
+                                        "append (axes) launch")
+                  : launch_append<false>(a, head_dim, bf16, pool, num_tokens, s, "append launch");
+}
+
+}  // namespace
+
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+int pa_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                   int64_t v_stride, int32_t src_dtype, const float* cos_sin, int32_t rotary_dim,
+                   int32_t max_pos, int32_t interleaved, const void* q_norm, const void* k_norm,
+                   float eps, const int32_t* block_tables, int32_t table_stride, int32_t num_seqs,
+                   const int32_t* token_seq, const int32_t* token_pos, int64_t num_tokens,
+                   void* q_out, void* k_cache, void* v_cache, int64_t num_blocks,
+                   int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                   int32_t cache_dtype, float k_scale, float v_scale, int64_t* slot_mapping,
+                   int32_t* err_word, pa_stream stream) {
+  return append(nullptr, nullptr, 0, q, q_stride, k, k_stride, v, v_stride, src_dtype, cos_sin,
+                rotary_dim, max_pos, interleaved, q_norm, k_norm, eps, block_tables, table_stride,
+                num_seqs, token_seq, token_pos, num_tokens, q_out, k_cache, v_cache, num_blocks,
+                block_size, num_q_heads, num_kv_heads, head_dim, cache_dtype, k_scale, v_scale,
+                slot_mapping, err_word, stream);
+}
+
+int pa_append_rope_axes(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, int32_t src_dtype, const float* cos_sin,
+                        int32_t rotary_dim, int32_t max_pos, const uint8_t* axis_of,
+                        const int32_t* rot_pos, int32_t num_axes, int32_t interleaved,
+                        const void* q_norm, const void* k_norm, float eps,
+                        const int32_t* block_tables, int32_t table_stride, int32_t num_seqs,
+                        const int32_t* token_seq, const int32_t* token_pos, int64_t num_tokens,
+                        void* q_out, void* k_cache, void* v_cache, int64_t num_blocks,
+                        int32_t block_size, int32_t num_q_heads, int32_t num_kv_heads,
+                        int32_t head_dim, int32_t cache_dtype, float k_scale, float v_scale,
+                        int64_t* slot_mapping, int32_t* err_word, pa_stream stream) {
+  if (num_axes < 1 || num_axes > kMaxAxes) return PA_ERR_UNSUPPORTED;
+  if (rotary_dim <= 0) return PA_ERR_INVALID_ARG;
+  return append(axis_of, rot_pos, num_axes, q, q_stride, k, k_stride, v, v_stride, src_dtype,
+                cos_sin, rotary_dim, max_pos, interleaved, q_norm, k_norm, eps, block_tables,
+                table_stride, num_seqs, token_seq, token_pos, num_tokens, q_out, k_cache, v_cache,
+                num_blocks, block_size, num_q_heads, num_kv_heads, head_dim, cache_dtype, k_scale,
+                v_scale, slot_mapping, err_word, stream);
 }
 
 int pa_cache_write_fp4(const void* k, const void* v, int32_t src_dtype,

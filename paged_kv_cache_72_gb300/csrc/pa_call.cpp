@@ -1,4 +1,5 @@
-// Python calls of the append and of the 4-bit cache, as an extension module.
+// Python calls of the appends, of the 4-bit cache and of the prefill over
+// quantized caches, as an extension module.
 //
 // The binding marshals: it checks types, shapes, layouts and devices, takes
 // addresses and the current stream, and calls the C ABI.  For a decode step of
@@ -193,11 +194,18 @@ int kv_rows(const at::Tensor& k, const at::Tensor& v, int64_t n, const Pools& p)
   return code16(k, "k");
 }
 
-// (q, k, v, cos_sin, block_tables, token_seq, token_pos, k_cache, v_cache,
-//  interleaved, q_norm, k_norm, eps, k_scale, v_scale, q_out, slot_mapping, err)
+// (q, k, v, cos_sin, [axis_of, rot_pos,] block_tables, token_seq, token_pos,
+//  k_cache, v_cache, interleaved, q_norm, k_norm, eps, k_scale, v_scale, q_out,
+//  slot_mapping, err)
+template <bool kAxes>
 int append_rope(Args& a) {
   const at::Tensor *q = a.any("q", true), *k = a.any("k"), *v = a.any("v");
-  const at::Tensor* cs = a.flat("cos_sin", true);
+  const at::Tensor* cs = a.flat("cos_sin", !kAxes);
+  const at::Tensor *axis_of = nullptr, *rot_pos = nullptr;
+  if constexpr (kAxes) {
+    axis_of = a.flat("axis_of", at::kByte, "uint8");
+    rot_pos = a.flat("rot_pos", at::kInt, "int32");
+  }
   const Tokens t = tokens(a);
   const Pools p = pools(a, false);
   const bool interleaved = a.truth();
@@ -235,6 +243,22 @@ int append_rope(Args& a) {
       raise(PyExc_ValueError, "q_norm and k_norm must be [D] of k's dtype");
   if (Hq > INT32_MAX || rot > INT32_MAX || max_pos > INT32_MAX)
     raise(PyExc_ValueError, "a dimension exceeds 32 bits");
+  if constexpr (kAxes) {
+    if (axis_of->numel() != rot / 2)
+      raise(PyExc_ValueError, "axis_of must be [rotary_dim / 2]");
+    if (rot_pos->dim() != 2 || rot_pos->size(1) != t.n || rot_pos->size(0) < 1 ||
+        rot_pos->size(0) > 4)
+      raise(PyExc_ValueError, "rot_pos must be [num_axes, num_tokens], 1 to 4 axes");
+    return pa_append_rope_axes(
+        at_(q), qs, at_(k), ks, at_(v), vs, code, static_cast<const float*>(at_(cs)), (int)rot,
+        (int)max_pos, static_cast<const uint8_t*>(at_(axis_of)),
+        static_cast<const int32_t*>(at_(rot_pos)), (int)rot_pos->size(0), interleaved ? 1 : 0,
+        at_(qn), at_(kn), (float)eps, static_cast<const int32_t*>(at_(t.bt)), t.stride, t.seqs,
+        static_cast<const int32_t*>(at_(t.seq)), static_cast<const int32_t*>(at_(t.pos)), t.n,
+        at_(q_out), at_(p.k), at_(p.v), p.blocks, p.B, (int)Hq, p.H, p.D, p.code, (float)k_scale,
+        (float)v_scale, static_cast<int64_t*>(at_(slots)), static_cast<int32_t*>(at_(err)),
+        a.stream());
+  }
   return pa_append_rope(
       at_(q), qs, at_(k), ks, at_(v), vs, code, static_cast<const float*>(at_(cs)), (int)rot,
       (int)max_pos, interleaved ? 1 : 0, at_(qn), at_(kn), (float)eps,
@@ -318,6 +342,38 @@ int decode_fp4(Args& a) {
                        static_cast<int32_t*>(at_(err)), a.stream());
 }
 
+// (q, k_cache, v_cache, block_tables, seq_lens, query_start, scale, k_scale,
+//  v_scale, window, out, workspace, err)
+template <bool kFour>
+int prefill_quant(Args& a) {
+  const at::Tensor* q = a.flat("q");
+  const Pools p = pools(a, kFour);
+  if (!kFour && p.code != PA_FP8_E4M3)
+    raise(PyExc_TypeError, "E4M3 pools must be uint8 tensors of codes [num_blocks, B, H_kv, D]");
+  const at::Tensor* bt = a.flat("block_tables", at::kInt, "int32");
+  const at::Tensor* lens = a.flat("seq_lens", at::kInt, "int32");
+  const at::Tensor* start = a.flat("query_start", at::kInt, "int32");
+  const double scale = a.number(), k_scale = a.number(), v_scale = a.number();
+  const long window = a.integer();
+  const at::Tensor *out = a.flat("out"), *ws = a.flat("workspace");
+  const at::Tensor* err = err_word(a);
+  const int code = code16(*q, "q");
+  if (q->dim() != 3 || q->size(2) != p.D || q->size(1) > INT32_MAX)
+    raise(PyExc_ValueError, "q must be [total_q, Hq, D]");
+  const int64_t N = lens->numel();
+  if (N > INT32_MAX || start->numel() != N + 1 || bt->dim() != 2 || bt->size(0) != N ||
+      bt->size(1) > INT32_MAX)
+    raise(PyExc_ValueError, "query_start must be [N + 1], block_tables [N, stride], seq_lens [N]");
+  if (out->sizes() != q->sizes() || out->scalar_type() != q->scalar_type())
+    raise(PyExc_ValueError, "out must be [total_q, Hq, D] of q's dtype");
+  return (kFour ? pa_prefill_fp4 : pa_prefill_fp8)(
+      at_(q), at_(p.k), at_(p.v), static_cast<const int32_t*>(at_(bt)), (int)bt->size(1),
+      static_cast<const int32_t*>(at_(lens)), static_cast<const int32_t*>(at_(start)), (int)N,
+      q->size(0), (int)q->size(1), p.H, p.D, p.B, p.blocks, code, (float)scale, (float)k_scale,
+      (float)v_scale, (int)window, at_(out), at_(ws), (size_t)ws->numel() * ws->element_size(),
+      static_cast<int32_t*>(at_(err)), a.stream());
+}
+
 // No C++ exception leaves a call.
 template <int (*kCall)(Args&), int kArgs>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -337,15 +393,18 @@ PyCFunction fast() {
 }
 
 PyMethodDef methods[] = {
-    {"append_rope", fast<append_rope, 18>(), METH_FASTCALL, nullptr},
+    {"append_rope", fast<append_rope<false>, 18>(), METH_FASTCALL, nullptr},
+    {"append_rope_axes", fast<append_rope<true>, 20>(), METH_FASTCALL, nullptr},
     {"cache_write_fp4", fast<cache_write_fp4, 8>(), METH_FASTCALL, nullptr},
     {"cache_write_fp4_mapped", fast<cache_write_fp4_mapped, 11>(), METH_FASTCALL, nullptr},
     {"cache_read_fp4", fast<cache_read_fp4, 8>(), METH_FASTCALL, nullptr},
     {"decode_fp4", fast<decode_fp4, 14>(), METH_FASTCALL, nullptr},
+    {"prefill_fp8", fast<prefill_quant<false>, 13>(), METH_FASTCALL, nullptr},
+    {"prefill_fp4", fast<prefill_quant<true>, 13>(), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pa_call",
-                      "Marshalling of the append's and the 4-bit cache's calls.", -1, methods,
+                      "Marshalling of the appends', the 4-bit cache's and the quantized prefill's calls.", -1, methods,
                       nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -2,8 +2,9 @@
 
 Every function takes CUDA tensors, checks dtypes and shapes, passes raw device
 pointers, sizes and the current CUDA stream to libpa.so, and raises PAError on
-a non-zero status.  The append and the 4-bit cache's calls are marshalled by an
-extension module (csrc/pa_call.cpp), the others here through ctypes.  Nothing is
+a non-zero status.  The appends, the 4-bit cache's calls and the prefill over
+quantized caches are marshalled by an extension module (csrc/pa_call.cpp), the
+others here through ctypes.  Nothing is
 computed here.
 """
 import ctypes
@@ -11,8 +12,8 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import (PA_BF16, PA_DECODE_AUTO, PA_F16, PA_FP4_E2M1, PA_FP8_E4M3, PA_SWAP_IN,
-                   PA_SWAP_OUT)
+from ._lib import (PA_BF16, PA_DECODE_AUTO, PA_F16, PA_FP4_E2M1, PA_FP8_E4M3,
+                   PA_PREFILL_QUANT_COUNTERS, PA_SWAP_IN, PA_SWAP_OUT)
 
 
 class PAError(RuntimeError):
@@ -421,6 +422,27 @@ def pa_append_rope(q, k, v, cos_sin, block_tables, token_seq, token_pos, k_cache
     return q_out
 
 
+def pa_append_rope_axes(q, k, v, cos_sin, axis_of, rot_pos, block_tables, token_seq, token_pos,
+                        k_cache, v_cache, interleaved=False, q_norm=None, k_norm=None, eps=1e-6,
+                        k_scale=1.0, v_scale=1.0, q_out=None, slot_mapping=None, err=None):
+    """pa_append_rope for tokens whose position has several axes: frequency i takes
+    its angle from row rot_pos[axis_of[i], token] of cos_sin.
+
+    axis_of: uint8 [rotary_dim / 2], the axis of every frequency; rot_pos: int32
+    [num_axes, num_tokens], 1 to 4 axes, the positions that select angles.
+    token_pos places the token in the cache alone.  Everything else is as for
+    pa_append_rope, to which the call is equal bit for bit when every row of
+    rot_pos is token_pos."""
+    if q_out is None and q is not None:
+        q_out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    status = (_call or _calls()).append_rope_axes(
+        q, k, v, cos_sin, axis_of, rot_pos, block_tables, token_seq, token_pos, k_cache, v_cache,
+        interleaved, q_norm, k_norm, eps, k_scale, v_scale, q_out, slot_mapping, err)
+    if status:
+        raise PAError(status, "pa_append_rope_axes")
+    return q_out
+
+
 def pa_cache_write_fp4(k, v, slot_mapping, k_cache, v_cache, k_scale, v_scale, err=None):
     """Quantize k[n], v[n] ([n_tok, H_kv, D], float16 / bfloat16) to E2M1 codes
     with an E4M3 scale per 16 head_dim values (value = code * scale16 * scale)
@@ -512,6 +534,63 @@ def pa_prefill(q, k_cache, v_cache, block_tables, seq_lens, query_start, scale, 
                         block_tables.shape[1], _ptr(seq_lens), _ptr(query_start), N, total, Hq, H,
                         D, B, nb, _dtype_code(q), float(scale), _ptr(out), _ptr(workspace),
                         workspace.numel(), _ptr(err), _stream()), "pa_prefill")
+    return out
+
+
+def pa_prefill_quant_workspace_size(num_q_heads, num_kv_heads, head_dim):
+    """Bytes of workspace that pa_prefill_fp8 and pa_prefill_fp4 need for this
+    shape on the current device; the first PA_PREFILL_QUANT_COUNTERS of them
+    must be zero before its first use."""
+    n = ctypes.c_size_t(0)
+    _check(_lib.load().pa_prefill_quant_workspace_size(num_q_heads, num_kv_heads, head_dim,
+                                                       ctypes.byref(n)),
+           "pa_prefill_quant_workspace_size")
+    return n.value
+
+
+def _quant_workspace(num_q_heads, num_kv_heads, head_dim, device):
+    ws = torch.empty(pa_prefill_quant_workspace_size(num_q_heads, num_kv_heads, head_dim),
+                     dtype=torch.uint8, device=device)
+    ws[:PA_PREFILL_QUANT_COUNTERS].zero_()
+    return ws
+
+
+def pa_prefill_fp8(q, k_cache, v_cache, block_tables, seq_lens, query_start, scale, k_scale,
+                   v_scale, window=0, out=None, workspace=None, err=None):
+    """Multi-query paged attention (chunks of new tokens, single tokens allowed)
+    over uint8 E4M3 pools [num_blocks, B, H_kv, D] (value = code * scale): q
+    [total_q, Hq, D]; sequence i's new tokens are rows [query_start[i],
+    query_start[i+1]), already written at the end of its seq_lens[i] tokens.
+    window >= 1: position p attends to tokens [max(0, p - window + 1), p]; 0: to
+    [0, p].  Rows of no sequence keep what out held (zeros when it is made
+    here)."""
+    if out is None:
+        out = torch.zeros_like(q)
+    if workspace is None:
+        _, _, H, D = _fp8_pools(k_cache, v_cache)
+        workspace = _quant_workspace(q.shape[1], H, D, q.device)
+    status = (_call or _calls()).prefill_fp8(q, k_cache, v_cache, block_tables, seq_lens,
+                                             query_start, scale, k_scale, v_scale, window, out,
+                                             workspace, err)
+    if status:
+        raise PAError(status, "pa_prefill_fp8")
+    return out
+
+
+def pa_prefill_fp4(q, k_cache, v_cache, block_tables, seq_lens, query_start, scale, k_scale,
+                   v_scale, window=0, out=None, workspace=None, err=None):
+    """pa_prefill_fp8 over 4-bit pools (pa_fp4_pool_shape; value = code * scale16 *
+    scale)."""
+    if out is None:
+        out = torch.zeros_like(q)
+    if workspace is None:
+        _, H, D = _fp4_pools(k_cache, v_cache)
+        workspace = _quant_workspace(q.shape[1], H, D, q.device)
+    status = (_call or _calls()).prefill_fp4(q, k_cache, v_cache, block_tables, seq_lens,
+                                             query_start, scale, k_scale, v_scale, window, out,
+                                             workspace, err)
+    if status:
+        raise PAError(status, "pa_prefill_fp4")
     return out
 
 
