@@ -13,19 +13,20 @@
 // bits, E2M1 times its scale 6), so the products run on the fifth-generation
 // tensor cores in binary16 with fp32 sums in tensor memory.
 //
-// Roles of a block of 16 warps, one block an SM:
-//  * warps 8-11 (loaders) walk the block's share of the work.  A thread copies
-//    4 rows x 16 elements of K and of V of a stage of 64 keys to shared memory
-//    as they lie in the pool (asynchronous copies into a ring that only the
-//    copying thread reads, so no barrier), converts them some stages later, and
-//    stores them as 16-bit operands with the 128-byte swizzle.  At a part's
-//    start they bring its query rows in, as binary16.
-//  * warps 12 and 13 (one thread each, a tile each): S = Q K^T of a stage.
+// Roles of a block of 20 warps, one block an SM:
+//  * warp 19 (copies) walks the block's share of the work. For every stage of 64
+//    keys it fetches the codes as they lie in the pool into a ring in shared
+//    memory, by bulk copies (4-bit: a plane, or its rows, is contiguous) or TMA
+//    boxes (E4M3: a block's rows of a head), and writes the stage's tag.
+//  * warps 8-11 and 12-15 (conversion), a warpgroup a stage in turn, turn the
+//    codes into 16-bit operands with the 128-byte swizzle.  With a part's first
+//    stage they bring its query rows in, as binary16.
+//  * warps 16 and 17 (one thread each, a tile each): S = Q K^T of a stage.
 //  * warps 0-3 (tile A) and 4-7 (tile B): thread r owns row r, tensor memory
 //    lane r.  It reads its scores, masks them, writes P = 2^(s - m) and keeps
 //    the row's sum; m moves only when a weight would pass 2^kTop, and then the
 //    row of O is rescaled in tensor memory.
-//  * warp 14 (one thread, both tiles): O += P V, P from tensor memory.
+//  * warp 18 (one thread, both tiles): O += P V, P from tensor memory.
 // A pair without a second tile gives its stages to the tiles in turn: both hold
 // the same rows and end with partial results, which tile A's warps join.
 //
@@ -48,11 +49,11 @@ namespace pa {
 namespace {
 
 constexpr int kKeys = 64;                 // of a stage
-constexpr int kLoaders = 8;               // first loader warp
-constexpr int kScore = 12;                // warps 12 and 13
-constexpr int kPv = 14;
-constexpr int kAlloc = 15;
-constexpr int kThreads = 512;
+constexpr int kConvert = 8;               // first conversion warp
+constexpr int kScore = 16;                // warps 16 and 17
+constexpr int kPv = 18;
+constexpr int kCopy = 19;
+constexpr int kThreads = 640;
 constexpr int kMaxGrid = 256;
 // A pair's start and end cost what this many tokens do.
 constexpr int kStart = 128;
@@ -62,9 +63,11 @@ constexpr int kLeast = 384;
 // until a weight would pass 2^kTop: binary16 holds weights down to 2^-14 - kShift
 // of the maximum with all their bits.
 constexpr float kShift = 7.f, kTop = 15.f, kTopPow = 32768.f;
-// Registers of the roles: softmax, loaders, the others (sum 4 x 128 a thread).
-constexpr int kRegsSoftmax = 168, kRegsLoad = 120, kRegsOther = 56;
-static_assert(2 * kRegsSoftmax + kRegsLoad + kRegsOther == 4 * 128, "the launch's registers");
+// Registers of the roles: softmax, conversion, the others (5 x 96 a thread).
+constexpr int kRegsLaunch = 96;
+constexpr int kRegsSoftmax = 144, kRegsConvert = 72, kRegsOther = 48;
+static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsOther == 5 * kRegsLaunch,
+              "the launch's registers");
 
 struct Args {
   const uint16_t* q;
@@ -86,16 +89,14 @@ constexpr int kTileRows = 128;
 // o[128][D], m[128], l[128]
 __host__ __device__ constexpr size_t rec_floats(int D) { return (size_t)kTileRows * (D + 2); }
 
-// A stage as it lies in the pool: units of 4 rows x 16 elements, kPiece bytes a
-// row, and for 4-bit pools the unit's four scales.
+// A stage as it lies in the pool: K, then V, 64 rows each; 4-bit planes of
+// min(B, 64) rows with their scales, E4M3 rows one after the other.
 template <int D, bool kFour>
 struct Raw {
-  static constexpr int kGroups = D / 16;
-  static constexpr int kUnits = (kKeys / 4) * kGroups;
-  static constexpr int kPiece = kFour ? 8 : 16;
-  static constexpr int kHalf = 4 * kUnits * kPiece + (kFour ? 4 * kUnits : 0);   // K, then V
+  static constexpr int kRowBytes = kFour ? fp4_row_bytes(D) : D;
+  static constexpr int kHalf = kKeys * kRowBytes;
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kRing = D == 64 ? 6 : (kFour ? 5 : 3);   // stages in flight
+  static constexpr int kRing = D == 64 ? 6 : (kFour ? 5 : 3);      // stages in flight
 };
 
 template <int D>
@@ -113,24 +114,39 @@ struct Tiles {
 enum : int {
   kStop = 1, kFirst = 2, kLast = 4, kActA = 8, kActB = 16, kFirstA = 32, kFirstB = 64,
   kLastA = 128, kLastB = 256, kAlt = 512, kWholeA = 1024, kWholeB = 2048, kBegins = 4096,
-  kHasB = 8192
+  kHasB = 8192,
+  kEdge = 1 << 15,                // some rows hold no data
+  kMarked = 1 << 16               // some bit of `mask` is set
 };
 
-// What the loaders say about a stage, beside its keys.
+// What is to be known about a stage, beside its keys.
 struct Tag {
-  int flags, kt, h, q0;             // q0: tile A's first q row
-  int ntok_a, ntok_b, p0, lo;       // tokens, tile A's first position, first attended token
-  int nkt_a, nkt, pad0, pad1;       // stages end of tile A, of the pair
+  int flags, kt;
+  uint32_t rows[2];                 // (kEdge) bits of keys: rows that hold data
+  uint32_t mask[4];                 // (kMarked) left out (2 words), NaN value rows (2 words)
+  // of the part, with its first stage
+  int h, q0, p0, lo;                // q0: tile A's first q row; p0: its position; lo: first
+                                    // attended token
+  int ntok_a, ntok_b, nkt_a, nkt;   // tokens of the tiles, ends of their stages
   long long i0, len;                // the pair's place on the line, its length there
-  uint32_t mask[4];                 // bits of keys: left out (2 words), NaN value rows (2 words)
+  int part, pad[3];                 // its number in this block
 };
 
-template <int S>
+// The query tiles hold one part's rows.  Part n may be loaded once part n - 1 has
+// been read, which is phase (n - 1) / kQueries of a barrier of its own: the two
+// conversion warpgroups do not see every part, and a wait on a barrier's parity
+// must not be more than one phase behind it or ahead of it.
+constexpr int kQueries = 16;
+
+template <int S, int kRing>
 struct Control {
-  unsigned long long full[S], empty[S], seen[S];
-  unsigned long long qempty, bdone, done[3];
+  // a stage's tag lives from its copies to its last reader
+  static constexpr int kTags = S + kRing;
+  static_assert(kRing >= 2 && S >= 2 && kQueries > 2 * S, "the barriers' parities");
+  unsigned long long full[S], empty[S], rfull[kRing], rempty[kRing];
+  unsigned long long qempty[kQueries], bdone, done[3];
   unsigned long long tile[2][8];    // s full, s free, p full[2], p empty[2], o free
-  alignas(16) Tag tag[S];
+  alignas(16) Tag tag[kTags];
   float factor[S][2][kTileRows];    // of a part's rows: what scores are multiplied by
   float ml[kTileRows][2];           // tile B's m and l, of a pair in turn
   volatile uint32_t pvq[2][8];      // records of products to issue: ring[4], tail, head, fin
@@ -149,7 +165,7 @@ enum : int { kSFull = 0, kSFree = 1, kPFull = 2, kPEmpty = 4, kOFree = 6 };
 template <int D, bool kFour>
 constexpr size_t smem_bytes() {
   return 1024 + Tiles<D>::kStages * Tiles<D>::kStage + 2 * Tiles<D>::kQTile +
-         Raw<D, kFour>::kRing * Raw<D, kFour>::kStage + sizeof(Control<Tiles<D>::kStages>);
+         Raw<D, kFour>::kRing * Raw<D, kFour>::kStage + sizeof(Control<Tiles<D>::kStages, Raw<D, kFour>::kRing>);
 }
 
 // D[tmem] (+)= A . B with A in tensor memory (M rows in lanes, K along columns,
@@ -162,31 +178,14 @@ __device__ __forceinline__ void umma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u));
 }
 
-// kBytes from global to shared memory; `on` false fills with zeros instead
-template <int kBytes>
-__device__ __forceinline__ void copy_piece(uint32_t dst, const uint8_t* src, bool on) {
-  const int n = on ? kBytes : 0;
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
-                 : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src),
-                 "n"(kBytes), "r"(n)
-                 : "memory");
-}
-__device__ __forceinline__ void commit_copies() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int kPending>
-__device__ __forceinline__ void wait_copies() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
-}
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 r;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "r"(addr));
-  return r;
+// a box of a 4-D tensor map into shared memory
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ uint2 lds8(uint32_t addr) {
   uint2 r;
@@ -311,7 +310,7 @@ struct Walk {
     done = false;
     int r = 0;   // the last run that starts at or before u0
 #pragma unroll
-    for (int b = kThreads / 2; b > 0; b >>= 1)
+    for (int b = 512; b > 0; b >>= 1)
       if (r + b < kThreads && run_pref[r + b] <= u0) r += b;
     long long rem = u0 - run_pref[r], one = 0;
     i = r * per;
@@ -342,7 +341,9 @@ struct Walk {
 };
 
 template <int D, bool kBF16, bool kFour>
-__global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a) {
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_quant_kernel(const __grid_constant__ CUtensorMap tmk,
+                         const __grid_constant__ CUtensorMap tmv, const Args a) {
   using R = Raw<D, kFour>;
   using X = Tiles<D>;
   constexpr int S = X::kStages;
@@ -351,16 +352,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
   const uint32_t stages = (raw0 + 1023u) & ~1023u;
   const uint32_t qtiles = stages + S * X::kStage;
   const uint32_t ring = qtiles + 2 * X::kQTile;
-  Control<S>& c = *reinterpret_cast<Control<S>*>(smem_raw + (ring - raw0) + R::kRing * R::kStage);
+  using C = Control<S, R::kRing>;
+  C& c = *reinterpret_cast<C*>(smem_raw + (ring - raw0) + R::kRing * R::kStage);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&c.full[s]), 128);      // the loaders' threads
-      mbar_init(smem_u32(&c.empty[s]), 4);       // per tile: a K share, a V share
-      mbar_init(smem_u32(&c.seen[s]), 8);        // a softmax warp each
+      mbar_init(smem_u32(&c.full[s]), 128);      // a conversion warpgroup's threads
+      // per tile a K share and a V share; every softmax warp once it has read
+      // the tag, so that none waits on a stage that is refilled already
+      mbar_init(smem_u32(&c.empty[s]), 4 + 8);
     }
-    mbar_init(smem_u32(&c.qempty), 2);           // a commit of each score issuer
+    for (int s = 0; s < R::kRing; ++s) {
+      mbar_init(smem_u32(&c.rfull[s]), 1);       // the copy warp's expect-tx
+      mbar_init(smem_u32(&c.rempty[s]), 4);      // a conversion warp each
+    }
+    for (int k = 0; k < kQueries; ++k)
+      mbar_init(smem_u32(&c.qempty[k]), 2);      // a commit of each score issuer
     mbar_init(smem_u32(&c.bdone), 128);          // tile B's threads
     for (int k = 0; k < 3; ++k) mbar_init(smem_u32(&c.done[k]), 1);
     for (int t = 0; t < 2; ++t) {
@@ -420,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
   const long long nb = min((long long)gridDim.x, (total + kLeast - 1) / kLeast);
   if ((long long)blockIdx.x >= nb) return;
   if (tid <= nb) c.bound[tid] = total * tid / nb;
-  if (warp == kAlloc) {
+  if (warp == kCopy) {
     tmem_alloc(smem_u32(&c.tmem), 512);
     tc_fence_before();
   }
@@ -457,14 +465,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
       const uint32_t tcol = tmem + (uint32_t)(256 * t);
       const uint64_t dq[2] = {umma_desc_sw128(qtiles, 16, 1024),
                               umma_desc_sw128(qtiles + (uint32_t)t * X::kQTile, 16, 1024)};
-      int rt = 0, ni = 0, st = 0;   // records pushed (scores issued), parts started, slot
+      int rt = 0, ni = 0;             // records pushed (scores issued), the tile's parts started
+      int st = 0, tg = 0, parts = 0;  // slots, parts walked
       uint32_t ph = 0u;
       bool ok = true;
       long long t_last = clock64();
       while (true) {
         bool progressed = false;
         if (rt - (int)q[5] < 2 && mbar_test(smem_u32(&c.full[st]), ph)) {
-          const int flags = *const_cast<volatile int*>(&c.tag[st].flags);
+          const int flags = *const_cast<volatile int*>(&c.tag[tg].flags);
           if (flags & kStop) break;
           bool ready = true;
           if (flags & act) {
@@ -499,11 +508,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
             mbar_arrive(smem_u32(&c.empty[st]));
           }
           if (ready) {
-            if (flags & kLast) umma_commit(smem_u32(&c.qempty));   // the queries are read
+            if (flags & kLast)   // the queries are read
+              umma_commit(smem_u32(&c.qempty[parts++ % kQueries]));
             if (++st == S) {
               st = 0;
               ph ^= 1u;
             }
+            if (++tg == C::kTags) tg = 0;
             progressed = true;
           }
         }
@@ -574,286 +585,365 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
       if (!ok) give_up();
       umma_commit(smem_u32(&c.done[2]));
       mbar_wait_bounded(smem_u32(&c.done[2]), 0u, nullptr);
+    } else if (warp == kCopy) {
+      // ===================== copies and tags =====================
+      const int B = 1 << a.log2B;
+      const int bs = min(B, kKeys), nblk = kKeys / bs;   // rows of a piece, pieces of a stage
+      const int kv = lane / nblk, b = lane & (nblk - 1); // this lane's: K's or V's piece b
+      const uint32_t piece = (uint32_t)(bs * R::kRowBytes);
+      const uint8_t* const pool = kv ? a.vc : a.kc;
+      const uint32_t dst0 = ring + (uint32_t)(kv * R::kHalf) + (uint32_t)b * piece;
+      Walk w;
+      w.start(a, c.run_pref, per, c.bound[blockIdx.x], c.bound[blockIdx.x + 1]);
+      // the block of this lane's piece; -2: no row of it is attended to
+      auto entry = [&]() -> int {
+        const int t = w.k * kKeys + b * bs;
+        if (kv >= 2 || w.done || t + bs - 1 < w.lo || t >= w.end) return -2;
+        return __ldg(a.bt + (size_t)w.i * a.stride + (t >> a.log2B));
+      };
+      int next = entry();
+      int rs = 0, tg = 0, parts = 0, part = 0, nkt_a = 0, stops = 0;
+      int flying = 0;   // slots whose copies may be in flight
+      uint32_t ph = 0u;
+      while (stops < 2) {   // a last tag for each conversion warpgroup
+        if (!wait_warp(c.rempty[rs], ph ^ 1u)) {
+          if (lane == 0) give_up();
+          break;
+        }
+        Tag& t = c.tag[tg];
+        const uint32_t bar = smem_u32(&c.rfull[rs]);
+        if (w.done) {
+          if (lane == 0) {
+            t.flags = kStop;
+            mbar_arrive(bar);
+          }
+          ++stops;
+        } else {
+          const int ent = next;
+          const int t0 = w.k * kKeys;
+          bool on = ent != -2;
+          if (on && (ent < 0 || (long long)ent >= a.num_blocks)) {
+            set_error(a.err, PA_DEVERR_BLOCK_ID);
+            on = false;
+          }
+          const uint32_t got = __ballot_sync(0xffffffffu, on);
+          const int n = w.k1 - w.k0, i = w.k - w.k0;
+          if (i == 0) {
+            const long long w2 = 2 * a.BM;
+            const int left = (int)min((long long)w.L - w2 * w.pr, w2);   // the pair's tokens
+            const int ntok_a = min(left, a.BM), ntok_b = left - ntok_a;
+            const int nkt = w.nkt(), klo = w.lo / kKeys;
+            const int p0 = w.T - w.L + (int)(w2 * w.pr);
+            nkt_a = ntok_b == 0 ? nkt : (p0 + ntok_a - 1) / kKeys + 1;
+            part = (ntok_b == 0 ? kAlt | (n >= 2 ? kHasB : 0) : 0) | (w.k0 == klo ? kBegins : 0) |
+                   (w.k0 == klo && w.k1 >= nkt_a ? kWholeA : 0) |
+                   (w.k0 == klo && w.k1 == nkt ? kWholeB : 0);
+
+            if (lane == 0) {
+              t.part = parts;
+              t.h = w.h;
+              t.q0 = w.q0 + (int)(w2 * w.pr);
+              t.p0 = p0;
+              t.lo = w.lo;
+              t.ntok_a = ntok_a;
+              t.ntok_b = ntok_b;
+              t.nkt_a = nkt_a;
+              t.nkt = nkt;
+              t.i0 = w.i0;
+              t.len = w.length();
+            }
+            ++parts;
+          }
+          int f = part | (i == 0 ? kFirst | kFirstA : 0) | (i == n - 1 ? kLast : 0);
+          if (part & kAlt) {
+            f |= (i & 1) ? kActB : kActA;
+            if (i == 1) f |= kFirstB;
+            if (i + 2 >= n) f |= (i & 1) ? kLastB : kLastA;
+          } else {
+            f |= kActB | (w.k < nkt_a ? kActA : 0) | (i == 0 ? kFirstB : 0) |
+                 (i == n - 1 ? kLastB : 0) | (w.k == min(w.k1, nkt_a) - 1 ? kLastA : 0);
+          }
+          if (t0 + kKeys > w.end || __popc(got) != 2 * nblk) {
+            // rows that hold data, and rows of blocks that are out of range
+            const uint64_t mine = (bs == 64 ? ~0ull : (1ull << bs) - 1ull) << (b * bs);
+            uint64_t rows = on ? mine : 0ull, bad = ent != -2 && !on ? mine : 0ull;
+            const int live = w.end - t0;   // keys before the pair's end
+            if (live < kKeys) {
+              rows &= (1ull << live) - 1ull;
+              bad &= (1ull << live) - 1ull;
+            }
+            const uint32_t r0 = __reduce_or_sync(0xffffffffu, (uint32_t)rows);
+            const uint32_t r1 = __reduce_or_sync(0xffffffffu, (uint32_t)(rows >> 32));
+            const uint32_t b0 = __reduce_or_sync(0xffffffffu, (uint32_t)bad);
+            const uint32_t b1 = __reduce_or_sync(0xffffffffu, (uint32_t)(bad >> 32));
+            f |= kEdge | ((b0 | b1) ? kMarked : 0);
+            if (lane == 0) {
+              t.rows[0] = r0;
+              t.rows[1] = r1;
+              t.mask[0] = b0;
+              t.mask[1] = b1;
+            }
+          } else if (lane == 0) {
+            t.mask[0] = t.mask[1] = 0u;
+          }
+          if (lane == 0) {
+            t.mask[2] = t.mask[3] = 0u;
+            t.flags = f;
+            t.kt = w.k;
+            mbar_arrive_expect_tx(bar, (uint32_t)__popc(got) * piece);
+          }
+          __syncwarp();
+          if (on) {
+            const uint32_t dst = dst0 + (uint32_t)(rs * R::kStage);
+            const int r = (t0 + b * bs) & (B - 1);
+            if constexpr (kFour) {
+              const uint8_t* const plane = pool + fp4_plane(ent, a.H, w.h, B * R::kRowBytes);
+              if (B <= kKeys) {
+                bulk_load(dst, plane, piece, bar);
+              } else {
+                bulk_load(dst, plane + r * (D / 2), kKeys * (D / 2), bar);
+                bulk_load(dst + kKeys * (D / 2), plane + B * (D / 2) + r * (D / 16),
+                          kKeys * (D / 16), bar);
+              }
+            } else {
+              tma_load_4d(dst, kv ? &tmv : &tmk, bar, 0, r, w.h, ent);
+            }
+          }
+          w.advance(a);
+          next = entry();
+          flying = min(flying + 1, R::kRing);
+        }
+        if (++rs == R::kRing) {
+          rs = 0;
+          ph ^= 1u;
+        }
+        if (++tg == C::kTags) tg = 0;
+      }
+      // after an abort no copy may land in shared memory once the block has left
+      if (c.abort) {
+        for (; flying > 0; --flying) {   // the slots before this one in the ring
+          rs = rs == 0 ? R::kRing - 1 : rs - 1;
+          if (rs == R::kRing - 1) ph ^= 1u;
+          mbar_wait_bounded(smem_u32(&c.rfull[rs]), ph, nullptr);
+        }
+      }
     }
     __syncwarp();
-  } else if (warp >= kLoaders) {
-    setmaxnreg_dec<kRegsLoad>();
-    // ========================= loaders =========================
-    const int x = tid - 32 * kLoaders;              // 0 .. 127
-    const int u = x % R::kUnits, part0 = D == 64 ? x / R::kUnits : 0;
-    constexpr int kParts = D == 64 ? 1 : 2;         // of K and V, a thread's
-    const int ua = u / R::kGroups, g = u % R::kGroups;
-    const int B = 1 << a.log2B;
+  } else if (warp >= kConvert) {
+    setmaxnreg_dec<kRegsConvert>();
+    // ========================= conversion =========================
+    const int x = tid & 127;                        // thread of the warpgroup
+    const int w = warp & 3;                         // rows 16 w .. of a stage
+    const int group = (warp - kConvert) >> 2;       // stages group, group + 2, ..
     const int tok_r = x / a.G, head_r = x % a.G;    // of this thread's query row
-    Walk cv;
-    cv.start(a, c.run_pref, per, c.bound[blockIdx.x], c.bound[blockIdx.x + 1]);
-    Walk ld = cv;
-    // the block of this thread's unit of a stage; -2: none of its tokens is
-    // attended to
-    auto entry = [&](const Walk& w) -> int {
-      if (w.done) return -2;
-      const int t = w.k * kKeys + 4 * ua;
-      if (t + 3 < w.lo || t >= w.end) return -2;
-      return __ldg(a.bt + (size_t)w.i * a.stride + (t >> a.log2B));
-    };
-    uint32_t bads = 0;   // a bit per ring slot: the unit's block is out of range
-    auto issue = [&](int slot, int ent) {
-      const int t = ld.k * kKeys + 4 * ua;
-      bool on = ent != -2;
-      bads &= ~(1u << slot);
-      if (on && (ent < 0 || (long long)ent >= a.num_blocks)) {
-        set_error(a.err, PA_DEVERR_BLOCK_ID);
-        bads |= 1u << slot;
-        on = false;
-      }
-      const int e = on ? ent : 0, r = t & (B - 1);
+    const int bs = min(1 << a.log2B, kKeys);
+    // A lane's pieces: 16 bytes of kRows rows, as words (8 codes of 4 bits) or
+    // double words (8 codes of 8 bits), each of which becomes one 16-byte chunk of
+    // the swizzled operand.  A lane takes word j ^ turn as its j-th: `turn` is such
+    // that neither the loads of a warp nor the stores of eight neighbours meet in
+    // a bank (rows lie 16 D / kPieces bytes apart in the ring, and chunk k of an
+    // operand's row r at k ^ r % 8).
+    constexpr int kPieces = kFour ? D / 32 : D / 16;   // of a row
+    constexpr int kRowsStep = 32 / kPieces;            // rows of a warp's load
+    constexpr int kRows = 16 / kRowsStep;
+    constexpr int kWords = kFour ? 4 : 2;
+    const int col = lane % kPieces, rl = lane / kPieces;
+    const int turn = kFour ? (D == 128 ? (((col >> 1) << 1) ^ (rl & 1) ^ (rl & 3) ^ ((rl >> 2) & 1))
+                                       : ((rl >> 2) & 3))
+                           : (D == 128 ? ((col >> 2) ^ (rl & 1)) : ((rl >> 1) & 1));
+    uint32_t from[kRows], scales[kFour ? kRows : 1], chunk[kWords];
 #pragma unroll
-      for (int p = 0; p < kParts; ++p) {
-        const int kv = part0 + p;
-        const uint8_t* const pool = kv ? a.vc : a.kc;
-        const uint32_t dst = ring + (uint32_t)(slot * R::kStage + kv * R::kHalf + u * R::kPiece);
-        if constexpr (kFour) {
-          const uint8_t* const plane =
-              pool + fp4_plane(e, a.H, on ? ld.h : 0, B * fp4_row_bytes(D));
-          const uint8_t* const src = on ? plane + r * (D / 2) + 8 * g : pool;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            copy_piece<8>(dst + i * (R::kUnits * 8), on ? src + i * (D / 2) : pool,
-                          on && t + i < ld.end);
-          copy_piece<4>(ring + (uint32_t)(slot * R::kStage + kv * R::kHalf + 32 * R::kUnits + 4 * u),
-                        on ? plane + fp4_scale_off<D>(B, r, g) : pool, on);
-        } else {
-          const size_t row = (size_t)a.H * D;
-          const uint8_t* const src =
-              on ? pool + ((size_t)e * B + r) * row + (size_t)ld.h * D + 16 * g : pool;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            copy_piece<16>(dst + i * (R::kUnits * 16), on ? src + i * row : pool,
-                           on && t + i < ld.end);
-        }
-      }
-      ld.advance(a);
-    };
-    {
-      int ents[R::kRing];
-      Walk w = cv;
-#pragma unroll
-      for (int n = 0; n < R::kRing; ++n) {
-        ents[n] = entry(w);
-        if (!w.done) w.advance(a);
-      }
-#pragma unroll
-      for (int n = 0; n < R::kRing; ++n) {
-        if (!ld.done) issue(n, ents[n]);
-        commit_copies();   // a group a stage, issued or not
-      }
+    for (int i = 0; i < kRows; ++i) {
+      const int row = 16 * w + rl + kRowsStep * i, blk = row / bs, rr = row % bs;
+      from[i] = ring + (uint32_t)(blk * bs * R::kRowBytes + rr * (kFour ? D / 2 : D) + 16 * col +
+                                  (16 / kWords) * turn);
+      if constexpr (kFour)
+        scales[i] = ring + (uint32_t)(blk * bs * R::kRowBytes + bs * (D / 2) + (rr >> 2) * (D / 4) +
+                                      8 * col);
     }
-    int ent = entry(ld);
-    int st = 0, slot = 0, parts = 0;
-    uint32_t ph = 0u;
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) {
+      const int k = kWords * col + (j ^ turn);   // 8 columns of the row
+      chunk[j] = stages + (uint32_t)(k >> 3) * X::kPlane + (uint32_t)(16 * w + rl) * 128u +
+                 (uint32_t)((k ^ rl) & 7) * 16u;
+    }
+    // the two scale bytes of a row's piece, the first for the lane's first words
+    const uint32_t pick = (uint32_t)(((turn & 2) ? 0x04 : 0x40) + 0x11 * (rl & 3));
+    int st = group, rs = group, tg = group;
+    uint32_t ph = 0u, rph = 0u;
     bool ok = true;
-    while (!cv.done) {
-      ok = wait_warp(c.empty[st], ph ^ 1u) && wait_warp(c.seen[st], ph ^ 1u);
-      const bool first = cv.k == cv.k0;
-      const long long w2 = 2 * a.BM;
-      const int left = (int)min((long long)cv.L - w2 * cv.pr, w2);   // the pair's tokens
-      const int ntok_a = min(left, a.BM), ntok_b = left - ntok_a;
-      const int q0 = cv.q0 + (int)(w2 * cv.pr);
-      if (ok && first) {
-        ok = wait_warp(c.qempty, ((uint32_t)parts & 1u) ^ 1u);
-        ++parts;
-        if (ok) {
-          // ---- query rows: thread x row x of a tile, as binary16.  A bfloat16
-          // row is brought into binary16's range by a power of two (its largest
-          // magnitude into [1, 2)), which its score factor takes back; elements
-          // 2^-14 below the largest lose bits below 2^-24 of it.
-#pragma unroll 1
-          for (int t = 0; t < (ntok_b > 0 ? 2 : 1); ++t) {
-            const bool valid = x < a.BM * a.G && tok_r < (t ? ntok_b : ntok_a);
-            uint32_t w[D / 2];
-            const uint4* src = reinterpret_cast<const uint4*>(
-                a.q + ((size_t)(valid ? q0 + t * a.BM + tok_r : 0) * a.Hq +
-                       (valid ? cv.h * a.G + head_r : 0)) * D);
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j) {
-              const uint4 y = valid ? __ldg(src + j) : make_uint4(0u, 0u, 0u, 0u);
-              w[4 * j] = y.x; w[4 * j + 1] = y.y; w[4 * j + 2] = y.z; w[4 * j + 3] = y.w;
-            }
-            float back = 1.f;
-            if constexpr (kBF16) {
-              float mx = 0.f;
-#pragma unroll
-              for (int j = 0; j < D / 2; ++j) {
-                const float2 f = unpack2<true>(w[j]);
-                mx = max3f(mx, fabsf(f.x), fabsf(f.y));
-              }
-              // 2^e <= mx < 2^(e+1); zero, subnormal or infinite maxima keep a
-              // factor whose inverse is a normal number
-              const int e = min(max((int)(__float_as_uint(mx) >> 23), 1), 253);
-              back = __uint_as_float((uint32_t)e << 23);
-              const float to = __uint_as_float((uint32_t)(254 - e) << 23);
-#pragma unroll
-              for (int j = 0; j < D / 2; ++j) {
-                const float2 f = unpack2<true>(w[j]);
-                w[j] = pack2<false>(f.x * to, f.y * to);
-              }
-            }
-            const uint32_t dst = qtiles + (uint32_t)t * X::kQTile + (uint32_t)x * 128u;
-#pragma unroll
-            for (int j = 0; j < D / 8; ++j)
-              sts16(dst + (uint32_t)(j >> 3) * X::kQPlane + (uint32_t)((j ^ x) & 7) * 16u,
-                    w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            c.factor[st][t][x] = a.scale_log2 * back;
-          }
-        }
-      }
-      if (!ok) {
-        if (lane == 0) give_up();
+    while (true) {
+      // (in this order: the stage before in this operand slot was converted, so
+      // the copies before in this ring slot have landed)
+      if (!wait_warp(c.empty[st], ph ^ 1u) || !wait_warp(c.rfull[rs], rph)) {
+        ok = false;
         break;
       }
+      Tag& t = c.tag[tg];
+      const int flags = t.flags;
+      if (flags & kStop) {
+        mbar_arrive(smem_u32(&c.full[st]));
+        break;
+      }
+      if (flags & kFirst) {
+        const int before = t.part - 1;
+        if (before >= 0 && !wait_warp(c.qempty[before % kQueries],
+                                      (uint32_t)(before / kQueries) & 1u)) {
+          ok = false;
+          break;
+        }
+        // ---- query rows: thread x row x of a tile, as binary16.  A bfloat16
+        // row is brought into binary16's range by a power of two (its largest
+        // magnitude into [1, 2)), which its score factor takes back; elements
+        // 2^-14 below the largest lose bits below 2^-24 of it.
+#pragma unroll 1
+        for (int k = 0; k < (t.ntok_b > 0 ? 2 : 1); ++k) {
+          const bool valid = x < a.BM * a.G && tok_r < (k ? t.ntok_b : t.ntok_a);
+          const uint4* const src = reinterpret_cast<const uint4*>(
+              a.q + ((size_t)(valid ? t.q0 + k * a.BM + tok_r : 0) * a.Hq +
+                     (valid ? t.h * a.G + head_r : 0)) * D);
+          const uint32_t dst = qtiles + (uint32_t)k * X::kQTile + (uint32_t)x * 128u;
+          float back = 1.f, to = 1.f;
+          if constexpr (kBF16) {
+            float mx = 0.f;
+#pragma unroll
+            for (int j0 = 0; j0 < D / 8; j0 += 8) {
+              uint4 y[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) y[j] = valid ? __ldg(src + j0 + j) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint32_t z[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 f = unpack2<true>(z[e]);
+                  mx = max3f(mx, fabsf(f.x), fabsf(f.y));
+                }
+              }
+            }
+            // 2^e <= mx < 2^(e+1); zero, subnormal or infinite maxima keep a
+            // factor whose inverse is a normal number
+            const int e = min(max((int)(__float_as_uint(mx) >> 23), 1), 253);
+            back = __uint_as_float((uint32_t)e << 23);
+            to = __uint_as_float((uint32_t)(254 - e) << 23);
+          }
+#pragma unroll
+          for (int j0 = 0; j0 < D / 8; j0 += 8) {
+            uint4 y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = valid ? __ldg(src + j0 + j) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t z[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
+              if constexpr (kBF16) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 f = unpack2<true>(z[e]);
+                  z[e] = pack2<false>(f.x * to, f.y * to);
+                }
+              }
+              sts16(dst + (uint32_t)(j0 >> 3) * X::kQPlane + (uint32_t)((j ^ x) & 7) * 16u, z[0],
+                    z[1], z[2], z[3]);
+            }
+          }
+          c.factor[st][k][x] = a.scale_log2 * back;
+        }
+      }
       // ---- the stage's keys and values to 16 bits
-      wait_copies<R::kRing - 1>();
-      const int t0 = cv.k * kKeys + 4 * ua;
-      uint32_t nan = 0u;   // a bit per row of the unit
+      uint32_t live = 0xffffu;   // of the warp's 16 rows
+      if (flags & kEdge) live = t.rows[w >> 1] >> (16 * (w & 1));
+      uint32_t nan = 0u;
+      const uint32_t src = (uint32_t)(rs * R::kStage), to = (uint32_t)st * X::kStage;
 #pragma unroll
-      for (int p = 0; p < kParts; ++p) {
-        const int kv = part0 + p;
-        const uint32_t src = ring + (uint32_t)(slot * R::kStage + kv * R::kHalf + u * R::kPiece);
-        // row r of the unit: chunks 2 g and 2 g + 1 of its 128-byte plane rows.
-        // Lanes of the other plane, or of the next unit of a 64-element row,
-        // store them the other way round: no two lanes of eight share a bank.
-        const uint32_t dst = stages + (uint32_t)st * X::kStage + (uint32_t)kv * X::kPart +
-                             (uint32_t)(g >> 2) * X::kPlane + (uint32_t)(4 * ua) * 128u;
-        const uint32_t turn = D == 128 ? (uint32_t)(g >> 2) : (uint32_t)(ua & 1);
-        uint32_t s01 = 0u, s23 = 0u;
-        if constexpr (kFour) {
-          uint32_t sc = lds4(ring + (uint32_t)(slot * R::kStage + kv * R::kHalf +
-                                               32 * R::kUnits + 4 * u));
-          const int n = cv.end - t0;   // attended tokens of the unit, from its first
-          if (n < 4) sc = n <= 0 ? 0u : sc & ((1u << (8 * n)) - 1u);
-          if (kv == 1) {
-            const uint32_t b = nan_bytes(sc);
-            if (b) {
-              sc &= ~((b >> 7) * 0xffu);
-              nan = ((b >> 7) & 1u) | ((b >> 14) & 2u) | ((b >> 21) & 4u) | ((b >> 28) & 8u);
+      for (int kv = 0; kv < 2; ++kv) {
+        constexpr int kBatch = kRows < 2 ? kRows : 2;   // rows loaded at a time
+#pragma unroll
+        for (int i0 = 0; i0 < kRows; i0 += kBatch) {
+          uint32_t y[kBatch][4];
+          uint32_t sc[kBatch];
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            const uint32_t at = from[i0 + i] + src + kv * R::kHalf;
+            if constexpr (kFour) {
+              const uint2 s2 = lds8(scales[i0 + i] + src + kv * R::kHalf);
+              sc[i] = prmt(s2.x, s2.y, pick) & 0xffffu;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) y[i][j] = lds4(at ^ (uint32_t)(4 * j));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint2 z = lds8(at ^ (uint32_t)(8 * j));
+                y[i][2 * j] = z.x;
+                y[i][2 * j + 1] = z.y;
+              }
             }
           }
-          e4m3x4_to_f16x2x2(sc, s01, s23);
-        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t f[8];
-          if constexpr (kFour) {
-            const uint2 w = lds8(src + i * (R::kUnits * 8));
-            uint32_t lo[4], hi[4];
-            e2m1x8_to_f16x2(w.x, lo);
-            e2m1x8_to_f16x2(w.y, hi);
-            const uint32_t s = i < 2 ? s01 : s23;
+          for (int i = 0; i < kBatch; ++i) {
+            const int rr = rl + kRowsStep * (i0 + i);   // of the warp's rows
+            const bool in = ((live >> rr) & 1u) != 0u;
+            const uint32_t up = to + kv * X::kPart + (uint32_t)(kRowsStep * (i0 + i)) * 128u;
+            // rows 4 apart swap halves of the swizzle
+            const uint32_t flip = (kRowsStep * (i0 + i)) & 4 ? 64u : 0u;
+            if constexpr (kFour) {
+              if (!in) sc[i] = 0u;
+              if (kv == 1 && nan_bytes(sc[i])) {
+                nan |= 1u << rr;
+                sc[i] = 0u;
+              }
+              const uint32_t s = e4m3x2_to_f16x2(sc[i]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              f[e] = (i & 1) ? hmul2_hi(lo[e], s) : hmul2_lo(lo[e], s);
-              f[4 + e] = (i & 1) ? hmul2_hi(hi[e], s) : hmul2_lo(hi[e], s);
+              for (int j = 0; j < 4; ++j) {
+                uint32_t f[4];
+                e2m1x8_to_f16x2(y[i][j], f);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f[e] = j < 2 ? hmul2_lo(f[e], s) : hmul2_hi(f[e], s);
+                sts16((chunk[j] ^ flip) + up, f[0], f[1], f[2], f[3]);
+              }
+            } else {
+              bool clear = !in;
+              if (kv == 1 && (nan_bytes(y[i][0]) | nan_bytes(y[i][1]) | nan_bytes(y[i][2]) |
+                              nan_bytes(y[i][3]))) {
+                if (in) nan |= 1u << rr;
+                clear = true;
+              }
+              if (clear) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0u;
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                uint32_t f[4];
+                e4m3x4_to_f16x2x2(y[i][2 * j], f[0], f[1]);
+                e4m3x4_to_f16x2x2(y[i][2 * j + 1], f[2], f[3]);
+                sts16((chunk[j] ^ flip) + up, f[0], f[1], f[2], f[3]);
+              }
             }
-          } else {
-            uint4 w = lds16(src + i * (R::kUnits * 16));
-            if (kv == 1 && (nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w))) {
-              nan |= 1u << i;
-              w = make_uint4(0u, 0u, 0u, 0u);
-            }
-            e4m3x4_to_f16x2x2(w.x, f[0], f[1]);
-            e4m3x4_to_f16x2x2(w.y, f[2], f[3]);
-            e4m3x4_to_f16x2x2(w.z, f[4], f[5]);
-            e4m3x4_to_f16x2x2(w.w, f[6], f[7]);
-          }
-          const uint32_t row = dst + (uint32_t)i * 128u;
-          const uint32_t sw = (uint32_t)((4 * ua + i) & 7);
-          const uint32_t ca = row + ((((uint32_t)(2 * g) & 7u) ^ sw) << 4);
-          const uint32_t cb = row + ((((uint32_t)(2 * g + 1) & 7u) ^ sw) << 4);
-          if (turn) {
-            sts16(cb, f[4], f[5], f[6], f[7]);
-            sts16(ca, f[0], f[1], f[2], f[3]);
-          } else {
-            sts16(ca, f[0], f[1], f[2], f[3]);
-            sts16(cb, f[4], f[5], f[6], f[7]);
           }
         }
       }
-      // ---- the stage's tag
-      const uint32_t bad = ((bads >> slot) & 1u) ? 0xfu : 0u;
-      if constexpr (D == 128) {   // a warp's units: 16 rows
-        const int sh = 4 * (ua & 3);
-        const uint32_t m = __reduce_or_sync(0xffffffffu, (bad << sh) | (nan << (16 + sh)));
+      if (__any_sync(0xffffffffu, nan != 0u)) {   // NaN among the values: rare
+        nan = __reduce_or_sync(0xffffffffu, nan);
         if (lane == 0) {
-          uint16_t* const w = reinterpret_cast<uint16_t*>(c.tag[st].mask) + (warp - kLoaders);
-          w[0] = (uint16_t)m;
-          w[4] = (uint16_t)(m >> 16);
+          atomicOr(&t.mask[2 + (w >> 1)], nan << (16 * (w & 1)));
+          atomicOr(&t.flags, kMarked);
         }
-      } else {                    // 32 rows, of V's warps
-        const int sh = 4 * (ua & 7);
-        const uint32_t mb = __reduce_or_sync(0xffffffffu, bad << sh);
-        const uint32_t mn = __reduce_or_sync(0xffffffffu, nan << sh);
-        if (lane == 0 && part0 == 1) {
-          c.tag[st].mask[(warp - kLoaders) & 1] = mb;
-          c.tag[st].mask[2 + ((warp - kLoaders) & 1)] = mn;
-        }
-      }
-      if (x == 0) {
-        const int nkt = cv.nkt(), klo = cv.lo / kKeys, n = cv.k1 - cv.k0, i = cv.k - cv.k0;
-        const bool alt = ntok_b == 0;
-        const int nkt_a = alt ? nkt : (cv.T - cv.L + (int)(w2 * cv.pr) + ntok_a - 1) / kKeys + 1;
-        int f = (first ? kFirst : 0) | (cv.k == cv.k1 - 1 ? kLast : 0) | (alt ? kAlt : 0) |
-                (cv.k0 == klo ? kBegins : 0);
-        if (alt) {
-          f |= (i & 1) ? kActB : kActA;
-          if (i == 0) f |= kFirstA;
-          if (i == 1) f |= kFirstB;
-          if (i == ((n - 1) & ~1)) f |= kLastA;
-          if (n >= 2) f |= kHasB;
-          if (n >= 2 && i == ((n - 2) | 1)) f |= kLastB;
-        } else {
-          f |= kActB | (cv.k < nkt_a ? kActA : 0);
-          if (i == 0) f |= kFirstB | kFirstA;
-          if (cv.k == min(cv.k1, nkt_a) - 1) f |= kLastA;
-          if (i == n - 1) f |= kLastB;
-        }
-        if (cv.k0 == klo && cv.k1 >= nkt_a) f |= kWholeA;
-        if (cv.k0 == klo && cv.k1 == nkt) f |= kWholeB;
-        Tag& tg = c.tag[st];
-        tg.flags = f;
-        tg.kt = cv.k;
-        tg.h = cv.h;
-        tg.q0 = q0;
-        tg.ntok_a = ntok_a;
-        tg.ntok_b = ntok_b;
-        tg.p0 = cv.T - cv.L + (int)(w2 * cv.pr);
-        tg.lo = cv.lo;
-        tg.nkt_a = nkt_a;
-        tg.nkt = nkt;
-        tg.i0 = cv.i0;
-        tg.len = cv.length();
       }
       fence_proxy_async_smem();   // the operands, before the tensor core reads them
       mbar_arrive(smem_u32(&c.full[st]));
-      // ---- the copies of the stage that takes this one's place in the ring
-      if (!ld.done) {
-        issue(slot, ent);
-        ent = entry(ld);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&c.rempty[rs]));
+      rs += 2;
+      if (rs >= R::kRing) {
+        rs -= R::kRing;
+        rph ^= 1u;
       }
-      commit_copies();
-      if (++slot == R::kRing) slot = 0;
-      if (++st == S) {
-        st = 0;
+      st += 2;
+      if (st >= S) {
+        st -= S;
         ph ^= 1u;
       }
-      cv.advance(a);
+      tg += 2;
+      if (tg >= C::kTags) tg -= C::kTags;
     }
-    if (ok && wait_warp(c.empty[st], ph ^ 1u) && wait_warp(c.seen[st], ph ^ 1u)) {
-      if (x == 0) c.tag[st].flags = kStop;
-      mbar_arrive(smem_u32(&c.full[st]));
-    } else if (lane == 0) {
-      give_up();
-    }
-    wait_copies<0>();   // nothing lands in shared memory after the block's end
+    if (!ok && lane == 0) give_up();
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
     // ========================= softmax =========================
@@ -866,24 +956,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
     const int tok_r = r / a.G;
     int ntok = 0, p0 = 0, prow = -1;
     bool busy = false;             // some row of this warp is a row
+    int h = 0, q0 = 0, lo = 0, nkt_t = 0;   // of the part
+    long long i0 = 0, line = 0;
     float factor = 0.f, m_used = -INFINITY, l = 0.f;
     bool poison = false;
     bool ok = true;
-    int st = 0, nt = 0, nb_alt = 0;
+    int st = 0, tgi = 0, nt = 0, nb_alt = 0;
     uint32_t ph = 0u;
     while (true) {
       if (!wait_warp(c.full[st], ph)) {
         ok = false;
         break;
       }
-      const Tag& tg = c.tag[st];
+      const Tag& tg = c.tag[tgi];
       const int flags = tg.flags, kt = tg.kt;
       if (flags & kStop) break;
-      const uint4 mk = *reinterpret_cast<const uint4*>(tg.mask);
-      const int h = tg.h, q0 = tg.q0, tag_lo = tg.lo;
-      const int nkt_t = tile ? tg.nkt : tg.nkt_a;
-      const long long i0 = tg.i0, line = tg.len;
+      uint4 mk = make_uint4(0u, 0u, 0u, 0u);
+      if (flags & kMarked) mk = *reinterpret_cast<const uint4*>(tg.mask);
       if (flags & kFirst) {
+        h = tg.h;
+        q0 = tg.q0;
+        lo = tg.lo;
+        nkt_t = tile ? tg.nkt : tg.nkt_a;
+        i0 = tg.i0;
+        line = tg.len;
         const bool other = tile == 1 && !(flags & kAlt);   // rows of the second tile
         ntok = other ? tg.ntok_b : tg.ntok_a;
         p0 = tg.p0 + (other ? a.BM : 0);
@@ -896,11 +992,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         poison = false;
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&c.seen[st]));   // the tag is read
+      if (lane == 0) mbar_arrive(smem_u32(&c.empty[st]));   // the tag is read
       if (++st == S) {
         st = 0;
         ph ^= 1u;
       }
+      if (++tgi == C::kTags) tgi = 0;
       if (!(flags & act)) continue;
       if (!wait_warp(tb[kSFull], (uint32_t)nt & 1u)) {
         ok = false;
@@ -937,7 +1034,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         // A stage that all rows attend to needs no mask, and once the row has a
         // reference no maximum either: every P is at most their sum, so a sum of
         // at most 2^kTop shows that the reference stays.
-        const bool plain = t0 + kKeys - 1 <= p0 && (mk.x | mk.y | mk.z | mk.w) == 0u &&
+        const bool plain = t0 + kKeys - 1 <= p0 && (flags & kMarked) == 0 &&
                            (a.window == 0 || (long long)t0 > (long long)p0 + ntok - 1 - a.window);
         const bool raw = plain && factor > 0.f;
         const bool guess = raw && m_used != -INFINITY;
@@ -1118,9 +1215,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
                 const int b = b0 + lane;
                 bool in = false, begins = false;
                 if (b <= e) {
-                  const int s0 = stage_at(c.bound[b] - i0, tag_lo, nkt_t);
-                  in = s0 < stage_at(c.bound[b + 1] - i0, tag_lo, nkt_t);
-                  begins = s0 == tag_lo / kKeys;
+                  const int s0 = stage_at(c.bound[b] - i0, lo, nkt_t);
+                  in = s0 < stage_at(c.bound[b + 1] - i0, lo, nkt_t);
+                  begins = s0 == lo / kKeys;
                 }
                 const uint32_t all = __ballot_sync(0xffffffffu, in);
                 if (in) c.parts[tile][n + __popc(all & ((1u << lane) - 1u))] =
@@ -1192,7 +1289,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kAlloc) tmem_dealloc(tmem, 512);
+  if (warp == kCopy) tmem_dealloc(tmem, 512);
 }
 
 inline int check_prefill_shape(int Hq, int H, int D) {
@@ -1214,11 +1311,35 @@ inline size_t prefill_quant_bytes(int D, int grid) {
 }
 static_assert(2 * kMaxGrid * sizeof(uint32_t) <= PA_PREFILL_QUANT_COUNTERS, "two counters a block");
 
+// Boxes of `rows` rows of one head of one block of an E4M3 pool.
+inline int encode_rows8(CUtensorMap* map, const void* pool, int D, int B, int H, long long nb,
+                        int rows) {
+  const EncodeTiledFn fn = encode_tiled_fn();
+  if (!fn) {
+    note_cuda_error(1000, "cuTensorMapEncodeTiled is not available");
+    return PA_ERR_CUDA;
+  }
+  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)B, (cuuint64_t)H, (cuuint64_t)nb};
+  const cuuint64_t strides[3] = {(cuuint64_t)H * D, (cuuint64_t)D, (cuuint64_t)B * H * D};
+  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)rows, 1, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pool), dims,
+                        strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    note_cuda_error(1000 + (int)r, "cuTensorMapEncodeTiled (E4M3 prefill)");
+    return PA_ERR_CUDA;
+  }
+  return PA_OK;
+}
+
 // The kernels' opt-in to their shared memory, once a device.
 constexpr int kMaxDevices = 64;
 
 template <int D, bool kBF16, bool kFour>
-int launch_prefill_quant(const Args& a, int grid, int device, cudaStream_t s) {
+int launch_prefill_quant(const CUtensorMap& tmk, const CUtensorMap& tmv, const Args& a, int grid,
+                         int device, cudaStream_t s) {
   static std::mutex mu;
   static bool ready[kMaxDevices];
   const auto kern = prefill_quant_kernel<D, kBF16, kFour>;
@@ -1233,12 +1354,12 @@ int launch_prefill_quant(const Args& a, int grid, int device, cudaStream_t s) {
       if (!e) e = cudaFuncGetAttributes(&at, kern);
       if (e) return launch_status(e, "cudaFuncSetAttribute (quantized prefill)");
       // the roles re-divide the launch's registers, which the increases wait for
-      if (at.numRegs != 128) return PA_ERR_UNSUPPORTED;
+      if (at.numRegs != kRegsLaunch) return PA_ERR_UNSUPPORTED;
       ready[device] = true;
     }
   }
   clear_stale_error();
-  return launch_status(launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, s, a),
+  return launch_status(launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, s, tmk, tmv, a),
                        "quantized prefill launch");
 }
 
@@ -1299,11 +1420,19 @@ int prefill_quant(const void* q, const void* k_cache, const void* v_cache,
   a.v_scale = v_scale;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = q_dtype == PA_BF16;
+  CUtensorMap tmk{}, tmv{};
+  if (!kFour) {
+    const int rows = block_size < kKeys ? block_size : kKeys;
+    if (int rc = encode_rows8(&tmk, k_cache, head_dim, block_size, num_kv_heads, num_blocks, rows))
+      return rc;
+    if (int rc = encode_rows8(&tmv, v_cache, head_dim, block_size, num_kv_heads, num_blocks, rows))
+      return rc;
+  }
   if (head_dim == 64)
-    return bf16 ? launch_prefill_quant<64, true, kFour>(a, grid, di.device, s)
-                : launch_prefill_quant<64, false, kFour>(a, grid, di.device, s);
-  return bf16 ? launch_prefill_quant<128, true, kFour>(a, grid, di.device, s)
-              : launch_prefill_quant<128, false, kFour>(a, grid, di.device, s);
+    return bf16 ? launch_prefill_quant<64, true, kFour>(tmk, tmv, a, grid, di.device, s)
+                : launch_prefill_quant<64, false, kFour>(tmk, tmv, a, grid, di.device, s);
+  return bf16 ? launch_prefill_quant<128, true, kFour>(tmk, tmv, a, grid, di.device, s)
+              : launch_prefill_quant<128, false, kFour>(tmk, tmv, a, grid, di.device, s);
 }
 
 }  // namespace
