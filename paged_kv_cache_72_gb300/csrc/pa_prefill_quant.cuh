@@ -18,9 +18,9 @@
 //    keys it fetches the codes as they lie in the pool into a ring in shared
 //    memory, by bulk copies (4-bit: a plane, or its rows, is contiguous) or TMA
 //    boxes (E4M3: a block's rows of a head), and writes the stage's tag.
-//  * warps 8-11 and 12-15 (conversion), a warpgroup a stage in turn, turn the
-//    codes into 16-bit operands with the 128-byte swizzle.  With a part's first
-//    stage they bring its query rows in, as binary16.
+//  * warps 8-11 (conversion of K) and 12-15 (of V) turn the codes into 16-bit
+//    operands with the 128-byte swizzle.  With a part's first stage they bring
+//    the query rows of tile A and of tile B in, as binary16.
 //  * warps 16 and 17 (one thread each, a tile each): S = Q K^T of a stage.
 //  * warps 0-3 (tile A) and 4-7 (tile B): thread r owns row r, tensor memory
 //    lane r.  It reads its scores, masks them, writes P = 2^(s - m) and keeps
@@ -124,7 +124,7 @@ struct Tag {
   int flags, kt;
   uint32_t rows[2];                 // (kEdge) bits of keys: rows that hold data
   uint32_t mask[4];                 // (kMarked) left out (2 words), NaN value rows (2 words)
-  // of the part, with its first stage
+  // of the part, with a tile's first stage
   int h, q0, p0, lo;                // q0: tile A's first q row; p0: its position; lo: first
                                     // attended token
   int ntok_a, ntok_b, nkt_a, nkt;   // tokens of the tiles, ends of their stages
@@ -132,28 +132,30 @@ struct Tag {
   int part, pad[3];                 // its number in this block
 };
 
-// The query tiles hold one part's rows.  Part n may be loaded once part n - 1 has
-// been read, which is phase (n - 1) / kQueries of a barrier of its own: the two
-// conversion warpgroups do not see every part, and a wait on a barrier's parity
-// must not be more than one phase behind it or ahead of it.
-constexpr int kQueries = 16;
+constexpr int kShare = 6;   // a tile's arrivals on a stage's `empty`
 
 template <int S, int kRing>
 struct Control {
   // a stage's tag lives from its copies to its last reader
   static constexpr int kTags = S + kRing;
-  static_assert(kRing >= 2 && S >= 2 && kQueries > 2 * S, "the barriers' parities");
+
   unsigned long long full[S], empty[S], rfull[kRing], rempty[kRing];
-  unsigned long long qempty[kQueries], bdone, done[3];
+  unsigned long long qempty, bdone, done[3];
   unsigned long long tile[2][8];    // s full, s free, p full[2], p empty[2], o free
   alignas(16) Tag tag[kTags];
-  float factor[S][2][kTileRows];    // of a part's rows: what scores are multiplied by
+  // of a part's rows: what scores are multiplied by; before the first part, the
+  // line before each thread's run of sequences
+  union {
+    float factor[kTags][2][kTileRows];
+    long long run_pref[kThreads];
+  };
   float ml[kTileRows][2];           // tile B's m and l, of a pair in turn
+  int4 scores[2][4];                // of a tile's score products: flags, stage, slot, tag
   volatile uint32_t pvq[2][8];      // records of products to issue: ring[4], tail, head, fin
-  long long run_pref[kThreads];     // the line before each thread's run of sequences
   long long warp_tot[kThreads / 32];
   long long bound[kMaxGrid + 1];
   uint16_t parts[2][kMaxGrid];      // of a cut tile: its records
+  float join[2][kTileRows][2];      // and its rows' maxima, and factors of the sums
   int nparts[2];
   int last[2];
   uint32_t tmem;
@@ -202,6 +204,16 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
                "r"(d)
                : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
+  asm volatile("{\n\t.reg .b64 s;\n\tmbarrier.arrive.shared::cta.b64 s, [%0], %1;\n\t}" ::"r"(bar),
+               "r"(n)
+               : "memory");
+}
+// once for the warp, behind what its lanes did
+__device__ __forceinline__ void warp_arrive(unsigned long long& bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bar));
 }
 // the 128 threads of a warpgroup
 __device__ __forceinline__ void group_sync(int id) {
@@ -297,11 +309,6 @@ struct Walk {
       P = pairs_of(L, a);
     }
   }
-  __device__ __forceinline__ void advance(const Args& a) {
-    if (++k < k1) return;
-    next_pair(a);
-    settle(a);
-  }
   // to place u0 of the line
   __device__ __forceinline__ void start(const Args& a, const long long* run_pref, int per,
                                         long long from, long long to) {
@@ -358,27 +365,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&c.full[s]), 128);      // a conversion warpgroup's threads
-      // per tile a K share and a V share; every softmax warp once it has read
-      // the tag, so that none waits on a stage that is refilled already
-      mbar_init(smem_u32(&c.empty[s]), 4 + 8);
+      mbar_init(smem_u32(&c.full[s]), 8);        // the conversion warps
+      // per tile: K read, V read, and its four softmax warps have read the tag
+      mbar_init(smem_u32(&c.empty[s]), 2 * kShare);
     }
     for (int s = 0; s < R::kRing; ++s) {
       mbar_init(smem_u32(&c.rfull[s]), 1);       // the copy warp's expect-tx
-      mbar_init(smem_u32(&c.rempty[s]), 4);      // a conversion warp each
+      mbar_init(smem_u32(&c.rempty[s]), 8);      // the same
     }
-    for (int k = 0; k < kQueries; ++k)
-      mbar_init(smem_u32(&c.qempty[k]), 2);      // a commit of each score issuer
-    mbar_init(smem_u32(&c.bdone), 128);          // tile B's threads
+    mbar_init(smem_u32(&c.qempty), 2);           // a commit of each score issuer
+    mbar_init(smem_u32(&c.bdone), 4);            // tile B's warps
     for (int k = 0; k < 3; ++k) mbar_init(smem_u32(&c.done[k]), 1);
     for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&c.tile[t][kSFull]), 1);
-      mbar_init(smem_u32(&c.tile[t][kSFree]), 128);
+      mbar_init(smem_u32(&c.tile[t][kSFull]), 2);        // the product, its record
+      mbar_init(smem_u32(&c.tile[t][kSFree]), 4);        // the tile's warps
       for (int p = 0; p < 2; ++p) {
-        mbar_init(smem_u32(&c.tile[t][kPFull + p]), 128);
+        mbar_init(smem_u32(&c.tile[t][kPFull + p]), 4);  // the same
         mbar_init(smem_u32(&c.tile[t][kPEmpty + p]), 1);
       }
-      mbar_init(smem_u32(&c.tile[t][kOFree]), 128);
+      mbar_init(smem_u32(&c.tile[t][kOFree]), 4);
       for (int w = 0; w < 8; ++w) c.pvq[t][w] = 0u;
     }
     c.abort = 0;
@@ -466,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t dq[2] = {umma_desc_sw128(qtiles, 16, 1024),
                               umma_desc_sw128(qtiles + (uint32_t)t * X::kQTile, 16, 1024)};
       int rt = 0, ni = 0;             // records pushed (scores issued), the tile's parts started
-      int st = 0, tg = 0, parts = 0;  // slots, parts walked
+      int st = 0, tg = 0;             // slots
       uint32_t ph = 0u;
       bool ok = true;
       long long t_last = clock64();
@@ -474,13 +479,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool progressed = false;
         if (rt - (int)q[5] < 2 && mbar_test(smem_u32(&c.full[st]), ph)) {
           const int flags = *const_cast<volatile int*>(&c.tag[tg].flags);
-          if (flags & kStop) break;
           bool ready = true;
-          if (flags & act) {
+          if (flags & (act | kStop)) {
+            // the softmax has read the scores (and their record) before these
             if (rt >= 1) ready = mbar_test(smem_u32(&tb[kSFree]), (uint32_t)(rt - 1) & 1u);
             if (ready && rt >= 2)
               ready = mbar_test(smem_u32(&tb[kPEmpty + (rt & 1)]), (uint32_t)((rt >> 1) - 1) & 1u);
             if (ready) {
+              c.scores[t][rt & 3] = make_int4(flags, c.tag[tg].kt, st, tg);
+              if (flags & kStop) {
+                mbar_arrive_n(smem_u32(&tb[kSFull]), 2);
+                break;
+              }
+              mbar_arrive(smem_u32(&tb[kSFull]));
               tc_fence_after();
               const uint64_t da = dq[(flags & kAlt) ? 0 : 1];
               const uint64_t db = umma_desc_sw128(stages + (uint32_t)st * X::kStage, 16, 1024);
@@ -492,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                          id_s, ks > 0);
               }
               umma_commit(smem_u32(&tb[kSFull]));
-              umma_commit(smem_u32(&c.empty[st]));   // the K share
+              umma_commit(smem_u32(&c.empty[st]));   // K is read
               uint32_t rc = (uint32_t)st;
               if (flags & first) {
                 rc |= 8u;
@@ -503,13 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               __threadfence_block();   // the record before the tail that publishes it
               q[4] = (uint32_t)(++rt);
             }
-          } else {   // not this tile's: both shares
-            umma_commit(smem_u32(&c.empty[st]));
-            mbar_arrive(smem_u32(&c.empty[st]));
+          } else {   // not this tile's
+            mbar_arrive_n(smem_u32(&c.empty[st]), kShare);
           }
           if (ready) {
-            if (flags & kLast)   // the queries are read
-              umma_commit(smem_u32(&c.qempty[parts++ % kQueries]));
+            if (flags & kLast) umma_commit(smem_u32(&c.qempty));   // the queries are read
             if (++st == S) {
               st = 0;
               ph ^= 1u;
@@ -595,17 +604,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t dst0 = ring + (uint32_t)(kv * R::kHalf) + (uint32_t)b * piece;
       Walk w;
       w.start(a, c.run_pref, per, c.bound[blockIdx.x], c.bound[blockIdx.x + 1]);
-      // the block of this lane's piece; -2: no row of it is attended to
-      auto entry = [&]() -> int {
-        const int t = w.k * kKeys + b * bs;
-        if (kv >= 2 || w.done || t + bs - 1 < w.lo || t >= w.end) return -2;
-        return __ldg(a.bt + (size_t)w.i * a.stride + (t >> a.log2B));
+      // 64 entries of the sequence's table from a multiple of 32 on, a pair a lane,
+      // so that no stage waits for its own; blocks without an attended token are
+      // not looked up
+      int win = 0, near = -1, far = -1;
+      auto look = [&](int at) -> int {
+        const int idx = at + lane;
+        return !w.done && idx >= (w.lo >> a.log2B) && idx <= ((w.end - 1) >> a.log2B)
+                   ? __ldg(a.bt + (size_t)w.i * a.stride + idx) : -1;
       };
-      int next = entry();
-      int rs = 0, tg = 0, parts = 0, part = 0, nkt_a = 0, stops = 0;
+      auto open = [&]() {
+        win = ((w.k * kKeys) >> a.log2B) & ~31;
+        near = look(win);
+        far = look(win + 32);
+      };
+      open();
+      int rs = 0, tg = 0, parts = 0, part = 0, nkt_a = 0;
       int flying = 0;   // slots whose copies may be in flight
       uint32_t ph = 0u;
-      while (stops < 2) {   // a last tag for each conversion warpgroup
+      while (true) {
         if (!wait_warp(c.rempty[rs], ph ^ 1u)) {
           if (lane == 0) give_up();
           break;
@@ -617,15 +634,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             t.flags = kStop;
             mbar_arrive(bar);
           }
-          ++stops;
+          break;
         } else {
-          const int ent = next;
-          const int t0 = w.k * kKeys;
-          bool on = ent != -2;
-          if (on && (ent < 0 || (long long)ent >= a.num_blocks)) {
-            set_error(a.err, PA_DEVERR_BLOCK_ID);
-            on = false;
+          const int t0 = w.k * kKeys, idx0 = t0 >> a.log2B;
+          if (idx0 - win >= 32) {
+            win += 32;
+            near = far;
+            far = look(win + 32);
           }
+          const int ent = __shfl_sync(0xffffffffu, near, (idx0 + ((b * bs) >> a.log2B)) & 31);
+          // some row of this lane's piece is attended to, and its block is there
+          const bool want = kv < 2 && t0 + b * bs + bs - 1 >= w.lo && t0 + b * bs < w.end;
+          const bool on = want && ent >= 0 && (long long)ent < a.num_blocks;
+          if (want && !on) set_error(a.err, PA_DEVERR_BLOCK_ID);
           const uint32_t got = __ballot_sync(0xffffffffu, on);
           const int n = w.k1 - w.k0, i = w.k - w.k0;
           if (i == 0) {
@@ -653,6 +674,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               t.len = w.length();
             }
             ++parts;
+          } else if (i == 1 && (part & kAlt) && lane == 0) {   // tile B's first
+            const Tag& t1 = c.tag[tg == 0 ? C::kTags - 1 : tg - 1];
+            t.part = t1.part;
+            t.h = t1.h;
+            t.q0 = t1.q0;
+            t.p0 = t1.p0;
+            t.lo = t1.lo;
+            t.ntok_a = t1.ntok_a;
+            t.ntok_b = 0;
+            t.nkt_a = t.nkt = t1.nkt;
+            t.i0 = t1.i0;
+            t.len = t1.len;
           }
           int f = part | (i == 0 ? kFirst | kFirstA : 0) | (i == n - 1 ? kLast : 0);
           if (part & kAlt) {
@@ -666,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t0 + kKeys > w.end || __popc(got) != 2 * nblk) {
             // rows that hold data, and rows of blocks that are out of range
             const uint64_t mine = (bs == 64 ? ~0ull : (1ull << bs) - 1ull) << (b * bs);
-            uint64_t rows = on ? mine : 0ull, bad = ent != -2 && !on ? mine : 0ull;
+            uint64_t rows = on ? mine : 0ull, bad = want && !on ? mine : 0ull;
             const int live = w.end - t0;   // keys before the pair's end
             if (live < kKeys) {
               rows &= (1ull << live) - 1ull;
@@ -709,8 +742,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               tma_load_4d(dst, kv ? &tmv : &tmk, bar, 0, r, w.h, ent);
             }
           }
-          w.advance(a);
-          next = entry();
+          if (++w.k >= w.k1) {
+            w.next_pair(a);
+            w.settle(a);
+            open();
+          }
           flying = min(flying + 1, R::kRing);
         }
         if (++rs == R::kRing) {
@@ -734,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ========================= conversion =========================
     const int x = tid & 127;                        // thread of the warpgroup
     const int w = warp & 3;                         // rows 16 w .. of a stage
-    const int group = (warp - kConvert) >> 2;       // stages group, group + 2, ..
+    const int kv = (warp - kConvert) >> 2;          // K or V, tile A's queries or B's
     const int tok_r = x / a.G, head_r = x % a.G;    // of this thread's query row
     const int bs = min(1 << a.log2B, kKeys);
     // A lane's pieces: 16 bytes of kRows rows, as words (8 codes of 4 bits) or
@@ -769,12 +805,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // the two scale bytes of a row's piece, the first for the lane's first words
     const uint32_t pick = (uint32_t)(((turn & 2) ? 0x04 : 0x40) + 0x11 * (rl & 3));
-    int st = group, rs = group, tg = group;
+    int st = 0, rs = 0, tg = 0;
     uint32_t ph = 0u, rph = 0u;
     bool ok = true;
     while (true) {
-      // (in this order: the stage before in this operand slot was converted, so
-      // the copies before in this ring slot have landed)
       if (!wait_warp(c.empty[st], ph ^ 1u) || !wait_warp(c.rfull[rs], rph)) {
         ok = false;
         break;
@@ -782,13 +816,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       Tag& t = c.tag[tg];
       const int flags = t.flags;
       if (flags & kStop) {
-        mbar_arrive(smem_u32(&c.full[st]));
+        warp_arrive(c.full[st]);
         break;
       }
       if (flags & kFirst) {
-        const int before = t.part - 1;
-        if (before >= 0 && !wait_warp(c.qempty[before % kQueries],
-                                      (uint32_t)(before / kQueries) & 1u)) {
+        if (!wait_warp(c.qempty, ((uint32_t)t.part & 1u) ^ 1u)) {
           ok = false;
           break;
         }
@@ -796,8 +828,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // row is brought into binary16's range by a power of two (its largest
         // magnitude into [1, 2)), which its score factor takes back; elements
         // 2^-14 below the largest lose bits below 2^-24 of it.
-#pragma unroll 1
-        for (int k = 0; k < (t.ntok_b > 0 ? 2 : 1); ++k) {
+        if (kv == 0 || t.ntok_b > 0) {
+          const int k = kv;
           const bool valid = x < a.BM * a.G && tok_r < (k ? t.ntok_b : t.ntok_a);
           const uint4* const src = reinterpret_cast<const uint4*>(
               a.q + ((size_t)(valid ? t.q0 + k * a.BM + tok_r : 0) * a.Hq +
@@ -846,26 +878,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     z[1], z[2], z[3]);
             }
           }
-          c.factor[st][k][x] = a.scale_log2 * back;
+          c.factor[t.part % C::kTags][k][x] = a.scale_log2 * back;
         }
       }
       // ---- the stage's keys and values to 16 bits
       uint32_t live = 0xffffu;   // of the warp's 16 rows
       if (flags & kEdge) live = t.rows[w >> 1] >> (16 * (w & 1));
       uint32_t nan = 0u;
-      const uint32_t src = (uint32_t)(rs * R::kStage), to = (uint32_t)st * X::kStage;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        constexpr int kBatch = kRows < 2 ? kRows : 2;   // rows loaded at a time
+      const uint32_t src = (uint32_t)(rs * R::kStage + kv * R::kHalf);
+      const uint32_t to = (uint32_t)st * X::kStage + (uint32_t)kv * X::kPart;
+      {
+        constexpr int kBatch = kRows;   // rows loaded at a time
 #pragma unroll
         for (int i0 = 0; i0 < kRows; i0 += kBatch) {
           uint32_t y[kBatch][4];
           uint32_t sc[kBatch];
 #pragma unroll
           for (int i = 0; i < kBatch; ++i) {
-            const uint32_t at = from[i0 + i] + src + kv * R::kHalf;
+            const uint32_t at = from[i0 + i] + src;
             if constexpr (kFour) {
-              const uint2 s2 = lds8(scales[i0 + i] + src + kv * R::kHalf);
+              const uint2 s2 = lds8(scales[i0 + i] + src);
               sc[i] = prmt(s2.x, s2.y, pick) & 0xffffu;
 #pragma unroll
               for (int j = 0; j < 4; ++j) y[i][j] = lds4(at ^ (uint32_t)(4 * j));
@@ -882,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < kBatch; ++i) {
             const int rr = rl + kRowsStep * (i0 + i);   // of the warp's rows
             const bool in = ((live >> rr) & 1u) != 0u;
-            const uint32_t up = to + kv * X::kPart + (uint32_t)(kRowsStep * (i0 + i)) * 128u;
+            const uint32_t up = to + (uint32_t)(kRowsStep * (i0 + i)) * 128u;
             // rows 4 apart swap halves of the swizzle
             const uint32_t flip = (kRowsStep * (i0 + i)) & 4 ? 64u : 0u;
             if constexpr (kFour) {
@@ -927,21 +959,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       fence_proxy_async_smem();   // the operands, before the tensor core reads them
-      mbar_arrive(smem_u32(&c.full[st]));
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&c.rempty[rs]));
-      rs += 2;
-      if (rs >= R::kRing) {
-        rs -= R::kRing;
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&c.full[st]));
+        mbar_arrive(smem_u32(&c.rempty[rs]));
+      }
+      if (++rs == R::kRing) {
+        rs = 0;
         rph ^= 1u;
       }
-      st += 2;
-      if (st >= S) {
-        st -= S;
+      if (++st == S) {
+        st = 0;
         ph ^= 1u;
       }
-      tg += 2;
-      if (tg >= C::kTags) tg -= C::kTags;
+      if (++tg == C::kTags) tg = 0;
     }
     if (!ok && lane == 0) give_up();
   } else {
@@ -952,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t trow = tmem + ((uint32_t)(32 * wq) << 16);
     const uint32_t tcol = trow + (uint32_t)(256 * tile);
     unsigned long long* const tb = c.tile[tile];
-    const int act = tile ? kActB : kActA, lastbit = tile ? kLastB : kLastA;
+    const int firstbit = tile ? kFirstB : kFirstA, lastbit = tile ? kLastB : kLastA;
     const int tok_r = r / a.G;
     int ntok = 0, p0 = 0, prow = -1;
     bool busy = false;             // some row of this warp is a row
@@ -961,48 +992,39 @@ __global__ void __launch_bounds__(kThreads, 1)
     float factor = 0.f, m_used = -INFINITY, l = 0.f;
     bool poison = false;
     bool ok = true;
-    int st = 0, tgi = 0, nt = 0, nb_alt = 0;
-    uint32_t ph = 0u;
+    int nt = 0, nb_alt = 0;   // scores read, pairs in turn joined
     while (true) {
-      if (!wait_warp(c.full[st], ph)) {
-        ok = false;
-        break;
-      }
-      const Tag& tg = c.tag[tgi];
-      const int flags = tg.flags, kt = tg.kt;
-      if (flags & kStop) break;
-      uint4 mk = make_uint4(0u, 0u, 0u, 0u);
-      if (flags & kMarked) mk = *reinterpret_cast<const uint4*>(tg.mask);
-      if (flags & kFirst) {
-        h = tg.h;
-        q0 = tg.q0;
-        lo = tg.lo;
-        nkt_t = tile ? tg.nkt : tg.nkt_a;
-        i0 = tg.i0;
-        line = tg.len;
-        const bool other = tile == 1 && !(flags & kAlt);   // rows of the second tile
-        ntok = other ? tg.ntok_b : tg.ntok_a;
-        p0 = tg.p0 + (other ? a.BM : 0);
-        const bool valid = r < a.BM * a.G && tok_r < ntok;
-        prow = valid ? p0 + tok_r : -1;
-        busy = 32 * wq < ntok * a.G;
-        factor = c.factor[st][other ? 1 : 0][r];
-        m_used = -INFINITY;
-        l = 0.f;
-        poison = false;
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&c.empty[st]));   // the tag is read
-      if (++st == S) {
-        st = 0;
-        ph ^= 1u;
-      }
-      if (++tgi == C::kTags) tgi = 0;
-      if (!(flags & act)) continue;
       if (!wait_warp(tb[kSFull], (uint32_t)nt & 1u)) {
         ok = false;
         break;
       }
+      const int4 rec = c.scores[tile][nt & 3];
+      const int flags = rec.x, kt = rec.y;
+      if (flags & kStop) break;
+      uint4 mk = make_uint4(0u, 0u, 0u, 0u);
+      if (flags & (firstbit | kMarked)) {
+        const Tag& tg = c.tag[rec.w];
+        mk = *reinterpret_cast<const uint4*>(tg.mask);
+        if (flags & firstbit) {
+          h = tg.h;
+          q0 = tg.q0;
+          lo = tg.lo;
+          nkt_t = tile ? tg.nkt : tg.nkt_a;
+          i0 = tg.i0;
+          line = tg.len;
+          const bool other = tile == 1 && !(flags & kAlt);   // rows of the second tile
+          ntok = other ? tg.ntok_b : tg.ntok_a;
+          p0 = tg.p0 + (other ? a.BM : 0);
+          const bool valid = r < a.BM * a.G && tok_r < ntok;
+          prow = valid ? p0 + tok_r : -1;
+          busy = 32 * wq < ntok * a.G;
+          factor = c.factor[tg.part % C::kTags][other ? 1 : 0][r];
+          m_used = -INFINITY;
+          l = 0.f;
+          poison = false;
+        }
+      }
+      warp_arrive(c.empty[rec.z]);   // the tag is read
       if (busy) {
         tc_fence_after();
         uint32_t sr[kKeys];
@@ -1010,7 +1032,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tcol + 32, *reinterpret_cast<uint32_t(*)[32]>(sr + 32));
         tmem_wait_ld();
         tc_fence_before();
-        mbar_arrive(smem_u32(&tb[kSFree]));
+        warp_arrive(tb[kSFree]);
         const int t0 = kt * kKeys;
         // P = 2^(s f - mu): one packed FFMA per two scores, one ex2 per score,
         // rounded to binary16; its sum in fp32 over the rounded values that O
@@ -1116,9 +1138,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         // no row here: this warp's lanes of P and O hold anything, and nobody
         // reads them
-        mbar_arrive(smem_u32(&tb[kSFree]));
+        warp_arrive(tb[kSFree]);
       }
-      mbar_arrive(smem_u32(&tb[kPFull + (nt & 1)]));
+      warp_arrive(tb[kPFull + (nt & 1)]);
       if (flags & lastbit) {
         // ---- the part's end
         if (!wait_warp(tb[kPEmpty + (nt & 1)], (uint32_t)(nt >> 1) & 1u)) {
@@ -1132,7 +1154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           c.ml[r][0] = m_used;
           c.ml[r][1] = l;
           tc_fence_before();
-          mbar_arrive(smem_u32(&c.bdone));
+          warp_arrive(c.bdone);
         } else {
           float wa = 1.f, wb = 0.f;
           const bool join = (flags & (kAlt | kHasB)) == (kAlt | kHasB);
@@ -1197,8 +1219,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           tc_fence_before();
-          mbar_arrive(smem_u32(&tb[kOFree]));
-          if (join) mbar_arrive(smem_u32(&c.tile[1][kOFree]));
+          warp_arrive(tb[kOFree]);
+          if (join) warp_arrive(c.tile[1][kOFree]);
           if (!whole) {
             if (prow >= 0) {
               rec[(size_t)kTileRows * D + r] = m_used;
@@ -1237,44 +1259,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             group_sync(1 + tile);
             if (c.last[tile]) {
-              // ---- the last record: join them all, in the order of the keys
-              constexpr int kLanes = D / 4, kRows = 128 / kLanes;
-              const int n = c.nparts[tile], rows = ntok * a.G, col = 4 * (r % kLanes);
-              for (int rr = r / kLanes; rr < rows; rr += kRows) {
+              // ---- the last record: join them all, in the order of the keys.  A
+              // thread finds its row's maximum and sum, then takes vectors of rows
+              constexpr int kLanes = D / 4, kAhead = 4;
+              const int n = c.nparts[tile], rows = ntok * a.G;
+              const float* const recs = a.ws_rec + (size_t)tile * rec_floats(D);
+              auto record = [&](int k) {
+                return recs + (size_t)c.parts[tile][k] * 2 * rec_floats(D);
+              };
+              if (r < rows) {
                 float m = -INFINITY, ls = 0.f;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int k0 = 0; k0 < n; k0 += 4) {
-                  float4 v[4];
-                  float pm[4], pl[4];
+                for (int k = 0; k < n; ++k) {
+                  const float* const p = record(k) + (size_t)kTileRows * D + r;
+                  const float pm = __ldcg(p), pl = __ldcg(p + kTileRows);
+                  const float mn = fmaxf(m, pm), base = mn == -INFINITY ? 0.f : mn;
+                  ls = ls * ex2_approx(m - base) + pl * ex2_approx(pm - base);
+                  m = mn;
+                }
+                c.join[tile][r][0] = m == -INFINITY ? 0.f : m;
+                c.join[tile][r][1] = ls == 0.f ? 0.f : a.v_scale / ls;
+              }
+              group_sync(1 + tile);
+              const int col = 4 * (r % kLanes);
+              for (int r0 = r / kLanes; r0 < rows; r0 += kAhead * (128 / kLanes)) {
+                float4 acc[kAhead];
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    const float* p = a.ws_rec +
-                                     ((size_t)c.parts[tile][min(k0 + k, n - 1)] * 2 + tile) *
-                                         rec_floats(D);
-                    v[k] = __ldcg(reinterpret_cast<const float4*>(p + (size_t)rr * D + col));
-                    pm[k] = __ldcg(p + (size_t)kTileRows * D + rr);
-                    pl[k] = __ldcg(p + (size_t)kTileRows * (D + 1) + rr);
+                for (int b = 0; b < kAhead; ++b) acc[b] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int k = 0; k < n; ++k) {
+                  const float* const p = record(k);
+                  float4 v[kAhead];
+                  float w[kAhead];
+#pragma unroll
+                  for (int b = 0; b < kAhead; ++b) {
+                    const int rr = min(r0 + b * (128 / kLanes), rows - 1);
+                    v[b] = __ldcg(reinterpret_cast<const float4*>(p + (size_t)rr * D + col));
+                    w[b] = __ldcg(p + (size_t)kTileRows * D + rr);
                   }
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    if (k0 + k >= n) break;
-                    const float mn = fmaxf(m, pm[k]), base = mn == -INFINITY ? 0.f : mn;
-                    const float x = ex2_approx(m - base), y = ex2_approx(pm[k] - base);
-                    m = mn;
-                    ls = ls * x + pl[k] * y;
-                    acc.x = acc.x * x + v[k].x * y;
-                    acc.y = acc.y * x + v[k].y * y;
-                    acc.z = acc.z * x + v[k].z * y;
-                    acc.w = acc.w * x + v[k].w * y;
+                  for (int b = 0; b < kAhead; ++b) {
+                    const int rr = min(r0 + b * (128 / kLanes), rows - 1);
+                    const float f = ex2_approx(w[b] - c.join[tile][rr][0]);
+                    acc[b].x = fmaf(v[b].x, f, acc[b].x);
+                    acc[b].y = fmaf(v[b].y, f, acc[b].y);
+                    acc[b].z = fmaf(v[b].z, f, acc[b].z);
+                    acc[b].w = fmaf(v[b].w, f, acc[b].w);
                   }
                 }
-                const float mulr = ls == 0.f ? 0.f : a.v_scale / ls;
-                const int tok = rr / a.G;
-                uint16_t* const dst =
-                    a.out + ((size_t)(q0 + (tile ? a.BM : 0) + tok) * a.Hq + (size_t)h * a.G +
-                             (rr - tok * a.G)) * D + col;
-                *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<kBF16>(acc.x * mulr, acc.y * mulr),
-                                                            pack2<kBF16>(acc.z * mulr, acc.w * mulr));
+#pragma unroll
+                for (int b = 0; b < kAhead; ++b) {
+                  const int rr = r0 + b * (128 / kLanes);
+                  if (rr >= rows) break;
+                  const float mul = c.join[tile][rr][1];
+                  const int tok = rr / a.G;
+                  uint16_t* const dst =
+                      a.out + ((size_t)(q0 + (tile ? a.BM : 0) + tok) * a.Hq + (size_t)h * a.G +
+                               (rr - tok * a.G)) * D + col;
+                  *reinterpret_cast<uint2*>(dst) =
+                      make_uint2(pack2<kBF16>(acc[b].x * mul, acc[b].y * mul),
+                                 pack2<kBF16>(acc[b].z * mul, acc[b].w * mul));
+                }
               }
             }
           }

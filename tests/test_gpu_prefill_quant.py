@@ -87,6 +87,23 @@ def test_long_contexts(four, L, T, G):
 
 
 @POOLS
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("L", [3, 70])
+def test_many_stages_a_block(four, D, L):
+    """Many stages in every thread block, tiles that take them in turn or together, the same
+    result every time."""
+    rng = np.random.default_rng(L)
+    n = 8
+    c = Chunks(24, four, BF16, 8, 8, D, 16, [L, 1] * (n // 2), rng.integers(8000, 12000, size=n))
+    out = check(c)
+    ws = torch.zeros(pa.pa_prefill_quant_workspace_size(8, 8, D), dtype=torch.uint8,
+                     device="cuda")
+    for _ in range(10):
+        assert torch.equal(c.run(pa, workspace=ws), out)
+    assert pa.pa_get_error(c.err) == 0
+
+
+@POOLS
 def test_ragged_long_and_short(four):
     rng = np.random.default_rng(9)
     lens = np.concatenate([rng.integers(1, 90, size=40), [6000, 3000, 1, 2]])
