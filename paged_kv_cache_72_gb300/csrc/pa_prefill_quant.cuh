@@ -14,19 +14,20 @@
 // tensor cores in binary16 with fp32 sums in tensor memory.
 //
 // Roles of a block of 20 warps, one block an SM:
-//  * warp 19 (copies) walks the block's share of the work. For every stage of 64
-//    keys it fetches the codes as they lie in the pool into a ring in shared
-//    memory, by bulk copies (4-bit: a plane, or its rows, is contiguous) or TMA
-//    boxes (E4M3: a block's rows of a head), and writes the stage's tag.
-//  * warps 8-11 (conversion of K) and 12-15 (of V) turn the codes into 16-bit
-//    operands with the 128-byte swizzle.  With a part's first stage they bring
-//    the query rows of tile A and of tile B in, as binary16.
-//  * warps 16 and 17 (one thread each, a tile each): S = Q K^T of a stage.
+//  * warp 18 walks the block's share of the work and writes a tag for every stage
+//    of 64 keys: what is to be done with it, and where its blocks lie.
+//  * warps 8-11 (K) and 12-15 (V), 16 keys each, fetch the codes as they lie in
+//    the pool into a ring of their own, some stages ahead (16-byte asynchronous
+//    copies: a TMA copy cost its issuing warp 200 to 300 cycles, and a stage of
+//    16-token blocks takes eight), and turn them into 16-bit operands with the
+//    128-byte swizzle.  With a part's first stage they bring the query rows of
+//    tile A and of tile B in, as binary16.
+//  * warps 16 and 17 (a tile each): S = Q K^T of a stage;
+//  * warp 19 (both tiles): O += P V, P from tensor memory.
 //  * warps 0-3 (tile A) and 4-7 (tile B): thread r owns row r, tensor memory
 //    lane r.  It reads its scores, masks them, writes P = 2^(s - m) and keeps
 //    the row's sum; m moves only when a weight would pass 2^kTop, and then the
 //    row of O is rescaled in tensor memory.
-//  * warp 18 (one thread, both tiles): O += P V, P from tensor memory.
 // A pair without a second tile gives its stages to the tiles in turn: both hold
 // the same rows and end with partial results, which tile A's warps join.
 //
@@ -50,9 +51,9 @@ namespace {
 
 constexpr int kKeys = 64;                 // of a stage
 constexpr int kConvert = 8;               // first conversion warp
-constexpr int kScore = 16;                // warps 16 and 17
-constexpr int kPv = 18;
-constexpr int kCopy = 19;
+constexpr int kIssue = 16;                // warps 16 and 17
+constexpr int kTagger = 18;
+constexpr int kValues = 19;
 constexpr int kThreads = 640;
 constexpr int kMaxGrid = 256;
 // A pair's start and end cost what this many tokens do.
@@ -65,7 +66,7 @@ constexpr int kLeast = 384;
 constexpr float kShift = 7.f, kTop = 15.f, kTopPow = 32768.f;
 // Registers of the roles: softmax, conversion, the others (5 x 96 a thread).
 constexpr int kRegsLaunch = 96;
-constexpr int kRegsSoftmax = 144, kRegsConvert = 72, kRegsOther = 48;
+constexpr int kRegsSoftmax = 144, kRegsConvert = 64, kRegsOther = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsOther == 5 * kRegsLaunch,
               "the launch's registers");
 
@@ -89,13 +90,14 @@ constexpr int kTileRows = 128;
 // o[128][D], m[128], l[128]
 __host__ __device__ constexpr size_t rec_floats(int D) { return (size_t)kTileRows * (D + 2); }
 
-// A stage as it lies in the pool: K, then V, 64 rows each; 4-bit planes of
-// min(B, 64) rows with their scales, E4M3 rows one after the other.
+// A conversion warp's 16 rows of K or V: the rows' codes one after the other, then
+// a 4-bit pool's scales, four rows (a quad) at a time as they lie in the pool.
 template <int D, bool kFour>
 struct Raw {
-  static constexpr int kRowBytes = kFour ? fp4_row_bytes(D) : D;
-  static constexpr int kHalf = kKeys * kRowBytes;
-  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kRowBytes = kFour ? D / 2 : D;
+  static constexpr int kCodes = 16 * kRowBytes;
+  static constexpr int kWarp = kCodes + (kFour ? D : 0);
+  static constexpr int kStage = 8 * kWarp;
   static constexpr int kRing = D == 64 ? 6 : (kFour ? 5 : 3);      // stages in flight
 };
 
@@ -130,28 +132,33 @@ struct Tag {
   int ntok_a, ntok_b, nkt_a, nkt;   // tokens of the tiles, ends of their stages
   long long i0, len;                // the pair's place on the line, its length there
   int part, pad[3];                 // its number in this block
+  // where the stage's pieces (min(B, 64) rows of one block) begin in the pools, or
+  // -1: not to be read
+  long long at[kKeys / 4];
 };
 
 constexpr int kShare = 6;   // a tile's arrivals on a stage's `empty`
+constexpr int kBatch = 4;   // tags written together
 
 template <int S, int kRing>
 struct Control {
-  // a stage's tag lives from its copies to its last reader
-  static constexpr int kTags = S + kRing;
+  // tags are written kBatch at a time, so far ahead that the fetches, kRing stages
+  // ahead of the conversion, find theirs
+  static constexpr int kAhead = kRing + 2 * kBatch;
+  static constexpr int kTags = S + kAhead;
 
-  unsigned long long full[S], empty[S], rfull[kRing], rempty[kRing];
+  unsigned long long kfull[S], vfull[S], empty[S], tfull[kAhead], tempty[kAhead];
   unsigned long long qempty, bdone, done[3];
   unsigned long long tile[2][8];    // s full, s free, p full[2], p empty[2], o free
   alignas(16) Tag tag[kTags];
   // of a part's rows: what scores are multiplied by; before the first part, the
   // line before each thread's run of sequences
   union {
-    float factor[kTags][2][kTileRows];
+    float factor[S + 1][2][kTileRows];
     long long run_pref[kThreads];
   };
   float ml[kTileRows][2];           // tile B's m and l, of a pair in turn
   int4 scores[2][4];                // of a tile's score products: flags, stage, slot, tag
-  volatile uint32_t pvq[2][8];      // records of products to issue: ring[4], tail, head, fin
   long long warp_tot[kThreads / 32];
   long long bound[kMaxGrid + 1];
   uint16_t parts[2][kMaxGrid];      // of a cut tile: its records
@@ -180,14 +187,16 @@ __device__ __forceinline__ void umma_tmem_a(uint32_t d_tmem, uint32_t a_tmem, ui
       "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u));
 }
 
-// a box of a 4-D tensor map into shared memory
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
-                                            int c0, int c1, int c2, int c3) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
-      : "memory");
+// 16 bytes from global to shared memory, past L1
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void commit_copies() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void wait_copies() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 __device__ __forceinline__ uint2 lds8(uint32_t addr) {
   uint2 r;
@@ -210,11 +219,22 @@ __device__ __forceinline__ void mbar_arrive_n(uint32_t bar, uint32_t n) {
                "r"(n)
                : "memory");
 }
+// One lane of the warp, which the compiler knows to be one.  tcgen05 instructions
+// stand behind this in code that all lanes reach: behind `lane == 0` each of them
+// is given a choice of lane and moves of its operands of its own (125 cycles for a
+// product's issue).
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0u;
+}
 // once for the warp, behind what its lanes did
 __device__ __forceinline__ void warp_arrive(unsigned long long& bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bar));
 }
+__device__ __forceinline__ int ilog2_device(int x) { return 31 - __clz(x); }
 // the 128 threads of a warpgroup
 __device__ __forceinline__ void group_sync(int id) {
   asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
@@ -348,9 +368,7 @@ struct Walk {
 };
 
 template <int D, bool kBF16, bool kFour>
-__global__ void __launch_bounds__(kThreads, 1)
-    prefill_quant_kernel(const __grid_constant__ CUtensorMap tmk,
-                         const __grid_constant__ CUtensorMap tmv, const Args a) {
+__global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a) {
   using R = Raw<D, kFour>;
   using X = Tiles<D>;
   constexpr int S = X::kStages;
@@ -365,13 +383,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&c.full[s]), 8);        // the conversion warps
+      mbar_init(smem_u32(&c.kfull[s]), 4);       // K's conversion warps
+      mbar_init(smem_u32(&c.vfull[s]), 4);       // V's
       // per tile: K read, V read, and its four softmax warps have read the tag
       mbar_init(smem_u32(&c.empty[s]), 2 * kShare);
     }
-    for (int s = 0; s < R::kRing; ++s) {
-      mbar_init(smem_u32(&c.rfull[s]), 1);       // the copy warp's expect-tx
-      mbar_init(smem_u32(&c.rempty[s]), 8);      // the same
+    for (int s = 0; s < C::kAhead; ++s) {
+      mbar_init(smem_u32(&c.tfull[s]), 1);       // the tag is written
+      mbar_init(smem_u32(&c.tempty[s]), 8);      // its stage is converted
     }
     mbar_init(smem_u32(&c.qempty), 2);           // a commit of each score issuer
     mbar_init(smem_u32(&c.bdone), 4);            // tile B's warps
@@ -384,7 +403,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&c.tile[t][kPEmpty + p]), 1);
       }
       mbar_init(smem_u32(&c.tile[t][kOFree]), 4);
-      for (int w = 0; w < 8; ++w) c.pvq[t][w] = 0u;
     }
     c.abort = 0;
     fence_barrier_init();
@@ -433,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long nb = min((long long)gridDim.x, (total + kLeast - 1) / kLeast);
   if ((long long)blockIdx.x >= nb) return;
   if (tid <= nb) c.bound[tid] = total * tid / nb;
-  if (warp == kCopy) {
+  if (warp == kTagger) {
     tmem_alloc(smem_u32(&c.tmem), 512);
     tc_fence_before();
   }
@@ -451,317 +469,307 @@ __global__ void __launch_bounds__(kThreads, 1)
     c.abort = 1;
   };
 
-  if (warp >= kScore) {
+  if (warp >= kIssue) {
     setmaxnreg_dec<kRegsOther>();
-    if (warp < kPv && lane == 0) {
+    if (warp < kTagger) {
       // ===================== score products of tile t =====================
-      // The next stage's S = Q K^T as soon as its keys are there, the S buffer
-      // and the P region its weights will go to are free, and at most one of
-      // the tile's O += P V is still to be issued (the tensor pipe executes in
-      // issue order).  Every product leaves a record for the O issuer: the
-      // stage's slot (bits 0-2), a part's first (3), wait for O (4) with
-      // parity (5).
-      static_assert(S <= 8, "slots take 3 bits");
-      const int t = warp - kScore;
-      const int act = t == 0 ? kActA : kActB, first = t == 0 ? kFirstA : kFirstB;
+      // S = Q K^T of the tile's next stage once its keys are there, its S buffer has
+      // been read and the P region that its weights will go to is free.
+      const int t = warp - kIssue;
+      const int act = t == 0 ? kActA : kActB;
       constexpr uint32_t id_s = umma_idesc_f16(false, kTileRows, kKeys, false);
-      volatile uint32_t* const q = c.pvq[t];
       unsigned long long* const tb = c.tile[t];
       const uint32_t tcol = tmem + (uint32_t)(256 * t);
       const uint64_t dq[2] = {umma_desc_sw128(qtiles, 16, 1024),
                               umma_desc_sw128(qtiles + (uint32_t)t * X::kQTile, 16, 1024)};
-      int rt = 0, ni = 0;             // records pushed (scores issued), the tile's parts started
-      int st = 0, tg = 0;             // slots
+      int rt = 0, st = 0, tg = 0;     // scores issued, slots
       uint32_t ph = 0u;
       bool ok = true;
-      long long t_last = clock64();
+      auto wait = [&](unsigned long long& bar, uint32_t parity) {
+        ok = ok && wait_warp(bar, parity);
+        return ok;
+      };
       while (true) {
-        bool progressed = false;
-        if (rt - (int)q[5] < 2 && mbar_test(smem_u32(&c.full[st]), ph)) {
-          const int flags = *const_cast<volatile int*>(&c.tag[tg].flags);
-          bool ready = true;
-          if (flags & (act | kStop)) {
-            // the softmax has read the scores (and their record) before these
-            if (rt >= 1) ready = mbar_test(smem_u32(&tb[kSFree]), (uint32_t)(rt - 1) & 1u);
-            if (ready && rt >= 2)
-              ready = mbar_test(smem_u32(&tb[kPEmpty + (rt & 1)]), (uint32_t)((rt >> 1) - 1) & 1u);
-            if (ready) {
-              c.scores[t][rt & 3] = make_int4(flags, c.tag[tg].kt, st, tg);
-              if (flags & kStop) {
-                mbar_arrive_n(smem_u32(&tb[kSFull]), 2);
-                break;
-              }
-              mbar_arrive(smem_u32(&tb[kSFull]));
-              tc_fence_after();
-              const uint64_t da = dq[(flags & kAlt) ? 0 : 1];
-              const uint64_t db = umma_desc_sw128(stages + (uint32_t)st * X::kStage, 16, 1024);
-              // K steps of 16 columns: 32 bytes on within a 64-column plane
-#pragma unroll
-              for (int ks = 0; ks < D / 16; ++ks) {
-                const uint32_t o = (uint32_t)(ks & 3) * 32u, p = (uint32_t)(ks >> 2);
-                umma_f16(tcol, da + ((p * X::kQPlane + o) >> 4), db + ((p * X::kPlane + o) >> 4),
-                         id_s, ks > 0);
-              }
-              umma_commit(smem_u32(&tb[kSFull]));
-              umma_commit(smem_u32(&c.empty[st]));   // K is read
-              uint32_t rc = (uint32_t)st;
-              if (flags & first) {
-                rc |= 8u;
-                if (ni > 0) rc |= 16u | ((uint32_t)((ni - 1) & 1) << 5);
-                ++ni;
-              }
-              q[rt & 3] = rc;
-              __threadfence_block();   // the record before the tail that publishes it
-              q[4] = (uint32_t)(++rt);
+        if (!wait(c.kfull[st], ph)) break;
+        const int flags = c.tag[tg].flags;
+        if (flags & (act | kStop)) {
+          // the softmax has read the scores (and their record) before these
+          if (rt >= 1 && !wait(tb[kSFree], (uint32_t)(rt - 1) & 1u)) break;
+          if (flags & kStop) {
+            if (lane == 0) {
+              c.scores[t][rt & 3] = make_int4(flags, 0, 0, 0);
+              mbar_arrive_n(smem_u32(&tb[kSFull]), 2);
             }
-          } else {   // not this tile's
-            mbar_arrive_n(smem_u32(&c.empty[st]), kShare);
-          }
-          if (ready) {
-            if (flags & kLast) umma_commit(smem_u32(&c.qempty));   // the queries are read
-            if (++st == S) {
-              st = 0;
-              ph ^= 1u;
-            }
-            if (++tg == C::kTags) tg = 0;
-            progressed = true;
-          }
-        }
-        if (progressed) {
-          t_last = clock64();
-        } else {
-          if (c.abort || clock64() - t_last > kWaitLimitCycles) {
-            ok = false;
             break;
           }
-          __nanosleep(20);   // the issue slots are the softmax warps'
-        }
-      }
-      if (!ok) give_up();
-      __threadfence_block();
-      q[6] = 1u;   // no more records
-      umma_commit(smem_u32(&c.done[t]));
-      mbar_wait_bounded(smem_u32(&c.done[t]), 0u, nullptr);
-    } else if (warp == kPv && lane == 0) {
-      // ===================== O += P V of both tiles =====================
-      constexpr uint32_t id_o = umma_idesc_f16(false, kTileRows, D, true);
-      int rh[2] = {0, 0};   // records issued
-      bool ok = true;
-      long long t_last = clock64();
-      auto try_pv = [&](int t, int& n) -> bool {
-        volatile uint32_t* const q = c.pvq[t];
-        if ((int)q[4] == n) return false;
-        __threadfence_block();
-        const uint32_t rc = q[n & 3];
-        unsigned long long* const tb = c.tile[t];
-        if (!mbar_test(smem_u32(&tb[kPFull + (n & 1)]), (uint32_t)(n >> 1) & 1u)) return false;
-        if ((rc & 16u) && !mbar_test(smem_u32(&tb[kOFree]), (rc >> 5) & 1u)) return false;
-        tc_fence_after();
-        const int st = (int)(rc & 7u);
-        const bool first = (rc & 8u) != 0u;
-        const uint32_t tcol = tmem + (uint32_t)(256 * t);
-        // V (64 keys x D) MN-major: 64-column planes kPlane apart, groups of 8
-        // keys 1024 bytes apart; 16 keys a step, 8 columns of P
-        const uint64_t dv = umma_desc_sw128(stages + (uint32_t)st * X::kStage + X::kPart,
-                                            X::kPlane, 1024);
-        const uint32_t p = tcol + 64u + 32u * (uint32_t)(n & 1);
+          if (rt >= 2 && !wait(tb[kPEmpty + (rt & 1)], (uint32_t)((rt >> 1) - 1) & 1u)) break;
+          // tile B's queries come with the first values
+          if (t == 1 && (flags & (kFirst | kAlt)) == kFirst && !wait(c.vfull[st], ph)) break;
+          if (lane == 0) {
+            c.scores[t][rt & 3] = make_int4(flags, c.tag[tg].kt, st, tg);
+            mbar_arrive(smem_u32(&tb[kSFull]));
+          }
+          tc_fence_after();
+          const uint64_t da = dq[(flags & kAlt) ? 0 : 1];
+          const uint64_t db = umma_desc_sw128(stages + (uint32_t)st * X::kStage, 16, 1024);
+          if (elect()) {
+            // K steps of 16 columns: 32 bytes on within a 64-column plane
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          umma_tmem_a(tcol + 128u, p + 8u * k, dv + ((uint32_t)k * 2048u >> 4), id_o,
-                      !first || k > 0);
-        umma_commit(smem_u32(&tb[kPEmpty + (n & 1)]));
-        umma_commit(smem_u32(&c.empty[st]));   // the V share
-        q[5] = (uint32_t)(++n);
-        return true;
-      };
-      while (true) {
-        bool progressed = try_pv(0, rh[0]);
-        progressed = try_pv(1, rh[1]) || progressed;
-        if (progressed) {
-          t_last = clock64();
-          continue;
-        }
-        if (c.pvq[0][6] && c.pvq[1][6]) {
-          __threadfence_block();
-          if ((int)c.pvq[0][4] == rh[0] && (int)c.pvq[1][4] == rh[1]) break;
-        }
-        if (c.abort || clock64() - t_last > kWaitLimitCycles) {
-          ok = false;
-          break;
-        }
-        __nanosleep(20);
-      }
-      if (!ok) give_up();
-      umma_commit(smem_u32(&c.done[2]));
-      mbar_wait_bounded(smem_u32(&c.done[2]), 0u, nullptr);
-    } else if (warp == kCopy) {
-      // ===================== copies and tags =====================
-      const int B = 1 << a.log2B;
-      const int bs = min(B, kKeys), nblk = kKeys / bs;   // rows of a piece, pieces of a stage
-      const int kv = lane / nblk, b = lane & (nblk - 1); // this lane's: K's or V's piece b
-      const uint32_t piece = (uint32_t)(bs * R::kRowBytes);
-      const uint8_t* const pool = kv ? a.vc : a.kc;
-      const uint32_t dst0 = ring + (uint32_t)(kv * R::kHalf) + (uint32_t)b * piece;
-      Walk w;
-      w.start(a, c.run_pref, per, c.bound[blockIdx.x], c.bound[blockIdx.x + 1]);
-      // 64 entries of the sequence's table from a multiple of 32 on, a pair a lane,
-      // so that no stage waits for its own; blocks without an attended token are
-      // not looked up
-      int win = 0, near = -1, far = -1;
-      auto look = [&](int at) -> int {
-        const int idx = at + lane;
-        return !w.done && idx >= (w.lo >> a.log2B) && idx <= ((w.end - 1) >> a.log2B)
-                   ? __ldg(a.bt + (size_t)w.i * a.stride + idx) : -1;
-      };
-      auto open = [&]() {
-        win = ((w.k * kKeys) >> a.log2B) & ~31;
-        near = look(win);
-        far = look(win + 32);
-      };
-      open();
-      int rs = 0, tg = 0, parts = 0, part = 0, nkt_a = 0;
-      int flying = 0;   // slots whose copies may be in flight
-      uint32_t ph = 0u;
-      while (true) {
-        if (!wait_warp(c.rempty[rs], ph ^ 1u)) {
-          if (lane == 0) give_up();
-          break;
-        }
-        Tag& t = c.tag[tg];
-        const uint32_t bar = smem_u32(&c.rfull[rs]);
-        if (w.done) {
-          if (lane == 0) {
-            t.flags = kStop;
-            mbar_arrive(bar);
-          }
-          break;
-        } else {
-          const int t0 = w.k * kKeys, idx0 = t0 >> a.log2B;
-          if (idx0 - win >= 32) {
-            win += 32;
-            near = far;
-            far = look(win + 32);
-          }
-          const int ent = __shfl_sync(0xffffffffu, near, (idx0 + ((b * bs) >> a.log2B)) & 31);
-          // some row of this lane's piece is attended to, and its block is there
-          const bool want = kv < 2 && t0 + b * bs + bs - 1 >= w.lo && t0 + b * bs < w.end;
-          const bool on = want && ent >= 0 && (long long)ent < a.num_blocks;
-          if (want && !on) set_error(a.err, PA_DEVERR_BLOCK_ID);
-          const uint32_t got = __ballot_sync(0xffffffffu, on);
-          const int n = w.k1 - w.k0, i = w.k - w.k0;
-          if (i == 0) {
-            const long long w2 = 2 * a.BM;
-            const int left = (int)min((long long)w.L - w2 * w.pr, w2);   // the pair's tokens
-            const int ntok_a = min(left, a.BM), ntok_b = left - ntok_a;
-            const int nkt = w.nkt(), klo = w.lo / kKeys;
-            const int p0 = w.T - w.L + (int)(w2 * w.pr);
-            nkt_a = ntok_b == 0 ? nkt : (p0 + ntok_a - 1) / kKeys + 1;
-            part = (ntok_b == 0 ? kAlt | (n >= 2 ? kHasB : 0) : 0) | (w.k0 == klo ? kBegins : 0) |
-                   (w.k0 == klo && w.k1 >= nkt_a ? kWholeA : 0) |
-                   (w.k0 == klo && w.k1 == nkt ? kWholeB : 0);
-
-            if (lane == 0) {
-              t.part = parts;
-              t.h = w.h;
-              t.q0 = w.q0 + (int)(w2 * w.pr);
-              t.p0 = p0;
-              t.lo = w.lo;
-              t.ntok_a = ntok_a;
-              t.ntok_b = ntok_b;
-              t.nkt_a = nkt_a;
-              t.nkt = nkt;
-              t.i0 = w.i0;
-              t.len = w.length();
+            for (int ks = 0; ks < D / 16; ++ks) {
+              const uint32_t o = (uint32_t)(ks & 3) * 32u, p = (uint32_t)(ks >> 2);
+              umma_f16(tcol, da + ((p * X::kQPlane + o) >> 4), db + ((p * X::kPlane + o) >> 4),
+                       id_s, ks > 0);
             }
-            ++parts;
-          } else if (i == 1 && (part & kAlt) && lane == 0) {   // tile B's first
-            const Tag& t1 = c.tag[tg == 0 ? C::kTags - 1 : tg - 1];
-            t.part = t1.part;
-            t.h = t1.h;
-            t.q0 = t1.q0;
-            t.p0 = t1.p0;
-            t.lo = t1.lo;
-            t.ntok_a = t1.ntok_a;
-            t.ntok_b = 0;
-            t.nkt_a = t.nkt = t1.nkt;
-            t.i0 = t1.i0;
-            t.len = t1.len;
-          }
-          int f = part | (i == 0 ? kFirst | kFirstA : 0) | (i == n - 1 ? kLast : 0);
-          if (part & kAlt) {
-            f |= (i & 1) ? kActB : kActA;
-            if (i == 1) f |= kFirstB;
-            if (i + 2 >= n) f |= (i & 1) ? kLastB : kLastA;
-          } else {
-            f |= kActB | (w.k < nkt_a ? kActA : 0) | (i == 0 ? kFirstB : 0) |
-                 (i == n - 1 ? kLastB : 0) | (w.k == min(w.k1, nkt_a) - 1 ? kLastA : 0);
-          }
-          if (t0 + kKeys > w.end || __popc(got) != 2 * nblk) {
-            // rows that hold data, and rows of blocks that are out of range
-            const uint64_t mine = (bs == 64 ? ~0ull : (1ull << bs) - 1ull) << (b * bs);
-            uint64_t rows = on ? mine : 0ull, bad = want && !on ? mine : 0ull;
-            const int live = w.end - t0;   // keys before the pair's end
-            if (live < kKeys) {
-              rows &= (1ull << live) - 1ull;
-              bad &= (1ull << live) - 1ull;
-            }
-            const uint32_t r0 = __reduce_or_sync(0xffffffffu, (uint32_t)rows);
-            const uint32_t r1 = __reduce_or_sync(0xffffffffu, (uint32_t)(rows >> 32));
-            const uint32_t b0 = __reduce_or_sync(0xffffffffu, (uint32_t)bad);
-            const uint32_t b1 = __reduce_or_sync(0xffffffffu, (uint32_t)(bad >> 32));
-            f |= kEdge | ((b0 | b1) ? kMarked : 0);
-            if (lane == 0) {
-              t.rows[0] = r0;
-              t.rows[1] = r1;
-              t.mask[0] = b0;
-              t.mask[1] = b1;
-            }
-          } else if (lane == 0) {
-            t.mask[0] = t.mask[1] = 0u;
-          }
-          if (lane == 0) {
-            t.mask[2] = t.mask[3] = 0u;
-            t.flags = f;
-            t.kt = w.k;
-            mbar_arrive_expect_tx(bar, (uint32_t)__popc(got) * piece);
+            umma_commit(smem_u32(&tb[kSFull]));
+            umma_commit(smem_u32(&c.empty[st]));   // K is read
+            if (flags & kLast) umma_commit(smem_u32(&c.qempty));   // the queries are read
           }
           __syncwarp();
-          if (on) {
-            const uint32_t dst = dst0 + (uint32_t)(rs * R::kStage);
-            const int r = (t0 + b * bs) & (B - 1);
-            if constexpr (kFour) {
-              const uint8_t* const plane = pool + fp4_plane(ent, a.H, w.h, B * R::kRowBytes);
-              if (B <= kKeys) {
-                bulk_load(dst, plane, piece, bar);
-              } else {
-                bulk_load(dst, plane + r * (D / 2), kKeys * (D / 2), bar);
-                bulk_load(dst + kKeys * (D / 2), plane + B * (D / 2) + r * (D / 16),
-                          kKeys * (D / 16), bar);
-              }
-            } else {
-              tma_load_4d(dst, kv ? &tmv : &tmk, bar, 0, r, w.h, ent);
-            }
+          ++rt;
+        } else {   // not this tile's: all but the V share
+          if (elect()) {
+            mbar_arrive_n(smem_u32(&c.empty[st]), kShare - 1);
+            if (flags & kLast) umma_commit(smem_u32(&c.qempty));
           }
-          if (++w.k >= w.k1) {
-            w.next_pair(a);
-            w.settle(a);
-            open();
-          }
-          flying = min(flying + 1, R::kRing);
+          __syncwarp();
         }
-        if (++rs == R::kRing) {
-          rs = 0;
+        if (++st == S) {
+          st = 0;
           ph ^= 1u;
         }
         if (++tg == C::kTags) tg = 0;
       }
-      // after an abort no copy may land in shared memory once the block has left
-      if (c.abort) {
-        for (; flying > 0; --flying) {   // the slots before this one in the ring
-          rs = rs == 0 ? R::kRing - 1 : rs - 1;
-          if (rs == R::kRing - 1) ph ^= 1u;
-          mbar_wait_bounded(smem_u32(&c.rfull[rs]), ph, nullptr);
+      if (!ok && lane == 0) give_up();
+      // every product has completed before the tensor memory is released
+      if (elect()) umma_commit(smem_u32(&c.done[t]));
+      __syncwarp();
+      mbar_wait_bounded(smem_u32(&c.done[t]), 0u, nullptr);
+    } else if (warp == kValues) {
+      // ===================== O += P V of both tiles =====================
+      // Each tile's stages in order; of the two, whichever has its weights written.
+      constexpr uint32_t id_o = umma_idesc_f16(false, kTileRows, D, true);
+      struct Cursor {
+        int n, ni, st, tg;   // products issued, parts begun, slots
+        uint32_t ph;
+        bool done;
+      };
+      Cursor cur[2] = {{0, 0, 0, 0, 0u, false}, {0, 0, 0, 0, 0u, false}};
+      auto ready = [&](unsigned long long& bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_test(smem_u32(&bar), parity)) != 0;
+      };
+      auto step = [&](int t, Cursor& k) -> bool {   // whether the tile went a stage on
+        if (k.done || !ready(c.vfull[k.st], k.ph)) return false;
+        const int flags = c.tag[k.tg].flags;
+        unsigned long long* const tb = c.tile[t];
+        if (flags & kStop) {
+          k.done = true;
+          return true;
         }
+        if (flags & (t == 0 ? kActA : kActB)) {
+          const bool first = (flags & (t == 0 ? kFirstA : kFirstB)) != 0;
+          if (!ready(tb[kPFull + (k.n & 1)], (uint32_t)(k.n >> 1) & 1u)) return false;
+          if (first && k.ni > 0 && !ready(tb[kOFree], (uint32_t)(k.ni - 1) & 1u)) return false;
+          if (first) ++k.ni;
+          tc_fence_after();
+          // V (64 keys x D) MN-major: 64-column planes kPlane apart, groups of 8
+          // keys 1024 bytes apart; 16 keys a step, 8 columns of P
+          const uint32_t tcol = tmem + (uint32_t)(256 * t);
+          const uint64_t dv = umma_desc_sw128(stages + (uint32_t)k.st * X::kStage + X::kPart,
+                                              X::kPlane, 1024);
+          const uint32_t p = tcol + 64u + 32u * (uint32_t)(k.n & 1);
+          if (elect()) {
+#pragma unroll
+            for (int e = 0; e < kKeys / 16; ++e)
+              umma_tmem_a(tcol + 128u, p + 8u * e, dv + ((uint32_t)e * 2048u >> 4), id_o,
+                          !first || e > 0);
+            umma_commit(smem_u32(&tb[kPEmpty + (k.n & 1)]));
+            umma_commit(smem_u32(&c.empty[k.st]));   // V is read
+          }
+          __syncwarp();
+          ++k.n;
+        } else if (lane == 0) {
+          mbar_arrive(smem_u32(&c.empty[k.st]));
+        }
+        if (++k.st == S) {
+          k.st = 0;
+          k.ph ^= 1u;
+        }
+        if (++k.tg == C::kTags) k.tg = 0;
+        return true;
+      };
+      long long t_last = clock64();
+      while (!(cur[0].done && cur[1].done)) {
+        const bool a0 = step(0, cur[0]), a1 = step(1, cur[1]);
+        if (a0 || a1) {
+          t_last = clock64();
+        } else if (__any_sync(0xffffffffu,
+                              c.abort != 0 || clock64() - t_last > kWaitLimitCycles)) {
+          if (lane == 0) give_up();
+          break;
+        }
+      }
+      if (elect()) umma_commit(smem_u32(&c.done[2]));
+      __syncwarp();
+      mbar_wait_bounded(smem_u32(&c.done[2]), 0u, nullptr);
+    } else if (warp == kTagger) {
+      // ===================== tags =====================
+      const int B = 1 << a.log2B;
+      const int bs = min(B, kKeys), nblk = kKeys / bs;   // rows of a piece, pieces of a stage
+      // bytes of a block, of a block's head, of a row of it
+      const long long block_bytes = kFour ? (long long)a.H * B * fp4_row_bytes(D)
+                                          : (long long)B * a.H * D;
+      const int head_bytes = kFour ? B * fp4_row_bytes(D) : D;
+      const int row_bytes = kFour ? D / 2 : a.H * D;
+      Walk w;
+      w.start(a, c.run_pref, per, c.bound[blockIdx.x], c.bound[blockIdx.x + 1]);
+      // Tags of up to kBatch stages of a part together, a lane each, and a table
+      // entry a lane (in kRounds rounds), which is loaded a batch ahead: value v is
+      // piece v % nblk of stage v / nblk
+      constexpr int kRounds = kBatch * 16 / 32;
+      const int lognblk = ilog2_device(nblk);
+      int ents[kRounds];
+      auto look = [&]() {
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u) {
+          const int v = lane + 32 * u;
+          const int k = w.k + (v >> lognblk), t = k * kKeys + (v & (nblk - 1)) * bs;
+          ents[u] = -2;   // no row of it is attended to
+          if (!w.done && v < kBatch * nblk && k < w.k1 && t + bs - 1 >= w.lo && t < w.end)
+            ents[u] = __ldg(a.bt + (size_t)w.i * a.stride + (t >> a.log2B));
+        }
+      };
+      look();
+      int ts = 0, tg = 0, parts = 0, part = 0, nkt_a = 0;
+      uint32_t ph = 0u;
+      bool ok = true;
+      while (true) {
+        const int m = w.done ? 1 : min(kBatch, w.k1 - w.k);   // stages of this batch
+        for (int k = 0; k < m && ok; ++k) {
+          const int b = ts + k;
+          ok = wait_warp(c.tempty[b < C::kAhead ? b : b - C::kAhead],
+                         (b < C::kAhead ? ph : ph ^ 1u) ^ 1u);
+        }
+        if (!ok) {
+          if (lane == 0) give_up();
+          break;
+        }
+        // this lane's stage of the batch, its tag and barrier
+        const int k = lane < m ? lane : 0;
+        const int tk = tg + k < C::kTags ? tg + k : tg + k - C::kTags;
+        Tag& t = c.tag[tk];
+        const int bk = ts + k < C::kAhead ? ts + k : ts + k - C::kAhead;
+        if (w.done) {
+          if (lane == 0) t.flags = kStop;
+          warp_arrive(c.tfull[ts]);
+          break;
+        }
+        uint32_t want[kRounds], got[kRounds];
+#pragma unroll
+        for (int u = 0; u < kRounds; ++u) {
+          const int v = lane + 32 * u, ent = ents[u];
+          const bool on = ent >= 0 && (long long)ent < a.num_blocks;
+          if (ent != -2 && !on) set_error(a.err, PA_DEVERR_BLOCK_ID);
+          want[u] = __ballot_sync(0xffffffffu, ent != -2);
+          got[u] = __ballot_sync(0xffffffffu, on);
+          const int sv = v >> lognblk;
+          if (sv < m) {
+            const int tv = tg + sv < C::kTags ? tg + sv : tg + sv - C::kTags;
+            c.tag[tv].at[v & (nblk - 1)] =
+                on ? ent * block_bytes + (long long)w.h * head_bytes +
+                         (long long)(((w.k + sv) * kKeys) & (B - 1)) * row_bytes
+                   : -1ll;
+          }
+        }
+        const int n = w.k1 - w.k0, i = w.k - w.k0 + k;   // stages of the part, this lane's
+        if (w.k == w.k0) {   // the part begins
+          const long long w2 = 2 * a.BM;
+          const int left = (int)min((long long)w.L - w2 * w.pr, w2);   // the pair's tokens
+          const int ntok_a = min(left, a.BM), ntok_b = left - ntok_a;
+          const int nkt = w.nkt(), klo = w.lo / kKeys;
+          const int p0 = w.T - w.L + (int)(w2 * w.pr);
+          nkt_a = ntok_b == 0 ? nkt : (p0 + ntok_a - 1) / kKeys + 1;
+          part = (ntok_b == 0 ? kAlt | (n >= 2 ? kHasB : 0) : 0) | (w.k0 == klo ? kBegins : 0) |
+                 (w.k0 == klo && w.k1 >= nkt_a ? kWholeA : 0) |
+                 (w.k0 == klo && w.k1 == nkt ? kWholeB : 0);
+          if (lane < min(m, 2)) {   // tile B's first stage may be the second
+            t.part = parts;
+            t.h = w.h;
+            t.q0 = w.q0 + (int)(w2 * w.pr);
+            t.p0 = p0;
+            t.lo = w.lo;
+            t.ntok_a = ntok_a;
+            t.ntok_b = ntok_b;
+            t.nkt_a = nkt_a;
+            t.nkt = nkt;
+            t.i0 = w.i0;
+            t.len = w.length();
+          }
+          ++parts;
+        }
+        const int kt = w.k + k;
+        int f = part | (i == 0 ? kFirst | kFirstA : 0) | (i == n - 1 ? kLast : 0);
+        if (part & kAlt) {
+          f |= (i & 1) ? kActB : kActA;
+          if (i == 1) f |= kFirstB;
+          if (i + 2 >= n) f |= (i & 1) ? kLastB : kLastA;
+        } else {
+          f |= kActB | (kt < nkt_a ? kActA : 0) | (i == 0 ? kFirstB : 0) |
+               (i == n - 1 ? kLastB : 0) | (kt == min(w.k1, nkt_a) - 1 ? kLastA : 0);
+        }
+        // the pieces of this lane's stage that are to be read, and that are there
+        const int v0 = k << lognblk;
+        uint32_t mine = got[0], wanted = want[0];
+#pragma unroll
+        for (int u = 1; u < kRounds; ++u)
+          if ((v0 >> 5) == u) {
+            mine = got[u];
+            wanted = want[u];
+          }
+        const uint32_t all = 0xffffffffu >> (32 - nblk);
+        mine = (mine >> (v0 & 31)) & all;
+        wanted = (wanted >> (v0 & 31)) & all;
+        uint4 mask = make_uint4(0u, 0u, 0u, 0u);
+        if (kt * kKeys + kKeys > w.end || mine != all) {
+          // rows that hold data, and rows of blocks that are out of range
+          uint64_t rows = 0ull, bad = 0ull;
+          for (int b = 0; b < nblk; ++b) {
+            const uint64_t bits = (~0ull >> (64 - bs)) << (b * bs);
+            if ((mine >> b) & 1u) rows |= bits;
+            else if ((wanted >> b) & 1u) bad |= bits;
+          }
+          const int live = w.end - kt * kKeys;   // keys before the pair's end
+          if (live < kKeys) {
+            rows &= (1ull << live) - 1ull;
+            bad &= (1ull << live) - 1ull;
+          }
+          f |= kEdge | (bad ? kMarked : 0);
+          mask.x = (uint32_t)bad;
+          mask.y = (uint32_t)(bad >> 32);
+          if (lane < m) {
+            t.rows[0] = (uint32_t)rows;
+            t.rows[1] = (uint32_t)(rows >> 32);
+          }
+        }
+        if (lane < m) {
+          *reinterpret_cast<uint4*>(t.mask) = mask;
+          t.flags = f;
+          t.kt = kt;
+        }
+        __syncwarp();
+        if (lane < m) mbar_arrive(smem_u32(&c.tfull[bk]));
+        w.k += m;
+        if (w.k >= w.k1) {
+          w.next_pair(a);
+          w.settle(a);
+        }
+        look();
+        ts += m;
+        if (ts >= C::kAhead) {
+          ts -= C::kAhead;
+          ph ^= 1u;
+        }
+        tg += m;
+        if (tg >= C::kTags) tg -= C::kTags;
       }
     }
     __syncwarp();
@@ -772,13 +780,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int w = warp & 3;                         // rows 16 w .. of a stage
     const int kv = (warp - kConvert) >> 2;          // K or V, tile A's queries or B's
     const int tok_r = x / a.G, head_r = x % a.G;    // of this thread's query row
-    const int bs = min(1 << a.log2B, kKeys);
+    const int B = 1 << a.log2B, log2s = min(a.log2B, 6);
     // A lane's pieces: 16 bytes of kRows rows, as words (8 codes of 4 bits) or
     // double words (8 codes of 8 bits), each of which becomes one 16-byte chunk of
     // the swizzled operand.  A lane takes word j ^ turn as its j-th: `turn` is such
     // that neither the loads of a warp nor the stores of eight neighbours meet in
-    // a bank (rows lie 16 D / kPieces bytes apart in the ring, and chunk k of an
-    // operand's row r at k ^ r % 8).
+    // a bank (rows lie kRowBytes apart in the ring, and chunk k of an operand's row
+    // r at k ^ r % 8).
     constexpr int kPieces = kFour ? D / 32 : D / 16;   // of a row
     constexpr int kRowsStep = 32 / kPieces;            // rows of a warp's load
     constexpr int kRows = 16 / kRowsStep;
@@ -787,16 +795,68 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int turn = kFour ? (D == 128 ? (((col >> 1) << 1) ^ (rl & 1) ^ (rl & 3) ^ ((rl >> 2) & 1))
                                        : ((rl >> 2) & 3))
                            : (D == 128 ? ((col >> 2) ^ (rl & 1)) : ((rl >> 1) & 1));
-    uint32_t from[kRows], scales[kFour ? kRows : 1], chunk[kWords];
+    const uint32_t mine = ring + (uint32_t)((4 * kv + w) * R::kWarp);
+    const uint32_t from = mine + (uint32_t)(rl * R::kRowBytes + 16 * col + (16 / kWords) * turn);
+    const uint32_t scales = mine + (uint32_t)(R::kCodes + (rl >> 2) * (D / 4) + 8 * col);
+    // the copies: this lane's bytes of its rows, behind the piece they lie in
+    const uint8_t* const pool = kv ? a.vc : a.kc;
+    const long long row_bytes = kFour ? D / 2 : (long long)a.H * D;
+    int piece[kRows], sc_piece = 0;
+    long long src[kRows], sc_src = 0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int row = 16 * w + rl + kRowsStep * i, blk = row / bs, rr = row % bs;
-      from[i] = ring + (uint32_t)(blk * bs * R::kRowBytes + rr * (kFour ? D / 2 : D) + 16 * col +
-                                  (16 / kWords) * turn);
-      if constexpr (kFour)
-        scales[i] = ring + (uint32_t)(blk * bs * R::kRowBytes + bs * (D / 2) + (rr >> 2) * (D / 4) +
-                                      8 * col);
+      const int row = 16 * w + rl + kRowsStep * i;
+      piece[i] = row >> log2s;
+      src[i] = (row & ((1 << log2s) - 1)) * row_bytes + 16 * col;
     }
+    constexpr int kScalePieces = kFour ? D / 16 : 0;   // 16 bytes each
+    if constexpr (kFour) {
+      const int q = lane / (D / 64), row = 16 * w + 4 * q;
+      sc_piece = (row & 63) >> log2s;
+      sc_src = B * (D / 2) + (row & ((1 << log2s) - 1)) * (D / 16) + 16 * (lane % (D / 64));
+    }
+    // Fetching a stage: its tag is looked at before the conversion of another, whose
+    // time hides the look, and the copies are issued behind it.
+    long long at[kRows], sc_at = -1;
+    int next_rs = 0, next_ts = 0, next_tg = 0;    // of the stage to be fetched next
+    uint32_t next_ph = 0u;
+    bool ok = true, more = true;
+    auto look = [&]() {
+      if (!more) return;
+      ok = ok && wait_warp(c.tfull[next_ts], next_ph);
+      const Tag& t = c.tag[next_tg];
+      more = ok && !(t.flags & kStop);
+      if (!more) return;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) at[i] = t.at[piece[i]];
+      if constexpr (kFour) {
+        // `at` counts a larger block's rows before the piece by their codes
+        const int r = (t.kt * kKeys) & (B - 1) & ~(kKeys - 1);
+        sc_at = t.at[sc_piece];
+        if (sc_at >= 0) sc_at += sc_src - (long long)r * (D / 2 - D / 16);
+        if (lane >= kScalePieces) sc_at = -1;
+      }
+      if (++next_ts == C::kAhead) {
+        next_ts = 0;
+        next_ph ^= 1u;
+      }
+      if (++next_tg == C::kTags) next_tg = 0;
+    };
+    auto fetch = [&]() {
+      if (more) {
+        const uint32_t slot = (uint32_t)(next_rs * R::kStage);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+          if (at[i] >= 0)
+            copy16(mine + slot + (uint32_t)((rl + kRowsStep * i) * R::kRowBytes + 16 * col),
+                   pool + src[i] + at[i]);
+        if constexpr (kFour)
+          if (sc_at >= 0) copy16(mine + slot + (uint32_t)(R::kCodes + 16 * lane), pool + sc_at);
+        if (++next_rs == R::kRing) next_rs = 0;
+      }
+      commit_copies();   // a group a stage, fetched or not
+    };
+    uint32_t chunk[kWords];
 #pragma unroll
     for (int j = 0; j < kWords; ++j) {
       const int k = kWords * col + (j ^ turn);   // 8 columns of the row
@@ -805,18 +865,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     // the two scale bytes of a row's piece, the first for the lane's first words
     const uint32_t pick = (uint32_t)(((turn & 2) ? 0x04 : 0x40) + 0x11 * (rl & 3));
-    int st = 0, rs = 0, tg = 0;
-    uint32_t ph = 0u, rph = 0u;
-    bool ok = true;
-    while (true) {
-      if (!wait_warp(c.empty[st], ph ^ 1u) || !wait_warp(c.rfull[rs], rph)) {
+    int st = 0, rs = 0, ts = 0, tg = 0;           // slots: operands, codes, barriers, tags
+    uint32_t ph = 0u;
+#pragma unroll 1
+    for (int k = 0; k < R::kRing; ++k) {
+      look();
+      fetch();
+    }
+    int flags = ok ? c.tag[0].flags : 0;
+    unsigned long long* const full = kv ? c.vfull : c.kfull;
+    while (ok) {
+      if (!wait_warp(c.empty[st], ph ^ 1u)) {
         ok = false;
         break;
       }
       Tag& t = c.tag[tg];
-      const int flags = t.flags;
-      if (flags & kStop) {
-        warp_arrive(c.full[st]);
+      if (flags & kStop) {   // the tag that ended the fetches
+        warp_arrive(full[st]);
         break;
       }
       if (flags & kFirst) {
@@ -878,103 +943,100 @@ __global__ void __launch_bounds__(kThreads, 1)
                     z[1], z[2], z[3]);
             }
           }
-          c.factor[t.part % C::kTags][k][x] = a.scale_log2 * back;
+          c.factor[t.part % (S + 1)][k][x] = a.scale_log2 * back;
         }
       }
-      // ---- the stage's keys and values to 16 bits
-      uint32_t live = 0xffffu;   // of the warp's 16 rows
-      if (flags & kEdge) live = t.rows[w >> 1] >> (16 * (w & 1));
-      uint32_t nan = 0u;
-      const uint32_t src = (uint32_t)(rs * R::kStage + kv * R::kHalf);
+      // ---- the stage's keys or values to 16 bits
+      wait_copies<R::kRing - 1>();
+      __syncwarp();   // every lane's copies have landed
+      const uint32_t f0 = from + (uint32_t)(rs * R::kStage);
       const uint32_t to = (uint32_t)st * X::kStage + (uint32_t)kv * X::kPart;
-      {
-        constexpr int kBatch = kRows;   // rows loaded at a time
+      uint32_t y[kRows][4], sc[kRows], odd = 0u;   // odd: bytes that are NaN
 #pragma unroll
-        for (int i0 = 0; i0 < kRows; i0 += kBatch) {
-          uint32_t y[kBatch][4];
-          uint32_t sc[kBatch];
+      for (int i = 0; i < kRows; ++i) {
+        if constexpr (kFour) {
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const uint32_t at = from[i0 + i] + src;
-            if constexpr (kFour) {
-              const uint2 s2 = lds8(scales[i0 + i] + src);
-              sc[i] = prmt(s2.x, s2.y, pick) & 0xffffu;
+          for (int j = 0; j < 4; ++j)
+            y[i][j] = lds4((f0 ^ (uint32_t)(4 * j)) + (uint32_t)(kRowsStep * i * R::kRowBytes));
+          const uint2 s2 = lds8(scales + (uint32_t)(rs * R::kStage) +
+                                (uint32_t)(kRowsStep * i / 4 * (D / 4)));
+          sc[i] = prmt(s2.x, s2.y, pick) & 0xffffu;
+          if (kv) odd |= nan_bytes(sc[i]);
+        } else {
 #pragma unroll
-              for (int j = 0; j < 4; ++j) y[i][j] = lds4(at ^ (uint32_t)(4 * j));
-            } else {
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint2 z = lds8(at ^ (uint32_t)(8 * j));
-                y[i][2 * j] = z.x;
-                y[i][2 * j + 1] = z.y;
-              }
-            }
+          for (int j = 0; j < 2; ++j) {
+            const uint2 z = lds8((f0 ^ (uint32_t)(8 * j)) + (uint32_t)(kRowsStep * i * R::kRowBytes));
+            y[i][2 * j] = z.x;
+            y[i][2 * j + 1] = z.y;
           }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i) {
-            const int rr = rl + kRowsStep * (i0 + i);   // of the warp's rows
-            const bool in = ((live >> rr) & 1u) != 0u;
-            const uint32_t up = to + (uint32_t)(kRowsStep * (i0 + i)) * 128u;
-            // rows 4 apart swap halves of the swizzle
-            const uint32_t flip = (kRowsStep * (i0 + i)) & 4 ? 64u : 0u;
-            if constexpr (kFour) {
-              if (!in) sc[i] = 0u;
-              if (kv == 1 && nan_bytes(sc[i])) {
-                nan |= 1u << rr;
-                sc[i] = 0u;
-              }
-              const uint32_t s = e4m3x2_to_f16x2(sc[i]);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t f[4];
-                e2m1x8_to_f16x2(y[i][j], f);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) f[e] = j < 2 ? hmul2_lo(f[e], s) : hmul2_hi(f[e], s);
-                sts16((chunk[j] ^ flip) + up, f[0], f[1], f[2], f[3]);
-              }
-            } else {
-              bool clear = !in;
-              if (kv == 1 && (nan_bytes(y[i][0]) | nan_bytes(y[i][1]) | nan_bytes(y[i][2]) |
-                              nan_bytes(y[i][3]))) {
-                if (in) nan |= 1u << rr;
-                clear = true;
-              }
-              if (clear) y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0u;
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                uint32_t f[4];
-                e4m3x4_to_f16x2x2(y[i][2 * j], f[0], f[1]);
-                e4m3x4_to_f16x2x2(y[i][2 * j + 1], f[2], f[3]);
-                sts16((chunk[j] ^ flip) + up, f[0], f[1], f[2], f[3]);
-              }
-            }
-          }
+          if (kv) odd |= nan_bytes(y[i][0]) | nan_bytes(y[i][1]) | nan_bytes(y[i][2]) |
+                         nan_bytes(y[i][3]);
         }
       }
-      if (__any_sync(0xffffffffu, nan != 0u)) {   // NaN among the values: rare
+      look();
+      const int tg1 = tg + 1 == C::kTags ? 0 : tg + 1;
+      const int flags1 = c.tag[tg1].flags;   // of the stage after this one
+      if ((flags & kEdge) || __any_sync(0xffffffffu, odd != 0u)) {
+        // rows that hold no data, and NaN among the values, become zeros: a weight
+        // of zero times NaN would reach rows that do not attend to them
+        const uint32_t live = (flags & kEdge) ? t.rows[w >> 1] >> (16 * (w & 1)) : 0xffffu;
+        uint32_t nan = 0u;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int rr = rl + kRowsStep * i;   // of the warp's rows
+          const bool in = ((live >> rr) & 1u) != 0u;
+          uint32_t bad = 0u;
+          if (kv)
+            bad = kFour ? nan_bytes(sc[i])
+                        : nan_bytes(y[i][0]) | nan_bytes(y[i][1]) | nan_bytes(y[i][2]) |
+                              nan_bytes(y[i][3]);
+          if (in && bad) nan |= 1u << rr;
+          if (!in || bad) sc[i] = y[i][0] = y[i][1] = y[i][2] = y[i][3] = 0u;
+        }
         nan = __reduce_or_sync(0xffffffffu, nan);
-        if (lane == 0) {
+        if (nan && lane == 0) {
           atomicOr(&t.mask[2 + (w >> 1)], nan << (16 * (w & 1)));
           atomicOr(&t.flags, kMarked);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        // rows 4 apart swap halves of the swizzle
+        const uint32_t flip = (kRowsStep * i) & 4 ? 64u : 0u;
+        uint32_t s = 0u;
+        if constexpr (kFour) s = e4m3x2_to_f16x2(sc[i]);
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          uint32_t f[4];
+          if constexpr (kFour) {
+            e2m1x8_to_f16x2(y[i][j], f);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = j < 2 ? hmul2_lo(f[e], s) : hmul2_hi(f[e], s);
+          } else {
+            e4m3x4_to_f16x2x2(y[i][2 * j], f[0], f[1]);
+            e4m3x4_to_f16x2x2(y[i][2 * j + 1], f[2], f[3]);
+          }
+          sts16((chunk[j] ^ flip) + to + (uint32_t)(kRowsStep * i * 128), f[0], f[1], f[2], f[3]);
         }
       }
       fence_proxy_async_smem();   // the operands, before the tensor core reads them
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(smem_u32(&c.full[st]));
-        mbar_arrive(smem_u32(&c.rempty[rs]));
+        mbar_arrive(smem_u32(&full[st]));
+        mbar_arrive(smem_u32(&c.tempty[ts]));
       }
-      if (++rs == R::kRing) {
-        rs = 0;
-        rph ^= 1u;
-      }
+      fetch();   // into the ring's place that is free now
+      if (++rs == R::kRing) rs = 0;
+      if (++ts == C::kAhead) ts = 0;
       if (++st == S) {
         st = 0;
         ph ^= 1u;
       }
-      if (++tg == C::kTags) tg = 0;
+      tg = tg1;
+      flags = flags1;
     }
     if (!ok && lane == 0) give_up();
+    wait_copies<0>();   // nothing lands in shared memory after the block's end
   } else {
     setmaxnreg_inc<kRegsSoftmax>();
     // ========================= softmax =========================
@@ -1018,7 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool valid = r < a.BM * a.G && tok_r < ntok;
           prow = valid ? p0 + tok_r : -1;
           busy = 32 * wq < ntok * a.G;
-          factor = c.factor[tg.part % C::kTags][other ? 1 : 0][r];
+          factor = c.factor[tg.part % (S + 1)][other ? 1 : 0][r];
           m_used = -INFINITY;
           l = 0.f;
           poison = false;
@@ -1332,7 +1394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kCopy) tmem_dealloc(tmem, 512);
+  if (warp == kTagger) tmem_dealloc(tmem, 512);
 }
 
 inline int check_prefill_shape(int Hq, int H, int D) {
@@ -1354,35 +1416,11 @@ inline size_t prefill_quant_bytes(int D, int grid) {
 }
 static_assert(2 * kMaxGrid * sizeof(uint32_t) <= PA_PREFILL_QUANT_COUNTERS, "two counters a block");
 
-// Boxes of `rows` rows of one head of one block of an E4M3 pool.
-inline int encode_rows8(CUtensorMap* map, const void* pool, int D, int B, int H, long long nb,
-                        int rows) {
-  const EncodeTiledFn fn = encode_tiled_fn();
-  if (!fn) {
-    note_cuda_error(1000, "cuTensorMapEncodeTiled is not available");
-    return PA_ERR_CUDA;
-  }
-  const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)B, (cuuint64_t)H, (cuuint64_t)nb};
-  const cuuint64_t strides[3] = {(cuuint64_t)H * D, (cuuint64_t)D, (cuuint64_t)B * H * D};
-  const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)rows, 1, 1};
-  const cuuint32_t step[4] = {1, 1, 1, 1};
-  const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(pool), dims,
-                        strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS) {
-    note_cuda_error(1000 + (int)r, "cuTensorMapEncodeTiled (E4M3 prefill)");
-    return PA_ERR_CUDA;
-  }
-  return PA_OK;
-}
-
 // The kernels' opt-in to their shared memory, once a device.
 constexpr int kMaxDevices = 64;
 
 template <int D, bool kBF16, bool kFour>
-int launch_prefill_quant(const CUtensorMap& tmk, const CUtensorMap& tmv, const Args& a, int grid,
-                         int device, cudaStream_t s) {
+int launch_prefill_quant(const Args& a, int grid, int device, cudaStream_t s) {
   static std::mutex mu;
   static bool ready[kMaxDevices];
   const auto kern = prefill_quant_kernel<D, kBF16, kFour>;
@@ -1402,7 +1440,7 @@ int launch_prefill_quant(const CUtensorMap& tmk, const CUtensorMap& tmv, const A
     }
   }
   clear_stale_error();
-  return launch_status(launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, s, tmk, tmv, a),
+  return launch_status(launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, s, a),
                        "quantized prefill launch");
 }
 
@@ -1463,19 +1501,11 @@ int prefill_quant(const void* q, const void* k_cache, const void* v_cache,
   a.v_scale = v_scale;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = q_dtype == PA_BF16;
-  CUtensorMap tmk{}, tmv{};
-  if (!kFour) {
-    const int rows = block_size < kKeys ? block_size : kKeys;
-    if (int rc = encode_rows8(&tmk, k_cache, head_dim, block_size, num_kv_heads, num_blocks, rows))
-      return rc;
-    if (int rc = encode_rows8(&tmv, v_cache, head_dim, block_size, num_kv_heads, num_blocks, rows))
-      return rc;
-  }
   if (head_dim == 64)
-    return bf16 ? launch_prefill_quant<64, true, kFour>(tmk, tmv, a, grid, di.device, s)
-                : launch_prefill_quant<64, false, kFour>(tmk, tmv, a, grid, di.device, s);
-  return bf16 ? launch_prefill_quant<128, true, kFour>(tmk, tmv, a, grid, di.device, s)
-              : launch_prefill_quant<128, false, kFour>(tmk, tmv, a, grid, di.device, s);
+    return bf16 ? launch_prefill_quant<64, true, kFour>(a, grid, di.device, s)
+                : launch_prefill_quant<64, false, kFour>(a, grid, di.device, s);
+  return bf16 ? launch_prefill_quant<128, true, kFour>(a, grid, di.device, s)
+              : launch_prefill_quant<128, false, kFour>(a, grid, di.device, s);
 }
 
 }  // namespace
