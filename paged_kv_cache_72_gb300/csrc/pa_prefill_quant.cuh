@@ -56,6 +56,7 @@ constexpr int kTagger = 18;
 constexpr int kValues = 19;
 constexpr int kThreads = 640;
 constexpr int kMaxGrid = 256;
+constexpr uint32_t kWaitCycles = 3800000000u;   // about 2 s, as every wait of the library
 // A pair's start and end cost what this many tokens do.
 constexpr int kStart = 128;
 // Small batches take a block for every kLeast of the line.
@@ -66,7 +67,7 @@ constexpr int kLeast = 384;
 constexpr float kShift = 7.f, kTop = 15.f, kTopPow = 32768.f;
 // Registers of the roles: softmax, conversion, the others (5 x 96 a thread).
 constexpr int kRegsLaunch = 96;
-constexpr int kRegsSoftmax = 144, kRegsConvert = 64, kRegsOther = 64;
+constexpr int kRegsSoftmax = 136, kRegsConvert = 72, kRegsOther = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsOther == 5 * kRegsLaunch,
               "the launch's registers");
 
@@ -147,7 +148,7 @@ struct Control {
   static constexpr int kAhead = kRing + 2 * kBatch;
   static constexpr int kTags = S + kAhead;
 
-  unsigned long long kfull[S], vfull[S], empty[S], tfull[kAhead], tempty[kAhead];
+  unsigned long long full[S], empty[S], tfull[kAhead], tempty[kAhead];
   unsigned long long qempty, bdone, done[3];
   unsigned long long tile[2][8];    // s full, s free, p full[2], p empty[2], o free
   alignas(16) Tag tag[kTags];
@@ -264,7 +265,7 @@ __device__ __forceinline__ int pairs_of(int L, const Args& a) {
 // The line's length of pairs 0 .. pr - 1 of a sequence with P of them (one KV
 // head): pair j ends with token T - L + min(2 BM (j + 1), L) and begins with the
 // first token its first row attends to.
-__device__ __forceinline__ long long line_before(long long pr, long long P, int L, int T,
+__device__ __noinline__ long long line_before(long long pr, long long P, int L, int T,
                                                  const Args& a) {
   const long long base = (long long)T - L, w = 2 * a.BM;
   long long sum = kStart * pr;
@@ -363,7 +364,6 @@ struct Walk {
     }
     pr = below;
     i0 = u0 - (rem - line_before(pr, P, L, T, a));
-    settle(a);
   }
 };
 
@@ -383,8 +383,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
 
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      mbar_init(smem_u32(&c.kfull[s]), 4);       // K's conversion warps
-      mbar_init(smem_u32(&c.vfull[s]), 4);       // V's
+      // the conversion warps: K's and V's, whose NaN the scores' softmax has to know
+      mbar_init(smem_u32(&c.full[s]), 8);
       // per tile: K read, V read, and its four softmax warps have read the tag
       mbar_init(smem_u32(&c.empty[s]), 2 * kShare);
     }
@@ -459,10 +459,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
   tc_fence_after();
   const uint32_t tmem = c.tmem;
 
-  // a wait whose outcome is the same in every lane of the warp
+  // a wait whose outcome is the same in every lane of the warp (every wait stands in
+  // line: it is kept short)
   auto wait_warp = [&](unsigned long long& bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait_bounded(smem_u32(&bar), parity,
-                                                     const_cast<volatile int*>(&c.abort))) != 0;
+    const uint32_t at = smem_u32(&bar);
+    if (__all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+    const uint32_t t0 = (uint32_t)clock();
+#pragma unroll 1
+    while (!__all_sync(0xffffffffu, mbar_try_wait(at, parity)))
+      if (c.abort != 0 || (uint32_t)clock() - t0 > kWaitCycles) return false;
+    return true;
   };
   auto give_up = [&]() {   // by one thread: the other roles leave on the flag
     if (!c.abort) set_error(a.err, PA_DEVERR_TIMEOUT);
@@ -490,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         return ok;
       };
       while (true) {
-        if (!wait(c.kfull[st], ph)) break;
+        if (!wait(c.full[st], ph)) break;
         const int flags = c.tag[tg].flags;
         if (flags & (act | kStop)) {
           // the softmax has read the scores (and their record) before these
@@ -503,8 +509,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
             break;
           }
           if (rt >= 2 && !wait(tb[kPEmpty + (rt & 1)], (uint32_t)((rt >> 1) - 1) & 1u)) break;
-          // tile B's queries come with the first values
-          if (t == 1 && (flags & (kFirst | kAlt)) == kFirst && !wait(c.vfull[st], ph)) break;
           if (lane == 0) {
             c.scores[t][rt & 3] = make_int4(flags, c.tag[tg].kt, st, tg);
             mbar_arrive(smem_u32(&tb[kSFull]));
@@ -558,7 +562,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         return __all_sync(0xffffffffu, mbar_test(smem_u32(&bar), parity)) != 0;
       };
       auto step = [&](int t, Cursor& k) -> bool {   // whether the tile went a stage on
-        if (k.done || !ready(c.vfull[k.st], k.ph)) return false;
+        if (k.done || !ready(c.full[k.st], k.ph)) return false;
         const int flags = c.tag[k.tg].flags;
         unsigned long long* const tb = c.tile[t];
         if (flags & kStop) {
@@ -628,7 +632,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
       constexpr int kRounds = kBatch * 16 / 32;
       const int lognblk = ilog2_device(nblk);
       int ents[kRounds];
+      bool begun = false;
       auto look = [&]() {
+        if (!begun || w.k >= w.k1) {   // the first part, or the next
+          if (begun) w.next_pair(a);
+          begun = true;
+          w.settle(a);
+        }
 #pragma unroll
         for (int u = 0; u < kRounds; ++u) {
           const int v = lane + 32 * u;
@@ -638,11 +648,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
             ents[u] = __ldg(a.bt + (size_t)w.i * a.stride + (t >> a.log2B));
         }
       };
-      look();
       int ts = 0, tg = 0, parts = 0, part = 0, nkt_a = 0;
       uint32_t ph = 0u;
       bool ok = true;
       while (true) {
+        look();
         const int m = w.done ? 1 : min(kBatch, w.k1 - w.k);   // stages of this batch
         for (int k = 0; k < m && ok; ++k) {
           const int b = ts + k;
@@ -758,11 +768,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         __syncwarp();
         if (lane < m) mbar_arrive(smem_u32(&c.tfull[bk]));
         w.k += m;
-        if (w.k >= w.k1) {
-          w.next_pair(a);
-          w.settle(a);
-        }
-        look();
         ts += m;
         if (ts >= C::kAhead) {
           ts -= C::kAhead;
@@ -800,9 +805,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
     const uint32_t scales = mine + (uint32_t)(R::kCodes + (rl >> 2) * (D / 4) + 8 * col);
     // the copies: this lane's bytes of its rows, behind the piece they lie in
     const uint8_t* const pool = kv ? a.vc : a.kc;
-    const long long row_bytes = kFour ? D / 2 : (long long)a.H * D;
-    int piece[kRows], sc_piece = 0;
-    long long src[kRows], sc_src = 0;
+    const int row_bytes = kFour ? D / 2 : a.H * D;   // (a block's bytes fit in 31 bits)
+    int piece[kRows], sc_piece = 0, src[kRows], sc_src = 0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int row = 16 * w + rl + kRowsStep * i;
@@ -815,44 +819,51 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
       sc_piece = (row & 63) >> log2s;
       sc_src = B * (D / 2) + (row & ((1 << log2s) - 1)) * (D / 16) + 16 * (lane % (D / 64));
     }
-    // Fetching a stage: its tag is looked at before the conversion of another, whose
-    // time hides the look, and the copies are issued behind it.
+    // Fetching a stage: its tag is looked at, on the chance that it is written, before
+    // the conversion of another, whose time hides the look; the copies are issued
+    // behind it.
     long long at[kRows], sc_at = -1;
     int next_rs = 0, next_ts = 0, next_tg = 0;    // of the stage to be fetched next
+    int next_flags = 0;
     uint32_t next_ph = 0u;
-    bool ok = true, more = true;
+    bool ok = true, more = true, written = false;
     auto look = [&]() {
-      if (!more) return;
-      ok = ok && wait_warp(c.tfull[next_ts], next_ph);
+      written = mbar_test(smem_u32(&c.tfull[next_ts]), next_ph);
       const Tag& t = c.tag[next_tg];
-      more = ok && !(t.flags & kStop);
-      if (!more) return;
+      next_flags = t.flags;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) at[i] = t.at[piece[i]];
       if constexpr (kFour) {
         // `at` counts a larger block's rows before the piece by their codes
         const int r = (t.kt * kKeys) & (B - 1) & ~(kKeys - 1);
         sc_at = t.at[sc_piece];
-        if (sc_at >= 0) sc_at += sc_src - (long long)r * (D / 2 - D / 16);
+        if (sc_at >= 0) sc_at += sc_src - r * (D / 2 - D / 16);
         if (lane >= kScalePieces) sc_at = -1;
       }
-      if (++next_ts == C::kAhead) {
-        next_ts = 0;
-        next_ph ^= 1u;
-      }
-      if (++next_tg == C::kTags) next_tg = 0;
     };
     auto fetch = [&]() {
+      if (more) {
+        if (!__all_sync(0xffffffffu, written)) {
+          ok = ok && wait_warp(c.tfull[next_ts], next_ph);
+          look();
+        }
+        more = ok && !(next_flags & kStop);
+      }
       if (more) {
         const uint32_t slot = (uint32_t)(next_rs * R::kStage);
 #pragma unroll
         for (int i = 0; i < kRows; ++i)
           if (at[i] >= 0)
             copy16(mine + slot + (uint32_t)((rl + kRowsStep * i) * R::kRowBytes + 16 * col),
-                   pool + src[i] + at[i]);
+                   pool + (at[i] + src[i]));
         if constexpr (kFour)
           if (sc_at >= 0) copy16(mine + slot + (uint32_t)(R::kCodes + 16 * lane), pool + sc_at);
         if (++next_rs == R::kRing) next_rs = 0;
+        if (++next_ts == C::kAhead) {
+          next_ts = 0;
+          next_ph ^= 1u;
+        }
+        if (++next_tg == C::kTags) next_tg = 0;
       }
       commit_copies();   // a group a stage, fetched or not
     };
@@ -869,19 +880,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
     uint32_t ph = 0u;
 #pragma unroll 1
     for (int k = 0; k < R::kRing; ++k) {
-      look();
+      written = false;
       fetch();
     }
     int flags = ok ? c.tag[0].flags : 0;
-    unsigned long long* const full = kv ? c.vfull : c.kfull;
+    bool free = false;   // the stage's operands, tried ahead
     while (ok) {
-      if (!wait_warp(c.empty[st], ph ^ 1u)) {
+      if (!__all_sync(0xffffffffu, free) && !wait_warp(c.empty[st], ph ^ 1u)) {
         ok = false;
         break;
       }
       Tag& t = c.tag[tg];
       if (flags & kStop) {   // the tag that ended the fetches
-        warp_arrive(full[st]);
+        warp_arrive(c.full[st]);
         break;
       }
       if (flags & kFirst) {
@@ -903,7 +914,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
           float back = 1.f, to = 1.f;
           if constexpr (kBF16) {
             float mx = 0.f;
-#pragma unroll
+#pragma unroll 1
             for (int j0 = 0; j0 < D / 8; j0 += 8) {
               uint4 y[8];
 #pragma unroll
@@ -924,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
             back = __uint_as_float((uint32_t)e << 23);
             to = __uint_as_float((uint32_t)(254 - e) << 23);
           }
-#pragma unroll
+#pragma unroll 1
           for (int j0 = 0; j0 < D / 8; j0 += 8) {
             uint4 y[8];
 #pragma unroll
@@ -947,6 +958,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         }
       }
       // ---- the stage's keys or values to 16 bits
+      look();
+      const int tg1 = tg + 1 == C::kTags ? 0 : tg + 1;
+      const int flags1 = c.tag[tg1].flags;   // of the stage after this one
       wait_copies<R::kRing - 1>();
       __syncwarp();   // every lane's copies have landed
       const uint32_t f0 = from + (uint32_t)(rs * R::kStage);
@@ -973,9 +987,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
                          nan_bytes(y[i][3]);
         }
       }
-      look();
-      const int tg1 = tg + 1 == C::kTags ? 0 : tg + 1;
-      const int flags1 = c.tag[tg1].flags;   // of the stage after this one
       if ((flags & kEdge) || __any_sync(0xffffffffu, odd != 0u)) {
         // rows that hold no data, and NaN among the values, become zeros: a weight
         // of zero times NaN would reach rows that do not attend to them
@@ -1022,7 +1033,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
       fence_proxy_async_smem();   // the operands, before the tensor core reads them
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive(smem_u32(&full[st]));
+        mbar_arrive(smem_u32(&c.full[st]));
         mbar_arrive(smem_u32(&c.tempty[ts]));
       }
       fetch();   // into the ring's place that is free now
@@ -1034,6 +1045,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
       }
       tg = tg1;
       flags = flags1;
+      free = mbar_test(smem_u32(&c.empty[st]), ph ^ 1u);
     }
     if (!ok && lane == 0) give_up();
     wait_copies<0>();   // nothing lands in shared memory after the block's end
