@@ -458,6 +458,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = c.tmem;
+  // (before the roles' registers are cut: it calls a function)
+  Walk w;
+  if (warp == kTagger) w.start(a, c.run_pref, per, c.bound[blockIdx.x], c.bound[blockIdx.x + 1]);
 
   // a wait whose outcome is the same in every lane of the warp (every wait stands in
   // line: it is kept short)
@@ -624,8 +627,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
                                           : (long long)B * a.H * D;
       const int head_bytes = kFour ? B * fp4_row_bytes(D) : D;
       const int row_bytes = kFour ? D / 2 : a.H * D;
-      Walk w;
-      w.start(a, c.run_pref, per, c.bound[blockIdx.x], c.bound[blockIdx.x + 1]);
       // Tags of up to kBatch stages of a part together, a lane each, and a table
       // entry a lane (in kRounds rounds), which is loaded a batch ahead: value v is
       // piece v % nblk of stage v / nblk
@@ -821,14 +822,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
     }
     // Fetching a stage: its tag is looked at, on the chance that it is written, before
     // the conversion of another, whose time hides the look; the copies are issued
-    // behind it.
+    // behind it.  The tag is read behind a branch on the test: loads that only stand
+    // behind it in the program were seen to return what was there before.
     long long at[kRows], sc_at = -1;
     int next_rs = 0, next_ts = 0, next_tg = 0;    // of the stage to be fetched next
     int next_flags = 0;
     uint32_t next_ph = 0u;
     bool ok = true, more = true, written = false;
-    auto look = [&]() {
-      written = mbar_test(smem_u32(&c.tfull[next_ts]), next_ph);
+    auto read_tag = [&]() {
       const Tag& t = c.tag[next_tg];
       next_flags = t.flags;
 #pragma unroll
@@ -841,11 +842,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         if (lane >= kScalePieces) sc_at = -1;
       }
     };
+    auto look = [&]() {
+      written = __all_sync(0xffffffffu, mbar_test(smem_u32(&c.tfull[next_ts]), next_ph)) != 0;
+      if (written) read_tag();
+    };
     auto fetch = [&]() {
       if (more) {
-        if (!__all_sync(0xffffffffu, written)) {
+        if (!written) {
           ok = ok && wait_warp(c.tfull[next_ts], next_ph);
-          look();
+          read_tag();
         }
         more = ok && !(next_flags & kStop);
       }

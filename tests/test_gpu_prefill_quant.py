@@ -278,6 +278,28 @@ def test_captured_and_replayed(four):
     assert pa.pa_get_error(c.err) == 0
 
 
+@POOLS
+def test_many_calls(four):
+    """Thousands of calls, in bursts: none gives up a wait, all give the same bits."""
+    chunks = [Chunks(21 + k, four, dt, 8, 2, D, 16, [33, 1, 1], [400, 3000, 9])
+              for k, (D, dt) in enumerate([(64, F16), (128, BF16)])]
+    ws = torch.zeros(pa.pa_prefill_quant_workspace_size(8, 2, 128), dtype=torch.uint8,
+                     device="cuda")
+    wants = [c.run(pa, workspace=ws).clone() for c in chunks]
+    outs = [torch.empty_like(c.q) for c in chunks]
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for step in range(1000):
+        for c, out, want in zip(chunks, outs, wants):
+            for _ in range(3):
+                c.run(pa, out=out, workspace=ws)
+            differ += (out != want).sum()
+        if step % 50 == 0:
+            torch.cuda.synchronize()
+    assert int(differ) == 0
+    for c in chunks:
+        assert pa.pa_get_error(c.err) == 0
+
+
 def test_two_streams():
     """Two calls at once, each with a workspace of its own."""
     cs = [Chunks(19 + i, bool(i), BF16, 8, 2, 128, 16, [40, 1], [700, 4000]) for i in range(2)]
