@@ -85,7 +85,14 @@ struct Args {
   long long num_blocks, total_q;
   int num_seqs, stride, Hq, H, G, BM, log2B, window;
   float scale_log2, v_scale;
+  int few;                  // which of the two kernels take sequences of few rows
+  uint32_t* few_count;      // [grid], zero between calls
+  float* few_rec;           // [grid][2] records of few_rec_floats(D)
 };
+// kFewNone: this kernel takes all sequences; kFewBoth: pa_prefill_few.cuh's those of
+// few rows; kFewOnly: it takes all
+enum : int { kFewNone, kFewBoth, kFewOnly };
+constexpr int kFewRows = 16;
 
 constexpr int kTileRows = 128;
 // o[128][D], m[128], l[128]
@@ -247,7 +254,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t x) {
 
 // Sequence i: its rows of q and its length; false (no tokens then) where they
 // contradict each other or the table.
-__device__ __forceinline__ bool load_seq(const Args& a, int i, int& q0, int& L, int& T) {
+__device__ __forceinline__ bool load_any(const Args& a, int i, int& q0, int& L, int& T) {
   const int s0 = __ldg(a.query_start + i), s1 = __ldg(a.query_start + i + 1);
   T = __ldg(a.seq_lens + i);
   const long long n = (long long)s1 - s0;
@@ -256,6 +263,27 @@ __device__ __forceinline__ bool load_seq(const Args& a, int i, int& q0, int& L, 
   q0 = s0;
   L = ok ? (int)n : 0;
   return ok;
+}
+
+// Of those, what the kernel with tiles of 128 rows takes.
+__device__ __forceinline__ bool load_seq(const Args& a, int i, int& q0, int& L, int& T) {
+  const bool ok = load_any(a, i, q0, L, T);
+  if (a.few == kFewBoth && (long long)L * a.G <= kFewRows) L = 0;
+  return ok;
+}
+
+// Sequences that contradict themselves: reported, their rows cleared.
+__device__ __forceinline__ void clear_bad(const Args& a, int D, int threads) {
+  for (int i = blockIdx.x; i < a.num_seqs; i += gridDim.x) {
+    int q0, L, T;
+    if (load_any(a, i, q0, L, T)) continue;
+    if (threadIdx.x == 0) set_error(a.err, PA_DEVERR_SEQ_LEN);
+    const long long r0 = max(q0, 0);
+    const long long r1 = min((long long)__ldg(a.query_start + i + 1), a.total_q);
+    uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)r0 * a.Hq * D);
+    for (long long e = threadIdx.x; e < (r1 - r0) * a.Hq * (D / 8); e += threads)
+      dst[e] = make_uint4(0u, 0u, 0u, 0u);
+  }
 }
 
 __device__ __forceinline__ int pairs_of(int L, const Args& a) {
@@ -436,18 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
   }
   c.run_pref[tid] = off + incl - mine;
   if (tid == 0) grid_dep_launch();
-  if (odd) {   // sequences that contradict themselves: reported, their rows cleared
-    for (int i = blockIdx.x; i < a.num_seqs; i += gridDim.x) {
-      int q0, L, T;
-      if (load_seq(a, i, q0, L, T)) continue;
-      if (tid == 0) set_error(a.err, PA_DEVERR_SEQ_LEN);
-      const long long r0 = max(q0, 0);
-      const long long r1 = min((long long)__ldg(a.query_start + i + 1), a.total_q);
-      uint4* dst = reinterpret_cast<uint4*>(a.out + (size_t)r0 * a.Hq * D);
-      for (long long e = tid; e < (r1 - r0) * a.Hq * (D / 8); e += kThreads)
-        dst[e] = make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
+  if (odd) clear_bad(a, D, kThreads);
   const long long nb = min((long long)gridDim.x, (total + kLeast - 1) / kLeast);
   if ((long long)blockIdx.x >= nb) return;
   if (tid <= nb) c.bound[tid] = total * tid / nb;
@@ -1414,6 +1431,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
   if (warp == kTagger) tmem_dealloc(tmem, 512);
 }
 
+}  // namespace
+
+}  // namespace pa
+
+#include "pa_prefill_few.cuh"
+
+namespace pa {
+
+namespace {
+
 inline int check_prefill_shape(int Hq, int H, int D) {
   if (Hq <= 0 || H <= 0 || Hq % H != 0) return PA_ERR_INVALID_ARG;
   if (D != 64 && D != 128) return PA_ERR_UNSUPPORTED;
@@ -1428,10 +1455,22 @@ inline int prefill_quant_grid(int* grid) {
   return PA_OK;
 }
 
-inline size_t prefill_quant_bytes(int D, int grid) {
+// The workspace: counters of this kernel, then of the other; records of this one,
+// four a block, then of the other, two a block.
+constexpr size_t kFewCounters = PA_PREFILL_QUANT_COUNTERS / 2;
+inline size_t few_records_at(int D, int grid) {
   return PA_PREFILL_QUANT_COUNTERS + (size_t)grid * 4 * rec_floats(D) * sizeof(float);
 }
-static_assert(2 * kMaxGrid * sizeof(uint32_t) <= PA_PREFILL_QUANT_COUNTERS, "two counters a block");
+inline size_t prefill_quant_bytes(int D, int grid) {
+  return few_records_at(D, grid) +
+         (size_t)kFewBlocks * grid * 2 * few_rec_floats(D) * sizeof(float);
+}
+static_assert(2 * kMaxGrid * sizeof(uint32_t) <= kFewCounters &&
+                  kFewBlocks * kMaxGrid * sizeof(uint32_t) <= PA_PREFILL_QUANT_COUNTERS - kFewCounters,
+              "a block's counters");
+
+// Average rows a sequence up to which a batch is split between the two kernels.
+constexpr int kFewAverage = 192;
 
 // The kernels' opt-in to their shared memory, once a device.
 constexpr int kMaxDevices = 64;
@@ -1441,8 +1480,9 @@ int launch_prefill_quant(const Args& a, int grid, int device, cudaStream_t s) {
   static std::mutex mu;
   static bool ready[kMaxDevices];
   const auto kern = prefill_quant_kernel<D, kBF16, kFour>;
-  constexpr size_t smem = smem_bytes<D, kFour>();
-  static_assert(smem <= 227 * 1024, "a block's shared memory");
+  const auto few = prefill_few_kernel<D, kBF16, kFour>;
+  constexpr size_t smem = smem_bytes<D, kFour>(), few_smem = sizeof(FewShared<D, kFour>);
+  static_assert(smem <= 227 * 1024 && kFewBlocks * few_smem <= 224 * 1024, "a block's shared memory");
   {
     std::lock_guard<std::mutex> lk(mu);
     if (!ready[device]) {
@@ -1453,12 +1493,19 @@ int launch_prefill_quant(const Args& a, int grid, int device, cudaStream_t s) {
       if (e) return launch_status(e, "cudaFuncSetAttribute (quantized prefill)");
       // the roles re-divide the launch's registers, which the increases wait for
       if (at.numRegs != kRegsLaunch) return PA_ERR_UNSUPPORTED;
+      e = cudaFuncSetAttribute(few, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)few_smem);
+      if (e) return launch_status(e, "cudaFuncSetAttribute (quantized prefill of few rows)");
       ready[device] = true;
     }
   }
   clear_stale_error();
-  return launch_status(launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, s, a),
-                       "quantized prefill launch");
+  if (a.few != kFewOnly)
+    if (int rc = launch_status(launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), smem, s, a),
+                               "quantized prefill launch"))
+      return rc;
+  if (a.few == kFewNone) return PA_OK;
+  return launch_status(launch_pdl(few, dim3((unsigned)(kFewBlocks * grid)), dim3(kFewThreads), few_smem, s, a),
+                       "quantized prefill launch (few rows)");
 }
 
 template <bool kFour>
@@ -1516,6 +1563,17 @@ int prefill_quant(const void* q, const void* k_cache, const void* v_cache,
   a.window = window;
   a.scale_log2 = scale * k_scale * 1.4426950408889634f;
   a.v_scale = v_scale;
+  // Sequences of few rows have a kernel of their own.  If even all of total_q in one
+  // would be one, it is the only one; where the average of the sequences is not far
+  // beyond, both run (their lengths are on the device); else there are hardly any.  48
+  // single tokens among 64 sequences, 144 rows on average: 181 us, 268 with this kernel
+  // alone; 7 chunks of 247 rows on average: 84 us with both, 79 with this one.
+  const long long rows = (long long)total_q * a.G;
+  a.few = rows <= kFewRows ? kFewOnly
+                           : (rows <= (long long)kFewAverage * num_seqs ? kFewBoth : kFewNone);
+  a.few_count = a.ws_count + kFewCounters / sizeof(uint32_t);
+  a.few_rec = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                       few_records_at(head_dim, grid));
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf16 = q_dtype == PA_BF16;
   if (head_dim == 64)

@@ -278,6 +278,96 @@ def test_captured_and_replayed(four):
     assert pa.pa_get_error(c.err) == 0
 
 
+# Sequences of few rows (tokens times heads of a KV head), alone and beside others: they have
+# a kernel of their own.
+
+@POOLS
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=["fp16", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,H", [(1, 1), (3, 3), (8, 2), (7, 1), (16, 1), (24, 3)])
+def test_few_rows(four, dtype, D, Hq, H):
+    G = Hq // H
+    most = 16 // G
+    lens = [1, 2, 31, 32, 33, 95, 128, 700, 2500]
+    new = [min(T, 1 + i % most) for i, T in enumerate(lens)]
+    check(Chunks(31, four, dtype, Hq, H, D, 16, new, lens))
+    check(Chunks(32, four, dtype, Hq, H, D, 16, [most], [1000]))
+    check(Chunks(33, four, dtype, Hq, H, D, 16, [0, 1, most + 1, 0, most, 40], [0, 77, 300, 5, 90, 70]))
+
+
+@POOLS
+@pytest.mark.parametrize("B", [4, 8, 32, 64, 256])
+@pytest.mark.parametrize("window", [0, 1, 31, 33, 500])
+def test_few_rows_blocks_and_windows(four, B, window):
+    check(Chunks(34, four, BF16, 4, 2, 128, B, [1, 3, 8, 2, 1], [600, 3, 41, 1300, 32],
+                 window=window))
+
+
+@POOLS
+@pytest.mark.parametrize("D", [64, 128])
+def test_few_rows_of_many_sequences(four, D):
+    rng = np.random.default_rng(35)
+    lens = rng.integers(1, 200, 700)
+    new = np.minimum(rng.integers(0, 5, 700), lens)
+    check(Chunks(35, four, F16, 4, 2, D, 16, new, lens))
+
+
+@POOLS
+@pytest.mark.parametrize("window", [0, 20])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("t", [70, 150, 155])
+def test_few_rows_nan_reaches_its_readers_alone(four, window, which, t):
+    c = Chunks(36, four, BF16, 2, 1, 128, 16, [8], [160], window=window)
+    want, tol = c.reference()
+    b, r = int(c.bt[0, t // 16]), t % 16
+    if b < 0:
+        return                                        # before every row's window
+    pool = getattr(c, which)
+    if four:
+        pool.view(pool.shape[0], 1, -1)[b, 0, 16 * 64 + (r // 4) * 32 + r % 4] = 0x7F
+    else:
+        pool[b, r, 0, 3] = 0xFF
+    out = c.run(pa)
+    p = torch.arange(152, 160, device="cuda")
+    hit = (p >= t) & (p < t + window if window else p >= 0)
+    assert bool(out[hit].isnan().all())
+    assert_within(out[~hit], want[~hit], tol[~hit])
+    assert pa.pa_get_error(c.err) == 0
+
+
+@POOLS
+@pytest.mark.parametrize("B", [4, 16, 128])
+def test_few_rows_bad_table_entries_are_left_out(four, B):
+    c = Chunks(37, four, BF16, 4, 2, 64, B, [3, 2], [400, 300])
+    nb = c.k.shape[0]
+    left = {}
+    for i, cols in {0: [1, 399 // B], 1: [0, 150 // B]}.items():
+        for n, b in enumerate(cols):
+            c.bt[i, b] = -5 if (i + n) % 2 else nb
+            left.setdefault(i, set()).update(range(b * B, (b + 1) * B))
+    out = c.run(pa)
+    assert pa.pa_get_error(c.err) == pa.PA_DEVERR_BLOCK_ID
+    want, tol = c.reference(left_out=left)
+    assert_within(out, want, tol)
+    c.bt[1] = -1
+    out = c.run(pa)
+    assert pa.pa_get_error(c.err) == pa.PA_DEVERR_BLOCK_ID
+    assert bool((out[3:5] == 0).all())
+
+
+@POOLS
+def test_few_rows_bad_lengths(four):
+    """One sequence that contradicts itself: its rows cleared, the others unharmed."""
+    c = Chunks(38, four, F16, 4, 4, 64, 16, [2, 1, 3], [40, 50, 60])
+    want, tol = c.reference()
+    c.lens[1] = -7
+    out = c.run(pa)
+    assert pa.pa_get_error(c.err) == pa.PA_DEVERR_SEQ_LEN
+    assert bool((out[2] == 0).all())
+    keep = [0, 1, 3, 4, 5]
+    assert_within(out[keep], want[keep], tol[keep])
+
+
 @POOLS
 def test_many_calls(four):
     """Thousands of calls, in bursts: none gives up a wait, all give the same bits."""
