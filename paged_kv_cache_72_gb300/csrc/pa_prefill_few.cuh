@@ -82,14 +82,6 @@ struct FewShared {
   alignas(128) uint8_t data[kRings > kSums ? kRings : kSums];
 };
 
-__device__ __forceinline__ uint4 lds16(uint32_t addr) {
-  uint4 r;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "r"(addr));
-  return r;
-}
-
 // A sequence's tiles of one KV head: from the one with its first attended token; 0
 // where it has no new tokens or more rows than are dealt with here.
 __device__ __forceinline__ int few_tiles(const Args& a, int i, int& q0, int& L, int& T,

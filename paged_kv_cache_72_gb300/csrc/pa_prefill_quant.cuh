@@ -21,7 +21,8 @@
 //    copies: a TMA copy cost its issuing warp 200 to 300 cycles, and a stage of
 //    16-token blocks takes eight), and turn them into 16-bit operands with the
 //    128-byte swizzle.  With a part's first stage they bring the query rows of
-//    tile A and of tile B in, as binary16.
+//    tile A and of tile B in, whole rows a copy (a row a thread took 7 us a part),
+//    and turn them into binary16 where they lie.
 //  * warps 16 and 17 (a tile each): S = Q K^T of a stage;
 //  * warp 19 (both tiles): O += P V, P from tensor memory.
 //  * warps 0-3 (tile A) and 4-7 (tile B): thread r owns row r, tensor memory
@@ -32,7 +33,7 @@
 // the same rows and end with partial results, which tile A's warps join.
 //
 // The split.  The pairs of all sequences and KV heads, in that order, are a line
-// on which a pair is kStart + (its attended tokens) long; it is cut into equal
+// on which a pair is `start` + (its attended tokens) long; it is cut into equal
 // shares, one a block.  A pair cut between blocks leaves one record (O, m, l) a
 // tile and block in the workspace, and the last block to count its record joins
 // them, always in the order of the keys: no block waits for another, and the
@@ -57,8 +58,11 @@ constexpr int kValues = 19;
 constexpr int kThreads = 640;
 constexpr int kMaxGrid = 256;
 constexpr uint32_t kWaitCycles = 3800000000u;   // about 2 s, as every wait of the library
-// A pair's start and end cost what this many tokens do.
-constexpr int kStart = 128;
+// A pair's start and end cost what this many tokens do.  bfloat16 queries, which are
+// scaled, against binary16 ones, us with 128 / 384: 16 chunks of 512 over 4 bits 569 /
+// 494, 64 sequences over E4M3 159 / 145, 4 prompts of 2,048 232 / 208; 7 chunks with a
+// window over E4M3 76 / 80, 20 chunks of head_dim 64 127 / 130 (both binary16).
+constexpr int kStart[2] = {128, 384};   // binary16, bfloat16
 // Small batches take a block for every kLeast of the line.
 constexpr int kLeast = 384;
 // The exponentials' reference is a maximum less kShift when it is set and stays
@@ -85,6 +89,7 @@ struct Args {
   long long num_blocks, total_q;
   int num_seqs, stride, Hq, H, G, BM, log2B, window;
   float scale_log2, v_scale;
+  int start;                // what a pair's start and end cost, in tokens
   int few;                  // which of the two kernels take sequences of few rows
   uint32_t* few_count;      // [grid], zero between calls
   float* few_rec;           // [grid][2] records of few_rec_floats(D)
@@ -206,6 +211,13 @@ template <int kPending>
 __device__ __forceinline__ void wait_copies() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 r;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+               : "r"(addr));
+  return r;
+}
 __device__ __forceinline__ uint2 lds8(uint32_t addr) {
   uint2 r;
   asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(addr));
@@ -296,7 +308,7 @@ __device__ __forceinline__ int pairs_of(int L, const Args& a) {
 __device__ __noinline__ long long line_before(long long pr, long long P, int L, int T,
                                                  const Args& a) {
   const long long base = (long long)T - L, w = 2 * a.BM;
-  long long sum = kStart * pr;
+  long long sum = a.start * pr;
   if (pr < P) sum += pr * base + w * (pr * (pr + 1) / 2);
   else if (P > 0) sum += (P - 1) * base + w * ((P - 1) * P / 2) + T;
   if (a.window > 0) {   // less the sum of max(0, base + w j - window + 1)
@@ -309,9 +321,9 @@ __device__ __noinline__ long long line_before(long long pr, long long P, int L, 
 
 // The first stage of a pair that begins at or behind `at` on the line, counted
 // from the pair's place (stages are 64 keys on from token 0; a pair's first one
-// stands at kStart).
-__device__ __forceinline__ int stage_at(long long at, int lo, int nkt) {
-  const long long r = at - kStart;
+// stands at `start`).
+__device__ __forceinline__ int stage_at(long long at, int lo, int nkt, int start) {
+  const long long r = at - start;
   if (r <= 0) return lo / kKeys;
   const long long k = (lo + r + kKeys - 1) / kKeys;
   return k < nkt ? (int)k : nkt;
@@ -325,7 +337,9 @@ struct Walk {
   long long i0, u0, u1;        // the pair's place; the block's share
   bool done;
 
-  __device__ __forceinline__ long long length() const { return (long long)kStart + end - lo; }
+  __device__ __forceinline__ long long length(const Args& a) const {
+    return (long long)a.start + end - lo;
+  }
   __device__ __forceinline__ int nkt() const { return (end - 1) / kKeys + 1; }
 
   // from the pair on to the next stage there is
@@ -339,15 +353,15 @@ struct Walk {
       end = (int)(base + min(w * (pr + 1), (long long)L));
       const long long first = base + w * pr - a.window + 1;
       lo = a.window > 0 && first > 0 ? (int)first : 0;
-      k0 = stage_at(u0 - i0, lo, nkt());
-      k1 = stage_at(u1 - i0, lo, nkt());
+      k0 = stage_at(u0 - i0, lo, nkt(), a.start);
+      k1 = stage_at(u1 - i0, lo, nkt(), a.start);
       k = k0;
       if (k0 < k1) return;
       next_pair(a);
     }
   }
   __device__ __forceinline__ void next_pair(const Args& a) {
-    i0 += length();
+    i0 += length(a);
     if (++pr < P) return;
     pr = 0;
     if (++h < a.H) return;
@@ -730,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
             t.nkt_a = nkt_a;
             t.nkt = nkt;
             t.i0 = w.i0;
-            t.len = w.length();
+            t.len = w.length(a);
           }
           ++parts;
         }
@@ -802,7 +816,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
     const int x = tid & 127;                        // thread of the warpgroup
     const int w = warp & 3;                         // rows 16 w .. of a stage
     const int kv = (warp - kConvert) >> 2;          // K or V, tile A's queries or B's
-    const int tok_r = x / a.G, head_r = x % a.G;    // of this thread's query row
+    const uint32_t inv_g = (65535u + (uint32_t)a.G) / (uint32_t)a.G;   // row / G, row < 128
     const int B = 1 << a.log2B, log2s = min(a.log2B, 6);
     // A lane's pieces: 16 bytes of kRows rows, as words (8 codes of 4 bits) or
     // double words (8 codes of 8 bits), each of which becomes one 16-byte chunk of
@@ -922,61 +936,67 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
           ok = false;
           break;
         }
-        // ---- query rows: thread x row x of a tile, as binary16.  A bfloat16
-        // row is brought into binary16's range by a power of two (its largest
-        // magnitude into [1, 2)), which its score factor takes back; elements
-        // 2^-14 below the largest lose bits below 2^-24 of it.
+        // ---- a warp's 32 query rows of a tile, a few whole rows a copy
         if (kv == 0 || t.ntok_b > 0) {
-          const int k = kv;
-          const bool valid = x < a.BM * a.G && tok_r < (k ? t.ntok_b : t.ntok_a);
-          const uint4* const src = reinterpret_cast<const uint4*>(
-              a.q + ((size_t)(valid ? t.q0 + k * a.BM + tok_r : 0) * a.Hq +
-                     (valid ? t.h * a.G + head_r : 0)) * D);
-          const uint32_t dst = qtiles + (uint32_t)k * X::kQTile + (uint32_t)x * 128u;
-          float back = 1.f, to = 1.f;
+          const uint32_t qt = qtiles + (uint32_t)kv * X::kQTile;
+          const int rows = (kv ? t.ntok_b : t.ntok_a) * a.G;
+          constexpr int kChunks = D / 8, kStep = 32 / kChunks;   // of 16 bytes; rows a copy
+          const int qc = lane % kChunks;
+          const uint16_t* const src =
+              a.q + ((size_t)(t.q0 + kv * a.BM) * a.Hq + (size_t)t.h * a.G) * D + 8 * qc;
+#pragma unroll 2
+          for (int i = 0; i < 32; i += kStep) {
+            const int row = 32 * w + i + lane / kChunks;
+            const uint32_t dst = qt + (uint32_t)(qc >> 3) * X::kQPlane + (uint32_t)row * 128u +
+                                 (uint32_t)((qc ^ row) & 7) * 16u;
+            const int tok = (int)((uint32_t)row * inv_g >> 16);
+            if (row < rows)
+              copy16(dst, reinterpret_cast<const uint8_t*>(
+                              src + ((size_t)tok * (a.Hq - a.G) + row) * D));
+            else sts16(dst, 0u, 0u, 0u, 0u);
+          }
+          commit_copies();
+          wait_copies<0>();
+          __syncwarp();
+          float back = 1.f;
           if constexpr (kBF16) {
+            // A bfloat16 row is brought into binary16's range, where it lies, by a
+            // power of two (its largest magnitude into [1, 2)), which its score
+            // factor takes back; elements 2^-14 below the largest lose bits below
+            // 2^-24 of it.  Thread x holds row x.
+            const uint32_t at = qt + (uint32_t)x * 128u;
             float mx = 0.f;
-#pragma unroll 1
-            for (int j0 = 0; j0 < D / 8; j0 += 8) {
-              uint4 y[8];
+#pragma unroll 4
+            for (int j = 0; j < D / 8; ++j) {
+              const uint4 y = lds16(at + (uint32_t)(j >> 3) * X::kQPlane +
+                                    (uint32_t)((j ^ x) & 7) * 16u);
+              const uint32_t z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-              for (int j = 0; j < 8; ++j) y[j] = valid ? __ldg(src + j0 + j) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const uint32_t z[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float2 f = unpack2<true>(z[e]);
-                  mx = max3f(mx, fabsf(f.x), fabsf(f.y));
-                }
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack2<true>(z[e]);
+                mx = max3f(mx, fabsf(f.x), fabsf(f.y));
               }
             }
             // 2^e <= mx < 2^(e+1); zero, subnormal or infinite maxima keep a
             // factor whose inverse is a normal number
             const int e = min(max((int)(__float_as_uint(mx) >> 23), 1), 253);
             back = __uint_as_float((uint32_t)e << 23);
-            to = __uint_as_float((uint32_t)(254 - e) << 23);
-          }
-#pragma unroll 1
-          for (int j0 = 0; j0 < D / 8; j0 += 8) {
-            uint4 y[8];
+            const float to = __uint_as_float((uint32_t)(254 - e) << 23);
+#pragma unroll 4
+            for (int j = 0; j < D / 8; ++j) {
+              const uint32_t p = at + (uint32_t)(j >> 3) * X::kQPlane +
+                                 (uint32_t)((j ^ x) & 7) * 16u;
+              const uint4 y = lds16(p);
+              uint32_t z[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = valid ? __ldg(src + j0 + j) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              uint32_t z[4] = {y[j].x, y[j].y, y[j].z, y[j].w};
-              if constexpr (kBF16) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float2 f = unpack2<true>(z[e]);
-                  z[e] = pack2<false>(f.x * to, f.y * to);
-                }
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = unpack2<true>(z[e]);
+                z[e] = pack2<false>(f.x * to, f.y * to);
               }
-              sts16(dst + (uint32_t)(j0 >> 3) * X::kQPlane + (uint32_t)((j ^ x) & 7) * 16u, z[0],
-                    z[1], z[2], z[3]);
+              sts16(p, z[0], z[1], z[2], z[3]);
             }
           }
-          c.factor[t.part % (S + 1)][k][x] = a.scale_log2 * back;
+          c.factor[t.part % (S + 1)][kv][x] = a.scale_log2 * back;
         }
       }
       // ---- the stage's keys or values to 16 bits
@@ -1333,8 +1353,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
                 const int b = b0 + lane;
                 bool in = false, begins = false;
                 if (b <= e) {
-                  const int s0 = stage_at(c.bound[b] - i0, lo, nkt_t);
-                  in = s0 < stage_at(c.bound[b + 1] - i0, lo, nkt_t);
+                  const int s0 = stage_at(c.bound[b] - i0, lo, nkt_t, a.start);
+                  in = s0 < stage_at(c.bound[b + 1] - i0, lo, nkt_t, a.start);
                   begins = s0 == lo / kKeys;
                 }
                 const uint32_t all = __ballot_sync(0xffffffffu, in);
@@ -1563,6 +1583,7 @@ int prefill_quant(const void* q, const void* k_cache, const void* v_cache,
   a.window = window;
   a.scale_log2 = scale * k_scale * 1.4426950408889634f;
   a.v_scale = v_scale;
+  a.start = kStart[q_dtype == PA_BF16 ? 1 : 0];
   // Sequences of few rows have a kernel of their own.  If even all of total_q in one
   // would be one, it is the only one; where the average of the sequences is not far
   // beyond, both run (their lengths are on the device); else there are hardly any.  48
