@@ -1587,8 +1587,8 @@ int prefill_quant(const void* q, const void* k_cache, const void* v_cache,
   // Sequences of few rows have a kernel of their own.  If even all of total_q in one
   // would be one, it is the only one; where the average of the sequences is not far
   // beyond, both run (their lengths are on the device); else there are hardly any.  48
-  // single tokens among 64 sequences, 144 rows on average: 181 us, 268 with this kernel
-  // alone; 7 chunks of 247 rows on average: 84 us with both, 79 with this one.
+  // single tokens among 64 sequences, 144 rows on average: 147 us, 174 with the other
+  // kernel alone; 7 chunks of 247 rows on average: 82 us with both, 77 with that one.
   const long long rows = (long long)total_q * a.G;
   a.few = rows <= kFewRows ? kFewOnly
                            : (rows <= (long long)kFewAverage * num_seqs ? kFewBoth : kFewNone);
