@@ -38,6 +38,16 @@
 // tile and block in the workspace, and the last block to count its record joins
 // them, always in the order of the keys: no block waits for another, and the
 // result depends on nobody's speed.
+//
+// What bounds it.  Products at the tensor cores' rate are the floor of long chunks; the
+// conversion comes before it: a stage is one chain a warp (wait for the place, codes
+// from shared memory, conversion, stores, fence, arrival, the next copies) of some
+// 1,700 cycles, and beside two query tiles of 32 KB (head_dim 128) three stages fit,
+// or six of head_dim 64.  Measured: 1,024 new tokens at 31,744 of an E4M3 cache, 64
+// query and 8 KV heads of 128, 1,005 us (1,079 TFLOP/s); 16 chunks of 512 over 4 bits,
+// 32 and 8 heads, 493 us (961 TFLOP/s); 32 contexts of 16 to 33 K tokens over 4 bits
+// with four new tokens each, 64 and 8 heads, 599 us (1.6 TB/s: a quarter of the
+// rows are in use); 7 ragged chunks of up to 277 with a window of 512, 79 us.
 #pragma once
 
 #include <cmath>
@@ -63,13 +73,14 @@ constexpr uint32_t kWaitCycles = 3800000000u;   // about 2 s, as every wait of t
 // 494, 64 sequences over E4M3 159 / 145, 4 prompts of 2,048 232 / 208; 7 chunks with a
 // window over E4M3 76 / 80, 20 chunks of head_dim 64 127 / 130 (both binary16).
 constexpr int kStart[2] = {128, 384};   // binary16, bfloat16
-// Small batches take a block for every kLeast of the line.
+// Small batches take a block for every kLeast of the line (256 and 768: within 1%).
 constexpr int kLeast = 384;
 // The exponentials' reference is a maximum less kShift when it is set and stays
 // until a weight would pass 2^kTop: binary16 holds weights down to 2^-14 - kShift
 // of the maximum with all their bits.
 constexpr float kShift = 7.f, kTop = 15.f, kTopPow = 32768.f;
-// Registers of the roles: softmax, conversion, the others (5 x 96 a thread).
+// Registers of the roles: softmax, conversion, the others (5 x 96 a thread; 8 to 44
+// bytes a thread are spilled).
 constexpr int kRegsLaunch = 96;
 constexpr int kRegsSoftmax = 136, kRegsConvert = 72, kRegsOther = 64;
 static_assert(2 * kRegsSoftmax + 2 * kRegsConvert + kRegsOther == 5 * kRegsLaunch,
