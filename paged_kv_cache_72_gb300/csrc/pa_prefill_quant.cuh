@@ -111,7 +111,7 @@ enum : int { kFewNone, kFewBoth, kFewOnly };
 constexpr int kFewRows = 16;
 
 constexpr int kTileRows = 128;
-// o[128][D], m[128], l[128]
+// o[D / 4][128][4] (a warp's 32 rows lie together), m[128], l[128]
 __host__ __device__ constexpr size_t rec_floats(int D) { return (size_t)kTileRows * (D + 2); }
 
 // A conversion warp's 16 rows of K or V: the rows' codes one after the other, then
@@ -1339,7 +1339,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
               } else if (prow >= 0) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                  *reinterpret_cast<uint4*>(rec + (size_t)r * D + cc + 4 * e) =
+                  *reinterpret_cast<uint4*>(rec + 4 * ((cc / 4 + e) * kTileRows + r)) =
                       make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
               }
               __syncwarp();
@@ -1387,8 +1387,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
             group_sync(1 + tile);
             if (c.last[tile]) {
               // ---- the last record: join them all, in the order of the keys.  A
-              // thread finds its row's maximum and sum, then takes vectors of rows
-              constexpr int kLanes = D / 4, kAhead = 4;
+              // thread finds its row's maximum and sum, then takes vectors of rows: a
+              // warp four neighbouring ones of eight rows
+              constexpr int kAhead = 4, kHalves = D / 64;
               const int n = c.nparts[tile], rows = ntok * a.G;
               const float* const recs = a.ws_rec + (size_t)tile * rec_floats(D);
               auto record = [&](int k) {
@@ -1407,8 +1408,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
                 c.join[tile][r][1] = ls == 0.f ? 0.f : a.v_scale / ls;
               }
               group_sync(1 + tile);
-              const int col = 4 * (r % kLanes);
-              for (int r0 = r / kLanes; r0 < rows; r0 += kAhead * (128 / kLanes)) {
+              for (int u = 0; u < (rows + 31) / 32 * kHalves; ++u) {
+                const int r0 = 32 * (u / kHalves) + (lane & 7);
+                const int vec = 16 * (u % kHalves) + 4 * wq + (lane >> 3), col = 4 * vec;
                 float4 acc[kAhead];
 #pragma unroll
                 for (int b = 0; b < kAhead; ++b) acc[b] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1418,13 +1420,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
                   float w[kAhead];
 #pragma unroll
                   for (int b = 0; b < kAhead; ++b) {
-                    const int rr = min(r0 + b * (128 / kLanes), rows - 1);
-                    v[b] = __ldcg(reinterpret_cast<const float4*>(p + (size_t)rr * D + col));
+                    const int rr = min(r0 + 8 * b, rows - 1);
+                    v[b] = __ldcg(reinterpret_cast<const float4*>(p + 4 * (vec * kTileRows + rr)));
                     w[b] = __ldcg(p + (size_t)kTileRows * D + rr);
                   }
 #pragma unroll
                   for (int b = 0; b < kAhead; ++b) {
-                    const int rr = min(r0 + b * (128 / kLanes), rows - 1);
+                    const int rr = min(r0 + 8 * b, rows - 1);
                     const float f = ex2_approx(w[b] - c.join[tile][rr][0]);
                     acc[b].x = fmaf(v[b].x, f, acc[b].x);
                     acc[b].y = fmaf(v[b].y, f, acc[b].y);
@@ -1434,7 +1436,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
                 }
 #pragma unroll
                 for (int b = 0; b < kAhead; ++b) {
-                  const int rr = r0 + b * (128 / kLanes);
+                  const int rr = r0 + 8 * b;
                   if (rr >= rows) break;
                   const float mul = c.join[tile][rr][1];
                   const int tok = rr / a.G;
