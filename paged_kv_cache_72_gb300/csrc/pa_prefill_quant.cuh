@@ -44,10 +44,10 @@
 // from shared memory, conversion, stores, fence, arrival, the next copies) of some
 // 1,700 cycles, and beside two query tiles of 32 KB (head_dim 128) three stages fit,
 // or six of head_dim 64.  Measured: 1,024 new tokens at 31,744 of an E4M3 cache, 64
-// query and 8 KV heads of 128, 1,005 us (1,079 TFLOP/s); 16 chunks of 512 over 4 bits,
-// 32 and 8 heads, 493 us (961 TFLOP/s); 32 contexts of 16 to 33 K tokens over 4 bits
+// query and 8 KV heads of 128, 998 us (1,085 TFLOP/s); 16 chunks of 512 over 4 bits,
+// 32 and 8 heads, 488 us (968 TFLOP/s); 32 contexts of 16 to 33 K tokens over 4 bits
 // with four new tokens each, 64 and 8 heads, 599 us (1.6 TB/s: a quarter of the
-// rows are in use); 7 ragged chunks of up to 277 with a window of 512, 79 us.
+// rows are in use); 7 ragged chunks of up to 277 with a window of 512, 76 us.
 #pragma once
 
 #include <cmath>
@@ -69,9 +69,10 @@ constexpr int kThreads = 640;
 constexpr int kMaxGrid = 256;
 constexpr uint32_t kWaitCycles = 3800000000u;   // about 2 s, as every wait of the library
 // A pair's start and end cost what this many tokens do.  bfloat16 queries, which are
-// scaled, against binary16 ones, us with 128 / 384: 16 chunks of 512 over 4 bits 569 /
-// 494, 64 sequences over E4M3 159 / 145, 4 prompts of 2,048 232 / 208; 7 chunks with a
-// window over E4M3 76 / 80, 20 chunks of head_dim 64 127 / 130 (both binary16).
+// scaled, against binary16 ones, us with 128 / 384, in an earlier form: 16 chunks of 512
+// over 4 bits 569 / 494, 64 sequences over E4M3 159 / 145, 4 prompts of 2,048 232 /
+// 208; 7 chunks with a window over E4M3 76 / 80, 20 chunks of head_dim 64 127 / 130
+// (both binary16).
 constexpr int kStart[2] = {128, 384};   // binary16, bfloat16
 // Small batches take a block for every kLeast of the line (256 and 768: within 1%).
 constexpr int kLeast = 384;
@@ -1600,7 +1601,7 @@ int prefill_quant(const void* q, const void* k_cache, const void* v_cache,
   // Sequences of few rows have a kernel of their own.  If even all of total_q in one
   // would be one, it is the only one; where the average of the sequences is not far
   // beyond, both run (their lengths are on the device); else there are hardly any.  48
-  // single tokens among 64 sequences, 144 rows on average: 147 us, 174 with the other
+  // single tokens among 64 sequences, 144 rows on average: 143 us, some 170 with the other
   // kernel alone; 7 chunks of 247 rows on average: 82 us with both, 77 with that one.
   const long long rows = (long long)total_q * a.G;
   a.few = rows <= kFewRows ? kFewOnly
