@@ -19,9 +19,9 @@
 // tokens of 32 and 32 heads (80 MB): 16.6 us.  A step of 256 tokens takes 3.9 us,
 // one of four 2.1.  A norm costs 8,192 tokens' stores into quantized pools 3 to 4
 // us (E4M3 36.9 for 34.0, 4-bit 40.5 for 36.6).  With positions of three axes the
-// 8,192 tokens take 43 us for 37.0 (every token's angles come from up to four rows
-// of the table), the 1,939 16.6 for 16.6, 32 tokens into a 4-bit pool 6.2 with the
-// read-back, four 3.4.
+// 8,192 tokens take 43 us for 37.0 (a token's angles come from several rows of the
+// table), 1,727 of 32 and 32 heads into an E4M3 pool 16.8, 32 into a 4-bit pool 6.2
+// with the read-back, four 3.8.
 //
 // A row (one head of one token) is held by D / 8 lanes of 16 bytes each, so
 // loads and stores are whole 16-byte vectors and the rotation's partner element
