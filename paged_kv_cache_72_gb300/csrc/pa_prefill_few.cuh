@@ -224,12 +224,14 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) prefill_few_kernel(co
         }
       }
       // ---- this warp's tiles: k0 + warp, every fourth
-      auto entries = [&](int k) -> int {   // lane j: the j-th block of tile k
+      // lane j: the j-th block of tile k; -2: no row of it is attended to; every negative
+      // entry of the table is -1
+      auto entries = [&](int k) -> int {
         const int t0 = (first / kTile + k) * kTile, idx = (t0 >> a.log2B) + lane;
         if (k >= k1 || lane >= max(kTile >> a.log2B, 1) || idx < (first >> a.log2B) ||
             idx > ((T - 1) >> a.log2B))
           return -2;
-        return __ldg(a.bt + (size_t)i * a.stride + idx);
+        return max(__ldg(a.bt + (size_t)i * a.stride + idx), -1);
       };
       uint32_t missing = 0u;   // a bit a ring slot: some row's block is not there
       uint32_t bads[X::kStages];   // rows whose block is out of range

@@ -689,7 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
           const int k = w.k + (v >> lognblk), t = k * kKeys + (v & (nblk - 1)) * bs;
           ents[u] = -2;   // no row of it is attended to
           if (!w.done && v < kBatch * nblk && k < w.k1 && t + bs - 1 >= w.lo && t < w.end)
-            ents[u] = __ldg(a.bt + (size_t)w.i * a.stride + (t >> a.log2B));
+            // (every negative entry is -1, none of them the mark above)
+            ents[u] = max(__ldg(a.bt + (size_t)w.i * a.stride + (t >> a.log2B)), -1);
         }
       };
       int ts = 0, tg = 0, parts = 0, part = 0, nkt_a = 0;
