@@ -224,21 +224,21 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) prefill_few_kernel(co
         }
       }
       // ---- this warp's tiles: k0 + warp, every fourth
-      // lane j: the j-th block of tile k; -2: no row of it is attended to; every negative
-      // entry of the table is -1
+      // lane j: the j-th block of tile k, and whether a row of it is attended to (apart from
+      // the entry, which may hold anything and is not waited for here)
+      bool need = false;
       auto entries = [&](int k) -> int {
         const int t0 = (first / kTile + k) * kTile, idx = (t0 >> a.log2B) + lane;
-        if (k >= k1 || lane >= max(kTile >> a.log2B, 1) || idx < (first >> a.log2B) ||
-            idx > ((T - 1) >> a.log2B))
-          return -2;
-        return max(__ldg(a.bt + (size_t)i * a.stride + idx), -1);
+        need = k < k1 && lane < max(kTile >> a.log2B, 1) && idx >= (first >> a.log2B) &&
+               idx <= ((T - 1) >> a.log2B);
+        return need ? __ldg(a.bt + (size_t)i * a.stride + idx) : -1;
       };
       uint32_t missing = 0u;   // a bit a ring slot: some row's block is not there
       uint32_t bads[X::kStages];   // rows whose block is out of range
       int next = k0 + warp, ent = entries(next);
       auto issue = [&](int slot) {
         const int t0 = (first / kTile + next) * kTile;
-        const bool bad = ent != -2 && (ent < 0 || (long long)ent >= a.num_blocks);
+        const bool bad = need && (ent < 0 || (long long)ent >= a.num_blocks);
         if (bad) {
           set_error(a.err, PA_DEVERR_BLOCK_ID);
           ent = -1;

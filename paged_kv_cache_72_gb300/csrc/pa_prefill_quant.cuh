@@ -676,6 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
       constexpr int kRounds = kBatch * 16 / 32;
       const int lognblk = ilog2_device(nblk);
       int ents[kRounds];
+      bool need[kRounds];
       bool begun = false;
       auto look = [&]() {
         if (!begun || w.k >= w.k1) {   // the first part, or the next
@@ -687,10 +688,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         for (int u = 0; u < kRounds; ++u) {
           const int v = lane + 32 * u;
           const int k = w.k + (v >> lognblk), t = k * kKeys + (v & (nblk - 1)) * bs;
-          ents[u] = -2;   // no row of it is attended to
-          if (!w.done && v < kBatch * nblk && k < w.k1 && t + bs - 1 >= w.lo && t < w.end)
-            // (every negative entry is -1, none of them the mark above)
-            ents[u] = max(__ldg(a.bt + (size_t)w.i * a.stride + (t >> a.log2B)), -1);
+          // whether a row of it is attended to (an entry that is needed may hold anything)
+          need[u] = !w.done && v < kBatch * nblk && k < w.k1 && t + bs - 1 >= w.lo && t < w.end;
+          ents[u] = need[u] ? __ldg(a.bt + (size_t)w.i * a.stride + (t >> a.log2B)) : -1;
         }
       };
       int ts = 0, tg = 0, parts = 0, part = 0, nkt_a = 0;
@@ -723,8 +723,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         for (int u = 0; u < kRounds; ++u) {
           const int v = lane + 32 * u, ent = ents[u];
           const bool on = ent >= 0 && (long long)ent < a.num_blocks;
-          if (ent != -2 && !on) set_error(a.err, PA_DEVERR_BLOCK_ID);
-          want[u] = __ballot_sync(0xffffffffu, ent != -2);
+          if (need[u] && !on) set_error(a.err, PA_DEVERR_BLOCK_ID);
+          want[u] = __ballot_sync(0xffffffffu, need[u]);
           got[u] = __ballot_sync(0xffffffffu, on);
           const int sv = v >> lognblk;
           if (sv < m) {
