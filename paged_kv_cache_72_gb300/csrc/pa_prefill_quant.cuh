@@ -175,6 +175,7 @@ struct Control {
   unsigned long long full[S], empty[S], tfull[kAhead], tempty[kAhead];
   unsigned long long qempty, bdone, done[3];
   unsigned long long tile[2][8];    // s full, s free, p full[2], p empty[2], o free
+  unsigned long long met[2];        // a tile's softmax warps
   alignas(16) Tag tag[kTags];
   // of a part's rows: what scores are multiplied by; before the first part, the
   // line before each thread's run of sequences
@@ -267,10 +268,6 @@ __device__ __forceinline__ void warp_arrive(unsigned long long& bar) {
   if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(&bar));
 }
 __device__ __forceinline__ int ilog2_device(int x) { return 31 - __clz(x); }
-// the 128 threads of a warpgroup
-__device__ __forceinline__ void group_sync(int id) {
-  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
-}
 // bytes of E4M3 codes that are NaN: 0x80 in their place
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t x) {
   return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
@@ -457,6 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         mbar_init(smem_u32(&c.tile[t][kPEmpty + p]), 1);
       }
       mbar_init(smem_u32(&c.tile[t][kOFree]), 4);
+      mbar_init(smem_u32(&c.met[t]), 4);
     }
     c.abort = 0;
     fence_barrier_init();
@@ -1121,7 +1119,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
     float factor = 0.f, m_used = -INFINITY, l = 0.f;
     bool poison = false;
     bool ok = true;
-    int nt = 0, nb_alt = 0;   // scores read, pairs in turn joined
+    int nt = 0, nb_alt = 0, nm = 0;   // scores read, pairs in turn joined, meetings
+    // The tile's four warps wait for one another, with a limit: a warp whose wait ran out
+    // has left, and one that looked at the same barrier a moment later has not (a named
+    // barrier would hold it for good).
+    auto meet = [&]() {
+      warp_arrive(c.met[tile]);
+      return wait_warp(c.met[tile], (uint32_t)nm++ & 1u);
+    };
     while (true) {
       if (!wait_warp(tb[kSFull], (uint32_t)nt & 1u)) {
         ok = false;
@@ -1355,7 +1360,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
               rec[(size_t)kTileRows * D + r] = m_used;
               rec[(size_t)kTileRows * (D + 1) + r] = l;
             }
-            group_sync(1 + tile);
+            if (!meet()) {
+              ok = false;
+              break;
+            }
             // the records of this tile: the blocks that hold stages of it
             if (wq == 0) {
               int f = blockIdx.x, e = blockIdx.x;
@@ -1378,7 +1386,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
               }
               if (lane == 0) {
                 c.nparts[tile] = n;
-                // releases this tile's record (ordered before by the barrier),
+                // releases this tile's record (ordered before by the meeting),
                 // acquires those counted before it
                 uint32_t* const cnt = a.ws_count + 2 * end + tile;
                 const bool last = atom_add_acq_rel_gpu(cnt, 1u) + 1u == (uint32_t)n;
@@ -1386,7 +1394,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
                 c.last[tile] = last ? 1 : 0;
               }
             }
-            group_sync(1 + tile);
+            if (!meet()) {
+              ok = false;
+              break;
+            }
             if (c.last[tile]) {
               // ---- the last record: join them all, in the order of the keys.  A
               // thread finds its row's maximum and sum, then takes vectors of rows: a
@@ -1409,7 +1420,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
                 c.join[tile][r][0] = m == -INFINITY ? 0.f : m;
                 c.join[tile][r][1] = ls == 0.f ? 0.f : a.v_scale / ls;
               }
-              group_sync(1 + tile);
+              if (!meet()) {
+                ok = false;
+                break;
+              }
               for (int u = 0; u < (rows + 31) / 32 * kHalves; ++u) {
                 const int r0 = 32 * (u / kHalves) + (lane & 7);
                 const int vec = 16 * (u % kHalves) + 4 * wq + (lane >> 3), col = 4 * vec;
