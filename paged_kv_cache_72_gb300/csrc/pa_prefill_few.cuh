@@ -62,6 +62,12 @@ struct FewTile {
   }
 };
 
+// A context: a sequence and KV head, and its place on the line.
+struct FewContext {
+  int i, q0, L, T, first, nt, h;
+  long long i0;
+};
+
 template <int D, bool kFour>
 struct FewShared {
   uint2 q[D / 16][kColumns][32];     // query fragments
@@ -72,6 +78,7 @@ struct FewShared {
   long long bound[kFewBlocks * kMaxGrid + 1];
   uint16_t parts[kFewBlocks * kMaxGrid];
   int nparts, last;
+  FewContext context[2];             // this one and the next, in turn
   float ml[kFewWarps][2][kFewRows];
   float join[kFewRows][2];
   int bad[kFewRows];                 // a NaN among the row's sums
@@ -138,29 +145,58 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) prefill_few_kernel(co
   __syncthreads();
   const long long u0 = c.bound[blockIdx.x], u1 = c.bound[blockIdx.x + 1];
 
-  // ---- the context at place u0 (every thread walks alike) -------------------
-  int i = 0;
-  {
+  // ---- the context at place u0.  One thread walks and the block takes what it found:
+  // lengths that change during the call then cannot part the block's threads.
+  if (tid == 0) {
+    FewContext x{};
     int r = 0;   // the last run that starts at or before u0
 #pragma unroll
     for (int b = 256; b > 0; b >>= 1)
       if (r + b < kFewThreads && c.run_pref[r + b] <= u0) r += b;
-    i = r * per;
+    x.i = r * per;
+    x.i0 = c.run_pref[r];
+    while (x.i < a.num_seqs) {
+      x.nt = few_tiles(a, x.i, x.q0, x.L, x.T, x.first);
+      const long long one = x.nt > 0 ? (long long)(x.nt + kStartTiles) * a.H : 0;
+      if (u0 < x.i0 + one) break;
+      x.i0 += one;
+      ++x.i;
+    }
+    if (x.i < a.num_seqs) {
+      x.h = (int)((u0 - x.i0) / (x.nt + kStartTiles));
+      x.i0 += (long long)x.h * (x.nt + kStartTiles);
+    }
+    c.context[0] = x;
   }
-  long long i0 = c.run_pref[per > 0 ? min(i / per, kFewThreads - 1) : 0];
-  int nt = 0;
-  while (i < a.num_seqs) {
-    nt = few_tiles(a, i, q0, L, T, first);
-    const long long one = nt > 0 ? (long long)(nt + kStartTiles) * a.H : 0;
-    if (u0 < i0 + one) break;
-    i0 += one;
-    ++i;
-  }
-  int h = 0;
-  if (i < a.num_seqs) {
-    h = (int)((u0 - i0) / (nt + kStartTiles));
-    i0 += (long long)h * (nt + kStartTiles);
-  }
+  __syncthreads();
+  int turn = 0, i = 0, h = 0, nt = 0;
+  long long i0 = 0;
+  auto take = [&]() {
+    const FewContext& x = c.context[turn];
+    i = x.i;
+    q0 = x.q0;
+    L = x.L;
+    T = x.T;
+    first = x.first;
+    nt = x.nt;
+    h = x.h;
+    i0 = x.i0;
+  };
+  take();
+  // The next context, by thread 0, once a turn of the loop below, before a barrier of it:
+  // the block takes it behind that one, and is done with the other place before it.
+  auto walk_on = [&]() {
+    if (tid != 0) return;
+    FewContext x = c.context[turn];
+    x.i0 += x.nt + kStartTiles;
+    if (++x.h == a.H) {
+      x.h = 0;
+      x.nt = 0;
+      while (x.nt == 0 && ++x.i < a.num_seqs)
+        x.nt = few_tiles(a, x.i, x.q0, x.L, x.T, x.first);
+    }
+    c.context[turn ^ 1] = x;
+  };
   const uint32_t ring = smem_u32(c.data) + (uint32_t)(warp * X::kStages * X::kStage);
   const size_t block_bytes = kFour ? (size_t)a.H * B * fp4_row_bytes(D) : (size_t)B * a.H * D;
 
@@ -288,6 +324,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) prefill_few_kernel(co
         if (next < k1) issue(k);
         commit_copies();
       }
+      walk_on();
       __syncthreads();   // the fragments, factors and positions
       float o[kColumns][D / 16][4], l[kColumns][4], base[kColumns][2], sl[kColumns][2];
       bool poison[kColumns][2];
@@ -736,14 +773,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) prefill_few_kernel(co
           __syncthreads();
         }
       }
+    } else {
+      walk_on();
+      __syncthreads();
     }
-    // the next context
-    i0 += nt + kStartTiles;
-    if (++h == a.H) {
-      h = 0;
-      nt = 0;
-      while (nt == 0 && ++i < a.num_seqs) nt = few_tiles(a, i, q0, L, T, first);
-    }
+    turn ^= 1;
+    take();
   }
 }
 

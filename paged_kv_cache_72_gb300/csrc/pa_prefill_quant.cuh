@@ -293,6 +293,15 @@ __device__ __forceinline__ bool load_seq(const Args& a, int i, int& q0, int& L, 
   return ok;
 }
 
+// The same by a whole warp, which goes on with one lane's words: lengths that change
+// during the call then cannot part its lanes.
+__device__ __forceinline__ void load_seq_warp(const Args& a, int i, int& q0, int& L, int& T) {
+  load_seq(a, i, q0, L, T);
+  q0 = __shfl_sync(0xffffffffu, q0, 0);
+  L = __shfl_sync(0xffffffffu, L, 0);
+  T = __shfl_sync(0xffffffffu, T, 0);
+}
+
 // Sequences that contradict themselves: reported, their rows cleared.
 __device__ __forceinline__ void clear_bad(const Args& a, int D, int threads) {
   for (int i = blockIdx.x; i < a.num_seqs; i += gridDim.x) {
@@ -338,7 +347,7 @@ __device__ __forceinline__ int stage_at(long long at, int lo, int nkt, int start
   return k < nkt ? (int)k : nkt;
 }
 
-// A place in a block's share of the line.
+// A place in a block's share of the line (a warp's).
 struct Walk {
   int i, q0, L, T, P;          // sequence
   int h, pr, lo, end;          // pair: first attended token, end of the attended ones
@@ -377,7 +386,7 @@ struct Walk {
     h = 0;
     P = 0;
     while (P == 0 && ++i < a.num_seqs) {
-      load_seq(a, i, q0, L, T);
+      load_seq_warp(a, i, q0, L, T);
       P = pairs_of(L, a);
     }
   }
@@ -394,7 +403,7 @@ struct Walk {
     long long rem = u0 - run_pref[r], one = 0;
     i = r * per;
     while (i < a.num_seqs) {
-      load_seq(a, i, q0, L, T);
+      load_seq_warp(a, i, q0, L, T);
       P = pairs_of(L, a);
       one = line_before(P, P, L, T, a);
       if (rem < one * a.H) break;
