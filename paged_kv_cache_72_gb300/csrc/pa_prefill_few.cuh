@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) prefill_few_kernel(co
       // the entry, which may hold anything and is not waited for here)
       bool need = false;
       auto entries = [&](int k) -> int {
-        const int t0 = (first / kTile + k) * kTile, idx = (t0 >> a.log2B) + lane;
+        const int t0 = (int)((uint32_t)(first / kTile + k) * kTile);   // (k < k1: in range)
+        const int idx = (t0 >> a.log2B) + lane;
         need = k < k1 && lane < max(kTile >> a.log2B, 1) && idx >= (first >> a.log2B) &&
                idx <= ((T - 1) >> a.log2B);
         return need ? __ldg(a.bt + (size_t)i * a.stride + idx) : -1;
@@ -348,7 +349,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) prefill_few_kernel(co
         __syncwarp();
         const int t0 = (first / kTile + k) * kTile;
         const uint32_t kt = ring + (uint32_t)(slot * X::kStage), vt = kt + X::kHalf;
-        const bool edge = ((missing >> slot) & 1u) || t0 + kTile - 1 > T - L ||
+        const bool edge = ((missing >> slot) & 1u) || t0 + (kTile - 1) > T - L ||
                           (a.window > 0 && (long long)t0 < (long long)T - a.window);
         // ---- S^T = K Q^T
         float s[2][kColumns][4];

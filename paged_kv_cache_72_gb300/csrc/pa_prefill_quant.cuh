@@ -694,9 +694,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
 #pragma unroll
         for (int u = 0; u < kRounds; ++u) {
           const int v = lane + 32 * u;
-          const int k = w.k + (v >> lognblk), t = k * kKeys + (v & (nblk - 1)) * bs;
+          const int k = w.k + (v >> lognblk);
+          const int t = (int)((uint32_t)k * kKeys) + (v & (nblk - 1)) * bs;   // (k < k1: in range)
           // whether a row of it is attended to (an entry that is needed may hold anything)
-          need[u] = !w.done && v < kBatch * nblk && k < w.k1 && t + bs - 1 >= w.lo && t < w.end;
+          need[u] = !w.done && v < kBatch * nblk && k < w.k1 && t > w.lo - bs && t < w.end;
           ents[u] = need[u] ? __ldg(a.bt + (size_t)w.i * a.stride + (t >> a.log2B)) : -1;
         }
       };
@@ -791,7 +792,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         mine = (mine >> (v0 & 31)) & all;
         wanted = (wanted >> (v0 & 31)) & all;
         uint4 mask = make_uint4(0u, 0u, 0u, 0u);
-        if (kt * kKeys + kKeys > w.end || mine != all) {
+        const int live = w.end - kt * kKeys;   // keys before the pair's end
+        if (live < kKeys || mine != all) {
           // rows that hold data, and rows of blocks that are out of range
           uint64_t rows = 0ull, bad = 0ull;
           for (int b = 0; b < nblk; ++b) {
@@ -799,7 +801,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
             if ((mine >> b) & 1u) rows |= bits;
             else if ((wanted >> b) & 1u) bad |= bits;
           }
-          const int live = w.end - kt * kKeys;   // keys before the pair's end
           if (live < kKeys) {
             rows &= (1ull << live) - 1ull;
             bad &= (1ull << live) - 1ull;
@@ -1199,7 +1200,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
         // A stage that all rows attend to needs no mask, and once the row has a
         // reference no maximum either: every P is at most their sum, so a sum of
         // at most 2^kTop shows that the reference stays.
-        const bool plain = t0 + kKeys - 1 <= p0 && (flags & kMarked) == 0 &&
+        const bool plain = t0 + (kKeys - 1) <= p0 && (flags & kMarked) == 0 &&
                            (a.window == 0 || (long long)t0 > (long long)p0 + ntok - 1 - a.window);
         const bool raw = plain && factor > 0.f;
         const bool guess = raw && m_used != -INFINITY;
