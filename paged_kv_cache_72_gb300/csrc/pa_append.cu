@@ -20,8 +20,10 @@
 // one of four 2.1.  A norm costs 8,192 tokens' stores into quantized pools 3 to 4
 // us (E4M3 36.9 for 34.0, 4-bit 40.5 for 36.6).  With positions of three axes the
 // 8,192 tokens take 43 us for 37.0 (a token's angles come from several rows of the
-// table), 1,727 of 32 and 32 heads into an E4M3 pool 16.8, 32 into a 4-bit pool 6.2
-// with the read-back, four 3.8.
+// table, and a norm's form spills up to 200 bytes a thread to hold them), 46.7 into a
+// 4-bit pool (40.6 with one position), 42.5 into an E4M3 pool (36.9); 1,358 of 32 and 32
+// heads, whole heads rotated, axes in turn, into an E4M3 pool 16.8 (with inputs repeated
+// 14.0, with one position 12.7), 32 into a 4-bit pool 6.2 with the read-back, four 3.4.
 //
 // A row (one head of one token) is held by D / 8 lanes of 16 bytes each, so
 // loads and stores are whole 16-byte vectors and the rotation's partner element
@@ -374,14 +376,6 @@ __device__ __forceinline__ void store_row(uint8_t* pool, const uint4& x, long lo
 constexpr int kBatch = 4;
 constexpr int kBlocks = 7;
 
-// One warp per token and share of its rows: query rows, then key rows with their
-// value rows, each D / 8 lanes wide.  The angles are loaded once per lane and
-// used for all of the share's rows; a norm's weights are multiplied into them, so
-// that a normed row costs one multiplication more than a plain one.  The first
-// rows of each kind are loaded before the token's slot is known.  A warp, not a
-// block, per token: slot, angles and weights cost a warp some 400 instructions
-// and three dependent loads, once for 24 passes of rows instead of four times
-// (50 us with a block per token, 42 with a warp at the same six blocks an SM).
 // Whether token `tok` can be rotated with axes: its positions, which `at` receives,
 // lie in the table, and every frequency's axis is one of them (every lane of the
 // warp takes part; a row's lanes read all of axis_of between them).
@@ -401,6 +395,14 @@ __device__ __forceinline__ bool axes_ok(const AppendArgs& a, long long tok, long
   return __all_sync(0xffffffffu, ok) != 0;
 }
 
+// One warp per token and share of its rows: query rows, then key rows with their
+// value rows, each D / 8 lanes wide.  The angles are loaded once per lane and
+// used for all of the share's rows; a norm's weights are multiplied into them, so
+// that a normed row costs one multiplication more than a plain one.  The first
+// rows of each kind are loaded before the token's slot is known.  A warp, not a
+// block, per token: slot, angles and weights cost a warp some 400 instructions
+// and three dependent loads, once for 24 passes of rows instead of four times
+// (50 us with a block per token, 42 with a warp at the same six blocks an SM).
 // kAxes: the angles of each frequency from the position on its axis.
 template <int D, bool kBF16, int kPool, bool kNorm, bool kAxes>
 __global__ void __launch_bounds__(kThreads, kBlocks)

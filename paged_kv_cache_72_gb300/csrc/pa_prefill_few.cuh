@@ -10,10 +10,15 @@
 // with four columns 32 rows took 1,000 us where the other kernel takes 597.
 //
 // Measured, 32 contexts of 16 to 33 K tokens, 64 query and 8 KV heads of 128 (the other
-// kernel: 600 us each): one new token 304 us over E4M3 (5.5 TB/s), 297 over 4 bits (3.1
+// kernel: 600 us each): one new token 305 us over E4M3 (5.4 TB/s), 285 over 4 bits (3.3
 // TB/s: the conversion's instructions and their latencies with 8 warps an SM), two
-// tokens 332 and 329.  For rows of one column alone 16 warps an SM took 288 and 223 us,
+// tokens 332 and 316.  For rows of one column alone 16 warps an SM took 288 and 223 us,
 // but two tokens then 608.
+//
+// The weights are one binary16 value each (2^-11), as in the other kernel, so that a
+// call's rows are alike: binary16 outputs are 2.8e-4 off 64 bits in norm (2.1e-4 is their
+// own rounding), bfloat16 ones 1.7e-3 with either.  A pair of values, as the 4-bit decode
+// has, takes second products: one token 336 us over E4M3 and 325 over 4 bits, two 372 and 371.
 //
 //  * The tiles of all (sequence, KV head) contexts are a line, kStartTiles and one
 //    for each tile a context, cut into equal shares, one a block.  The warps

@@ -13,6 +13,15 @@
 // bits, E2M1 times its scale 6), so the products run on the fifth-generation
 // tensor cores in binary16 with fp32 sums in tensor memory.
 //
+// The weights are one binary16 value each (2^-11), as the chunks over 16-bit pools hold
+// one value of the query's type: binary16 outputs are 2.8e-4 off 64 bits in norm (2.1e-4
+// is their own rounding), bfloat16 ones 1.7e-3 with either.  A pair of values, as the
+// 4-bit decode has, takes a second product and, tensor memory being full (64 columns of
+// scores, 64 of weights, 128 of values a tile of head_dim 128), leaves one place for
+// weights instead of two.  Built and measured, us for the pair / for one value: 16 chunks of
+// 512 over 4 bits 640 / 486, the 32 K prompt 1,289 / 993, 32 verified contexts 749 / 600,
+// chunks of 400 and head_dim 64 151 / 130.
+//
 // Roles of a block of 20 warps, one block an SM:
 //  * warp 18 walks the block's share of the work and writes a tag for every stage
 //    of 64 keys: what is to be done with it, and where its blocks lie.
@@ -44,9 +53,9 @@
 // from shared memory, conversion, stores, fence, arrival, the next copies) of some
 // 1,700 cycles, and beside two query tiles of 32 KB (head_dim 128) three stages fit,
 // or six of head_dim 64.  Measured: 1,024 new tokens at 31,744 of an E4M3 cache, 64
-// query and 8 KV heads of 128, 998 us (1,085 TFLOP/s); 16 chunks of 512 over 4 bits,
+// query and 8 KV heads of 128, 994 us (1,090 TFLOP/s); 16 chunks of 512 over 4 bits,
 // 32 and 8 heads, 488 us (968 TFLOP/s); 32 contexts of 16 to 33 K tokens over 4 bits
-// with four new tokens each, 64 and 8 heads, 599 us (1.6 TB/s: a quarter of the
+// with four new tokens each, 64 and 8 heads, 601 us (1.6 TB/s: a quarter of the
 // rows are in use); 7 ragged chunks of up to 277 with a window of 512, 76 us.
 #pragma once
 
@@ -69,10 +78,11 @@ constexpr int kThreads = 640;
 constexpr int kMaxGrid = 256;
 constexpr uint32_t kWaitCycles = 3800000000u;   // about 2 s, as every wait of the library
 // A pair's start and end cost what this many tokens do.  bfloat16 queries, which are
-// scaled, against binary16 ones, us with 128 / 384, in an earlier form: 16 chunks of 512
-// over 4 bits 569 / 494, 64 sequences over E4M3 159 / 145, 4 prompts of 2,048 232 /
-// 208; 7 chunks with a window over E4M3 76 / 80, 20 chunks of head_dim 64 127 / 130
-// (both binary16).
+// scaled, us with 128 / 256 / 384: 16 chunks of 512 over 4 bits 565 / 516 / 485, 64
+// sequences over E4M3 157 / 147 / 142, 4 prompts of 2,048 230 / 212 / 203, 7 chunks with
+// a window 77 / 78 / 79, 20 of head_dim 64 159 / 159 / 157.  Binary16 ones: 534 / 493 /
+// 491, 144 / 138 / 137, 207 / 191 / 195, 74 / 76 / 77, 130 / 130 / 132: short pairs
+// decided, the long ones would take 256.
 constexpr int kStart[2] = {128, 384};   // binary16, bfloat16
 // Small batches take a block for every kLeast of the line (256 and 768: within 1%).
 constexpr int kLeast = 384;
@@ -80,7 +90,7 @@ constexpr int kLeast = 384;
 // until a weight would pass 2^kTop: binary16 holds weights down to 2^-14 - kShift
 // of the maximum with all their bits.
 constexpr float kShift = 7.f, kTop = 15.f, kTopPow = 32768.f;
-// Registers of the roles: softmax, conversion, the others (5 x 96 a thread; 8 to 44
+// Registers of the roles: softmax, conversion, the others (5 x 96 a thread; 8 to 52
 // bytes a thread are spilled).
 constexpr int kRegsLaunch = 96;
 constexpr int kRegsSoftmax = 136, kRegsConvert = 72, kRegsOther = 64;
@@ -678,8 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
       const int head_bytes = kFour ? B * fp4_row_bytes(D) : D;
       const int row_bytes = kFour ? D / 2 : a.H * D;
       // Tags of up to kBatch stages of a part together, a lane each, and a table
-      // entry a lane (in kRounds rounds), which is loaded a batch ahead: value v is
-      // piece v % nblk of stage v / nblk
+      // entry a lane (in kRounds rounds), which is loaded ahead of the wait for the
+      // tags' places: value v is piece v % nblk of stage v / nblk
       constexpr int kRounds = kBatch * 16 / 32;
       const int lognblk = ilog2_device(nblk);
       int ents[kRounds];
@@ -874,8 +884,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_quant_kernel(const Args a
     }
     // Fetching a stage: its tag is looked at, on the chance that it is written, before
     // the conversion of another, whose time hides the look; the copies are issued
-    // behind it.  The tag is read behind a branch on the test: loads that only stand
-    // behind it in the program were seen to return what was there before.
+    // behind it.  The tag is read behind a branch on the test.  A form that read it beside
+    // the test, in program order behind it, and used it where the test had passed got, in
+    // one of some 10^4 calls, what the place had held before; neither the program's order
+    // nor the memory model explains that, and the cause is not known.
     long long at[kRows], sc_at = -1;
     int next_rs = 0, next_ts = 0, next_tg = 0;    // of the stage to be fetched next
     int next_flags = 0;
@@ -1528,7 +1540,8 @@ static_assert(2 * kMaxGrid * sizeof(uint32_t) <= kFewCounters &&
                   kFewBlocks * kMaxGrid * sizeof(uint32_t) <= PA_PREFILL_QUANT_COUNTERS - kFewCounters,
               "a block's counters");
 
-// Average rows a sequence up to which a batch is split between the two kernels.
+// Average rows a sequence up to which a batch is split between the two kernels (the
+// lengths themselves are on the device).
 constexpr int kFewAverage = 192;
 
 // The kernels' opt-in to their shared memory, once a device.
@@ -1624,10 +1637,14 @@ int prefill_quant(const void* q, const void* k_cache, const void* v_cache,
   a.v_scale = v_scale;
   a.start = kStart[q_dtype == PA_BF16 ? 1 : 0];
   // Sequences of few rows have a kernel of their own.  If even all of total_q in one
-  // would be one, it is the only one; where the average of the sequences is not far
-  // beyond, both run (their lengths are on the device); else there are hardly any.  48
-  // single tokens among 64 sequences, 144 rows on average: 143 us, some 170 with the other
-  // kernel alone; 7 chunks of 247 rows on average: 82 us with both, 77 with that one.
+  // would be one, it is the only one; both run where the average of the sequences is not
+  // far beyond.  An average cannot tell who they are: a few long chunks hide single
+  // tokens, and chunks that are all of some 30 rows pay for a launch that finds nothing.
+  // Us with the kernel of 128-row tiles alone / with both: 64 single tokens over 2 to 8 K
+  // of 4 bits beside a chunk of 512 425 / 241 (both run); 63 beside a chunk of 2,048 288 /
+  // 265, 64 beside one of 8,192 3,242 / 3,130, 64 beside four of 2,048 730 / 676 (tiles
+  // alone); 32 verified proposals of 4 tokens over 2 to 4 K 101 / 111 (both); 16 chunks of
+  // 512 550 / 568, one of 64 tokens 14.9 / 17.4 (tiles alone).
   const long long rows = (long long)total_q * a.G;
   a.few = rows <= kFewRows ? kFewOnly
                            : (rows <= (long long)kFewAverage * num_seqs ? kFewBoth : kFewNone);
